@@ -387,6 +387,141 @@ rkv_status rkv_dense_decode_noalloc(const void* q, const void* k, const void* v,
                                     const int32_t* len, int n, int n_kv, int gqa, int head_dim,
                                     int max_len, float scale, void* out, void* stream);
 
+/* ------------------------------------------------------------------------------------------ */
+/* A cache held in 4 bits                                                                      */
+/* ------------------------------------------------------------------------------------------ */
+/* The other way to a smaller cache: every token stays, in 144 bytes per KV head instead of 512.
+ * A row of 128 values (K or V of one token) is stored as
+ *   codes  64 bytes: e2m1 numbers (sign, magnitudes 0 .5 1 1.5 2 3 4 6), dimension 2 j in the low
+ *          half of byte j, 2 j + 1 in the high half;
+ *   scales 8 bytes, one per 16 consecutive dimensions: an unsigned number of 5 exponent and 3
+ *          mantissa bits (byte b stands for the fp16 number whose bits are b << 7), b <= 226.
+ * A row's value is code * scale: at most 6 significant bits, exact in bf16 and in fp16.
+ * Quantisation of 16 values x: scale = max|x| / 6 rounded to the nearest such number (ties to
+ * even, at most 10240), code = the e2m1 number nearest to x / scale (ties to even, at most 6 in
+ * magnitude), with x's sign bit. NaN becomes +0; values beyond +-61440 are clipped to it first;
+ * a block whose largest magnitude is at most 3 * 2^-17 becomes zeros.
+ *
+ * Layouts: k_codes, v_codes [n][n_kv][cap][64], k_scales, v_scales [n][n_kv][cap][8] bytes; paged:
+ * pools [num_blocks][n_kv][block][64] and [..][8] with a block table as for the paged calls above,
+ * block at least 16. All 16-byte aligned. Rows at and past a unit's length are never read. */
+
+/* Quantise the new_len[u] new rows of every KV head of unit u behind its len[u] cached ones.
+ *   new_k, new_v [n][n_kv][max_new][128] bf16: rows 0 .. new_len[u]-1 are taken
+ *   new_len  [n] int32 (device) or NULL (max_new rows of every unit)
+ *   len      [n] int32: rows in the cache before the call
+ *   len_out  [n] int32: len[u] + new_len[u]; may be the same array as len. A unit with new_len[u]
+ *            outside [0, max_new], len[u] < 0 or len[u] + new_len[u] > cap sets
+ *            RKV_DEV_LEN_OVER_CAP and is left as it was (len_out[u] = len[u]).
+ *   k_values, v_values NULL or [n][n_kv][max_new][128] bf16: the values the rows now stand for
+ *            (for a prompt whose own attention is to see what the decode will see); rows past
+ *            new_len[u] are left as they were. Both or neither.
+ * Workspace rkv_kv4_append_workspace_bytes. */
+size_t rkv_kv4_append_workspace_bytes(int n);
+rkv_status rkv_kv4_append(const void* new_k, const void* new_v, const int32_t* new_len, int n,
+                          int n_kv, int head_dim, int max_new, void* k_codes, void* k_scales,
+                          void* v_codes, void* v_scales, int cap, const int32_t* len,
+                          int32_t* len_out, void* k_values, void* v_values, void* ws,
+                          size_t ws_bytes, void* stream);
+rkv_status rkv_kv4_append_paged(const void* new_k, const void* new_v, const int32_t* new_len,
+                                int n, int n_kv, int head_dim, int max_new, void* k_codes,
+                                void* k_scales, void* v_codes, void* v_scales, int num_blocks,
+                                int block, const int32_t* block_table, int max_blocks,
+                                const int32_t* len, int32_t* len_out, void* k_values,
+                                void* v_values, void* ws, size_t ws_bytes, void* stream);
+
+/* One decode step over the 4-bit cache: out[u][h] = softmax(scale * q[u][h] . K[u][g]^T) V[u][g]
+ * over the unit's tokens (g = h / gqa), in one pass over the cache. If new_k / new_v are given, the
+ * step's token is first quantised into row len[u] (as rkv_kv4_append; the attention sees its
+ * quantised row) and len_out[u] = len[u] + 1; a unit that is full sets RKV_DEV_LEN_OVER_CAP,
+ * appends nothing and attends to its cap tokens. A unit without tokens gets zeros.
+ *   q, out [n][n_kv*gqa][128] bf16; gqa 1, 2, 4 or 8
+ *   new_k, new_v NULL or [n][n_kv][128] bf16; len_out [n] int32 (may be len), NULL without them
+ *   weights NULL or [n][n_kv][cap] fp32 (paged: cap = max_blocks * block): the softmax weight of
+ *           every token, summed over the group's query heads, is added to its entry (rows at and
+ *           past the length are left as they are, so entries of rows to come should hold zero)
+ * Workspace rkv_kv4_decode_workspace_bytes (cap as above; with_weights: whether weights are asked
+ * for, which takes 4 * gqa bytes per cached row). Results do not depend on what the workspace
+ * holds, status word apart. */
+size_t rkv_kv4_decode_workspace_bytes(int n, int n_kv, int gqa, int cap, int with_weights);
+rkv_status rkv_kv4_decode(const void* q, const void* new_k, const void* new_v, void* k_codes,
+                          void* k_scales, void* v_codes, void* v_scales, const int32_t* len,
+                          int32_t* len_out, int n, int n_kv, int gqa, int head_dim, int cap,
+                          float scale, void* out, float* weights, void* ws, size_t ws_bytes,
+                          void* stream);
+rkv_status rkv_kv4_decode_paged(const void* q, const void* new_k, const void* new_v,
+                                void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                                const int32_t* block_table, const int32_t* len, int32_t* len_out,
+                                int n, int n_kv, int gqa, int head_dim, int num_blocks, int block,
+                                int max_blocks, float scale, void* out, float* weights, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Eviction by accumulated attention weight                                                    */
+/* ------------------------------------------------------------------------------------------ */
+/* SnapKV++ evicts once, by what the last window of the prompt attends to. These calls evict again
+ * and again while a sequence grows, by what everything so far has attended to: the prompt call and
+ * the decode calls add each token's softmax weight (summed over the query heads of its KV group)
+ * to an array, and the eviction keeps the tokens with the largest sums besides the newest ones.
+ * A unit's entries start at zero.
+ *
+ * rkv_dense_decode with the weights: adds sum over the group's heads h of
+ * softmax(scale * q[u][h] . K[u][g]^T)[j] to weights[u][g][j], j < len[u].
+ *   q, k, v, len, out as rkv_dense_decode (0 <= len[u]: a unit without tokens gets zeros; a longer
+ *   one than max_len sets RKV_DEV_LEN_OVER_CAP and counts as max_len)
+ *   weights [n][n_kv][max_len] fp32, rows past len[u] left as they are */
+size_t rkv_dense_decode_weights_workspace_bytes(int n, int n_kv, int gqa, int max_len);
+rkv_status rkv_dense_decode_weights(const void* q, const void* k, const void* v,
+                                    const int32_t* len, int n, int n_kv, int gqa, int head_dim,
+                                    int max_len, float scale, void* out, float* weights, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* The weights of a prompt, or of a chunk of one behind cached tokens: query i < q_len[u] of every
+ * head stands at position len[u] - q_len[u] + i and sees the keys up to its own; the softmax weight
+ * that key j gets from all of them is added to weights[u][g][j]. (rkv_snapkv_scores without the
+ * window's limits: any number of queries, and every key gets its weight.)
+ *   q       [n][n_kv*gqa][max_q][128] bf16; rows q_len[u] and up are not used
+ *   q_len   [n] int32, 0 <= q_len[u] <= min(max_q, len[u]) (else RKV_DEV_BAD_WINDOW, unit skipped)
+ *   k       [n][n_kv][max_len][128] bf16, the chunk's own keys included; rows len[u] and up unused
+ *   len     [n] int32, at most max_len (else RKV_DEV_LEN_OVER_CAP, unit skipped)
+ *   gqa     1 .. 64
+ *   weights [n][n_kv][max_len] fp32 */
+size_t rkv_prompt_weights_workspace_bytes(int n, int n_kv, int gqa, int max_q, int max_len);
+rkv_status rkv_prompt_weights(const void* q, const int32_t* q_len, const void* k,
+                              const int32_t* len, int n, int n_kv, int gqa, int head_dim,
+                              int max_q, int max_len, float scale, float* weights, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Shrink every unit of more than `keep` rows to `keep`, per KV head: the tokens of the last
+ * `recent` positions stay, and of the others those with the largest weights (ties -> lower row;
+ * NaN counts as largest). Kept rows below `keep` do not move; the i-th free row below `keep`
+ * takes the i-th kept row at or past `keep`, so a step that evicts few rows moves few, and rows
+ * are in no particular order of position (attention does not depend on it; page summaries have
+ * to be rebuilt). A unit of at most `keep` rows is left as it is.
+ *   k, v     [n][n_kv][cap][128] bf16, or the 4-bit arrays: moved in place
+ *   len      [n] int32; len_out [n] int32: min(len[u], keep); may be the same array
+ *   weights  [n][n_kv][cap] fp32, pos [n][n_kv][cap] int32: a row's position in its sequence, or -1
+ *            for a row appended since the last eviction (its position is then
+ *            seen[u] - (len[u] - row)); all -1 at first
+ *   seen     [n] int32: tokens the sequence has had so far (the position of the next one)
+ *   weights_out, pos_out: the arrays after the move (may be the same arrays): rows below
+ *            len_out[u] belong to the rows now there (of an evicted unit, every position is
+ *            known), rows from len_out[u] to len[u] - 1 are reset (0 and -1), later rows are left
+ *            as they were
+ *   src_rows NULL or [n][n_kv][keep] int32: the row each row came from, -1 past len_out[u]
+ *   0 <= recent <= keep, 1 <= keep. len[u] outside [0, cap]: RKV_DEV_LEN_OVER_CAP, unit left as it
+ *   was (len_out[u] = len[u]; weights_out, pos_out and src_rows not written). */
+size_t rkv_evict_workspace_bytes(int n, int n_kv, int cap, int keep);
+rkv_status rkv_evict(void* k, void* v, const int32_t* len, int32_t* len_out, const float* weights,
+                     float* weights_out, const int32_t* pos, int32_t* pos_out,
+                     const int32_t* seen, int n, int n_kv, int head_dim, int cap, int keep,
+                     int recent, int32_t* src_rows, void* ws, size_t ws_bytes, void* stream);
+rkv_status rkv_evict_kv4(void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                         const int32_t* len, int32_t* len_out, const float* weights,
+                         float* weights_out, const int32_t* pos, int32_t* pos_out,
+                         const int32_t* seen, int n, int n_kv, int head_dim, int cap, int keep,
+                         int recent, int32_t* src_rows, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "librkv.so")
-SOURCES = ["api.cu", "decode.cu", "snapkv.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "decode.cu", "snapkv.cu", "noalloc.cu", "api_cache.cu", "cache_decode.cu",
+           "prompt.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{os.path.join(ROOT, 'include')}"]

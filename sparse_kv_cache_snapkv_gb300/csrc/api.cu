@@ -9,6 +9,7 @@
 
 #include "../../include/rkv.h"
 #include "../../include/rkv_testing.h"
+#include "api_util.h"
 #include "rkv_internal.h"
 
 using namespace rkv;
@@ -65,13 +66,6 @@ int device_sm_count() {
 
 namespace {
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-inline uint32_t* status_ptr(void* ws) { return reinterpret_cast<uint32_t*>(ws); }
-inline rkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RKV_OK : RKV_ERR_CUDA; }
-inline bool gqa_ok(int g) { return g == 1 || g == 2 || g == 4 || g == 8; }
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxAvgKernel = (1 << 20) - 1;  // keeps a fixed-point window sum below 2^60
 
 }  // namespace
@@ -495,11 +489,6 @@ rkv_status rkv_hybrid_decode_mt(const void* q, const void* new_k, const void* ne
 }
 
 // ------------------------------------------------------------------------------- paged
-static bool paged_ok(const void* table, int num_blocks, int block, int max_blocks) {
-  return table && num_blocks > 0 && max_blocks > 0 && pow2(block) && block <= 65536 &&
-         (long long)max_blocks * block <= (1ll << 30);
-}
-
 rkv_status rkv_snapkv_compress_paged(const void* k, const void* v, const int32_t* seq_lens,
                                      const void* q_win, int n, int n_kv, int gqa, int head_dim,
                                      int max_len, int window, int kernel_size, int keep,

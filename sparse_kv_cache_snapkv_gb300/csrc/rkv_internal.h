@@ -191,4 +191,95 @@ void snapkv_plan(int n, int n_kv, int gqa, int max_len, int window, int* nsplit,
 size_t snapkv_scratch_bytes(int n, int n_kv, int gqa, int max_len, int window);
 cudaError_t launch_snapkv(const SnapArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------- 4-bit cache
+constexpr int kCodeBytes = kHeadDim / 2;     // e2m1 codes of one row
+constexpr int kScaleGroup = 16;              // dimensions that share a scale byte
+constexpr int kRowScales = kHeadDim / kScaleGroup;
+constexpr int kMinKv4Block = 16;             // smallest block of a paged 4-bit cache: one tile
+
+struct Kv4AppendArgs {
+  const bf16* new_k;
+  const bf16* new_v;
+  const int32_t* new_len;  // nullptr: max_new for every unit
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const int32_t* len;
+  int32_t* len_out;
+  bf16* k_values;  // nullptr: not asked for
+  bf16* v_values;
+  PagedMap pm;  // table == nullptr: not paged
+  int n, n_kv, max_new, cap;
+  uint32_t* status;
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
+
+// Decode over a whole cache in bf16 (k, v) or 4 bits (codes and scales), with the optional
+// append (4 bits only) and the optional accumulation of the tokens' weights.
+struct CacheDecodeArgs {
+  const bf16* q;
+  const void* k;  // bf16 rows, or codes
+  const void* v;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* len;
+  int32_t* len_out;  // nullptr: no append
+  const bf16* new_k;
+  const bf16* new_v;
+  PagedMap pm;
+  int n, n_kv, gqa, cap;
+  int nsplit, tokens_per_split;
+  float scale_log2;
+  bf16* out;
+  float* weights;  // nullptr: not asked for
+  float* logits;   // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
+  float* part_ml;  // workspace [n*n_kv][nsplit][gqa][2]
+  float* part_o;   // workspace [n*n_kv][nsplit][gqa][128]
+  uint32_t* status;
+  bool kv4;
+};
+void cache_decode_plan(int n, int n_kv, int cap, int* nsplit, int* tokens_per_split);
+size_t cache_decode_scratch_bytes(int n, int n_kv, int gqa, int cap, bool with_weights);
+// places logits and the partials in the scratch area (after the status word)
+void cache_decode_carve(CacheDecodeArgs* a, void* scratch);
+cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------- prompt weights
+constexpr int kMaxPromptGqa = 64;  // query heads of a KV group
+
+struct PromptArgs {
+  const bf16* q;
+  const int32_t* q_len;
+  const bf16* k;
+  const int32_t* len;
+  int n, n_kv, gqa, max_q, max_len;
+  float scale_log2;
+  float* weights;
+  void* scratch;  // workspace after the status word
+  uint32_t* status;
+};
+size_t prompt_scratch_bytes(int n, int n_kv, int gqa, int max_q, int max_len);
+cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------- eviction
+struct EvictArgs {
+  // the cache's arrays and the bytes of a row in each (multiples of 8; unused ones are nullptr)
+  uint8_t* rows[4];
+  int row_bytes[4];
+  const int32_t* len;
+  int32_t* len_out;
+  const float* weights;
+  float* weights_out;
+  const int32_t* pos;
+  int32_t* pos_out;
+  const int32_t* seen;
+  int n, n_kv, cap, keep, recent;
+  int32_t* src_rows;  // nullptr: not asked for
+  void* scratch;      // workspace after the status word
+  uint32_t* status;
+};
+size_t evict_scratch_bytes(int n, int n_kv, int cap, int keep);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
 }  // namespace rkv

@@ -34,6 +34,11 @@ SYMBOLS = [
     "rkv_snapkv_compress_paged", "rkv_build_page_summaries_paged", "rkv_hybrid_decode_paged",
     "rkv_snapkv_compress_summarized", "rkv_snapkv_compress_avg_pool", "rkv_snapkv_select",
     "rkv_snapkv_scores", "rkv_testing_scores_wait_timeout", "rkv_testing_decode_layout",
+    "rkv_kv4_append_workspace_bytes", "rkv_kv4_append", "rkv_kv4_append_paged",
+    "rkv_kv4_decode_workspace_bytes", "rkv_kv4_decode", "rkv_kv4_decode_paged",
+    "rkv_dense_decode_weights_workspace_bytes", "rkv_dense_decode_weights",
+    "rkv_prompt_weights_workspace_bytes", "rkv_prompt_weights", "rkv_evict_workspace_bytes",
+    "rkv_evict", "rkv_evict_kv4",
 ]
 
 
@@ -111,6 +116,27 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "rkv_hybrid_decode_mt": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                   i32, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp],
                                  i32),
+        "rkv_kv4_append_workspace_bytes": ([i32], sz),
+        "rkv_kv4_append": ([vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp,
+                            vp, sz, vp], i32),
+        "rkv_kv4_append_paged": ([vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, vp,
+                                  i32, vp, vp, vp, vp, vp, sz, vp], i32),
+        "rkv_kv4_decode_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "rkv_kv4_decode": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp,
+                            vp, vp, sz, vp], i32),
+        "rkv_kv4_decode_paged": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                  i32, i32, f32, vp, vp, vp, sz, vp], i32),
+        "rkv_dense_decode_weights_workspace_bytes": ([i32, i32, i32, i32], sz),
+        "rkv_dense_decode_weights": ([vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp,
+                                      sz, vp], i32),
+        "rkv_prompt_weights_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "rkv_prompt_weights": ([vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz,
+                                vp], i32),
+        "rkv_evict_workspace_bytes": ([i32, i32, i32, i32], sz),
+        "rkv_evict": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp,
+                       sz, vp], i32),
+        "rkv_evict_kv4": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                           i32, vp, vp, sz, vp], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -512,3 +538,272 @@ def rkv_dense_decode_noalloc(q, k, v, length, scale: float, out, stream=None):
     code = load().rkv_dense_decode_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(length), n, n_kv, gqa,
                                            d, max_len, float(scale), _ptr(out), _stream(stream))
     _check("rkv_dense_decode_noalloc", code)
+
+
+# ------------------------------------------------------------------------------- 4-bit cache
+CODE_BYTES = HEAD_DIM // 2
+ROW_SCALES = HEAD_DIM // 16
+
+
+def _shaped(t: torch.Tensor, name: str, dtype, shape):
+    """A tensor of the call: its type and its shape (None: any size)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
+    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{tuple('any' if w is None else w for w in shape)}")
+
+
+class _Call:
+    """One device for every tensor of a call, and the stream that it runs on: the one given, or
+    the current stream of that device. Inside the block that device is current, and a workspace
+    that the call makes belongs to that stream."""
+
+    def __init__(self, stream, *tensors):
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError("librkv takes device tensors only, all on one device")
+        self.device = devices.pop()
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
+        self.given = stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.given is not None or torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.stream(self.given or torch.cuda.current_stream(self.device))
+            self.guard.__enter__()
+        self.stream = ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+        return self
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+    def ws(self, ws, nbytes):
+        if ws is None:
+            return workspace(nbytes, self.device)
+        if ws.device != self.device:
+            raise ValueError("the workspace is on another device")
+        return ws
+
+
+def kv4_cache(n: int, n_kv: int, cap: int, device="cuda"):
+    """Zeroed arrays of a 4-bit cache: (k_codes, k_scales, v_codes, v_scales)."""
+    z = lambda w: torch.zeros(n, n_kv, cap, w, dtype=torch.uint8, device=device)  # noqa: E731
+    return z(CODE_BYTES), z(ROW_SCALES), z(CODE_BYTES), z(ROW_SCALES)
+
+
+def _kv4(k_codes, k_scales, v_codes, v_scales):
+    lead = tuple(k_codes.shape[:3])
+    for t, name, w in ((k_codes, "k_codes", CODE_BYTES), (k_scales, "k_scales", ROW_SCALES),
+                       (v_codes, "v_codes", CODE_BYTES), (v_scales, "v_scales", ROW_SCALES)):
+        _shaped(t, name, torch.uint8, lead + (w,))
+    return lead
+
+
+def rkv_kv4_append_workspace_bytes(n: int) -> int:
+    return int(load().rkv_kv4_append_workspace_bytes(n))
+
+
+def _kv4_append(fn, new_k, new_v, cache, lead, sizes, tables, length, length_out, new_len,
+                k_values, v_values, ws, stream):
+    n, n_kv, max_new, d = new_k.shape
+    _shaped(new_k, "new_k", torch.bfloat16, (n, lead[1], None, None))
+    _shaped(new_v, "new_v", torch.bfloat16, new_k.shape)
+    for t, name in ((length, "len"), (length_out, "len_out"), (new_len, "new_len")):
+        if t is not None:
+            _shaped(t, name, torch.int32, (n,))
+    for t, name in ((k_values, "k_values"), (v_values, "v_values")):
+        if t is not None:
+            _shaped(t, name, torch.bfloat16, new_k.shape)
+    with _Call(stream, new_k, new_v, *cache, *tables, length, length_out, new_len, k_values,
+               v_values) as call:
+        ws = call.ws(ws, rkv_kv4_append_workspace_bytes(n))
+        code = getattr(load(), fn)(
+            _ptr(new_k), _ptr(new_v), _ptr(new_len), n, n_kv, d, max_new,
+            *[_ptr(t) for t in cache], *sizes, _ptr(length), _ptr(length_out), _ptr(k_values),
+            _ptr(v_values), _ptr(ws), ws.numel(), call.stream)
+    _check(fn, code)
+    return ws
+
+
+def rkv_kv4_append(new_k, new_v, k_codes, k_scales, v_codes, v_scales, length, length_out,
+                   new_len=None, k_values=None, v_values=None, ws=None, stream=None):
+    """Quantise new rows ([n][n_kv][max_new][128] bf16) behind each unit's length[u] rows; see
+    include/rkv.h. length_out may be length."""
+    lead = _kv4(k_codes, k_scales, v_codes, v_scales)
+    if lead[0] != new_k.shape[0]:
+        raise ValueError(f"{new_k.shape[0]} units of new rows for a cache of {lead[0]}")
+    return _kv4_append("rkv_kv4_append", new_k, new_v, (k_codes, k_scales, v_codes, v_scales),
+                       lead, (lead[2],), (), length, length_out, new_len, k_values, v_values, ws,
+                       stream)
+
+
+def rkv_kv4_append_paged(new_k, new_v, k_codes, k_scales, v_codes, v_scales, block_table, length,
+                         length_out, new_len=None, k_values=None, v_values=None, ws=None,
+                         stream=None):
+    """rkv_kv4_append into pools [num_blocks][n_kv][block][..] through block_table [n][max_blocks]."""
+    lead = _kv4(k_codes, k_scales, v_codes, v_scales)
+    _shaped(block_table, "block_table", torch.int32, (new_k.shape[0], None))
+    return _kv4_append("rkv_kv4_append_paged", new_k, new_v,
+                       (k_codes, k_scales, v_codes, v_scales), lead,
+                       (lead[0], lead[2], _ptr(block_table), block_table.shape[1]),
+                       (block_table,), length, length_out, new_len, k_values, v_values, ws,
+                       stream)
+
+
+def rkv_kv4_decode_workspace_bytes(n: int, n_kv: int, gqa: int, cap: int,
+                                   with_weights: bool) -> int:
+    return int(load().rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, int(with_weights)))
+
+
+def _decode_args(q, out, length, n, n_kv, cap, weights):
+    _shaped(q, "q", torch.bfloat16, (n, None, None))
+    _shaped(out, "out", torch.bfloat16, q.shape)
+    _shaped(length, "len", torch.int32, (n,))
+    if weights is not None:
+        _shaped(weights, "weights", torch.float32, (n, n_kv, cap))
+    return _group(q.shape[1], n_kv), q.shape[2]
+
+
+def _appended(new_k, new_v, length_out, n, n_kv, d):
+    for t, name in ((new_k, "new_k"), (new_v, "new_v")):
+        if t is not None:
+            _shaped(t, name, torch.bfloat16, (n, n_kv, d))
+    if length_out is not None:
+        _shaped(length_out, "len_out", torch.int32, (n,))
+
+
+def rkv_kv4_decode(q, k_codes, k_scales, v_codes, v_scales, length, scale: float, out, new_k=None,
+                   new_v=None, length_out=None, weights=None, ws=None, stream=None):
+    """One decode step over the 4-bit cache, optionally appending new_k / new_v first and adding
+    each token's softmax weight to weights; see include/rkv.h. length_out may be length."""
+    n, n_kv, cap = _kv4(k_codes, k_scales, v_codes, v_scales)
+    gqa, d = _decode_args(q, out, length, n, n_kv, cap, weights)
+    _appended(new_k, new_v, length_out, n, n_kv, d)
+    with _Call(stream, q, out, length, k_codes, k_scales, v_codes, v_scales, new_k, new_v,
+               length_out, weights) as call:
+        ws = call.ws(ws, rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None))
+        code = load().rkv_kv4_decode(
+            _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
+            _ptr(v_scales), _ptr(length), _ptr(length_out), n, n_kv, gqa, d, cap, float(scale),
+            _ptr(out), _ptr(weights), _ptr(ws), ws.numel(), call.stream)
+    _check("rkv_kv4_decode", code)
+    return ws
+
+
+def rkv_kv4_decode_paged(q, k_codes, k_scales, v_codes, v_scales, block_table, length,
+                         scale: float, out, new_k=None, new_v=None, length_out=None, weights=None,
+                         ws=None, stream=None):
+    """rkv_kv4_decode over pools [num_blocks][n_kv][block][..] through block_table
+    [n][max_blocks]; weights [n][n_kv][max_blocks * block]."""
+    num_blocks, n_kv, block = _kv4(k_codes, k_scales, v_codes, v_scales)
+    n = q.shape[0]
+    _shaped(block_table, "block_table", torch.int32, (n, None))
+    max_blocks = block_table.shape[1]
+    cap = max_blocks * block
+    gqa, d = _decode_args(q, out, length, n, n_kv, cap, weights)
+    _appended(new_k, new_v, length_out, n, n_kv, d)
+    with _Call(stream, q, out, length, k_codes, k_scales, v_codes, v_scales, block_table, new_k,
+               new_v, length_out, weights) as call:
+        ws = call.ws(ws, rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None))
+        code = load().rkv_kv4_decode_paged(
+            _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
+            _ptr(v_scales), _ptr(block_table), _ptr(length), _ptr(length_out), n, n_kv, gqa, d,
+            num_blocks, block, max_blocks, float(scale), _ptr(out), _ptr(weights), _ptr(ws),
+            ws.numel(), call.stream)
+    _check("rkv_kv4_decode_paged", code)
+    return ws
+
+
+# ------------------------------------------------------------------------------- weights, eviction
+def rkv_dense_decode_weights_workspace_bytes(n: int, n_kv: int, gqa: int, max_len: int) -> int:
+    return int(load().rkv_dense_decode_weights_workspace_bytes(n, n_kv, gqa, max_len))
+
+
+def rkv_dense_decode_weights(q, k, v, length, scale: float, out, weights, ws=None, stream=None):
+    """Full-KV decode attention that adds each token's softmax weight (summed over the query heads
+    of its group) to weights [n][n_kv][max_len] fp32."""
+    _shaped(k, "k", torch.bfloat16, (None, None, None, None))
+    _shaped(v, "v", torch.bfloat16, k.shape)
+    n, n_kv, max_len, _ = k.shape
+    gqa, d = _decode_args(q, out, length, n, n_kv, max_len, weights)
+    _shaped(k, "k", torch.bfloat16, (n, n_kv, max_len, d))
+    with _Call(stream, q, k, v, length, out, weights) as call:
+        ws = call.ws(ws, rkv_dense_decode_weights_workspace_bytes(n, n_kv, gqa, max_len))
+        code = load().rkv_dense_decode_weights(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(length), n, n_kv, gqa, d, max_len, float(scale),
+            _ptr(out), _ptr(weights), _ptr(ws), ws.numel(), call.stream)
+    _check("rkv_dense_decode_weights", code)
+    return ws
+
+
+def rkv_prompt_weights_workspace_bytes(n: int, n_kv: int, gqa: int, max_q: int,
+                                       max_len: int) -> int:
+    return int(load().rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len))
+
+
+def rkv_prompt_weights(q, q_len, k, length, scale: float, weights, ws=None, stream=None):
+    """Adds the softmax weight that every key gets from the last q_len[u] positions' queries
+    (q [n][Hq][max_q][128]) to weights [n][n_kv][max_len] fp32; see include/rkv.h."""
+    _shaped(k, "k", torch.bfloat16, (None, None, None, None))
+    n, n_kv, max_len, d = k.shape
+    _shaped(q, "q", torch.bfloat16, (n, None, None, d))
+    _shaped(q_len, "q_len", torch.int32, (n,))
+    _shaped(length, "len", torch.int32, (n,))
+    _shaped(weights, "weights", torch.float32, (n, n_kv, max_len))
+    gqa, max_q = _group(q.shape[1], n_kv), q.shape[2]
+    with _Call(stream, q, q_len, k, length, weights) as call:
+        ws = call.ws(ws, rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len))
+        code = load().rkv_prompt_weights(
+            _ptr(q), _ptr(q_len), _ptr(k), _ptr(length), n, n_kv, gqa, d, max_q, max_len,
+            float(scale), _ptr(weights), _ptr(ws), ws.numel(), call.stream)
+    _check("rkv_prompt_weights", code)
+    return ws
+
+
+def rkv_evict_workspace_bytes(n: int, n_kv: int, cap: int, keep: int) -> int:
+    return int(load().rkv_evict_workspace_bytes(n, n_kv, cap, keep))
+
+
+def _evict(fn, cache, n, n_kv, cap, d, length, weights, pos, seen, keep, recent, length_out,
+           weights_out, pos_out, src_rows, ws, stream):
+    for t, name in ((length, "len"), (length_out, "len_out"), (seen, "seen")):
+        _shaped(t, name, torch.int32, (n,))
+    for t, name, dt in ((weights, "weights", torch.float32), (pos, "pos", torch.int32),
+                        (weights_out, "weights_out", torch.float32),
+                        (pos_out, "pos_out", torch.int32)):
+        _shaped(t, name, dt, (n, n_kv, cap))
+    if src_rows is not None:
+        _shaped(src_rows, "src_rows", torch.int32, (n, n_kv, keep))
+    with _Call(stream, *cache, length, weights, pos, seen, length_out, weights_out, pos_out,
+               src_rows) as call:
+        ws = call.ws(ws, rkv_evict_workspace_bytes(n, n_kv, cap, keep))
+        code = getattr(load(), fn)(
+            *[_ptr(t) for t in cache], _ptr(length), _ptr(length_out), _ptr(weights),
+            _ptr(weights_out), _ptr(pos), _ptr(pos_out), _ptr(seen), n, n_kv, d, cap, int(keep),
+            int(recent), _ptr(src_rows), _ptr(ws), ws.numel(), call.stream)
+    _check(fn, code)
+    return ws
+
+
+def rkv_evict(k, v, length, weights, pos, seen, keep: int, recent: int, length_out, weights_out,
+              pos_out, src_rows=None, ws=None, stream=None):
+    """Keep the `keep` rows of largest weight (the last `recent` positions always) of every
+    (unit, KV head), in place; the *_out arrays may be the inputs. See include/rkv.h."""
+    _shaped(k, "k", torch.bfloat16, (None, None, None, None))
+    _shaped(v, "v", torch.bfloat16, k.shape)
+    n, n_kv, cap, d = k.shape
+    return _evict("rkv_evict", (k, v), n, n_kv, cap, d, length, weights, pos, seen, keep, recent,
+                  length_out, weights_out, pos_out, src_rows, ws, stream)
+
+
+def rkv_evict_kv4(k_codes, k_scales, v_codes, v_scales, length, weights, pos, seen, keep: int,
+                  recent: int, length_out, weights_out, pos_out, src_rows=None, ws=None,
+                  stream=None):
+    """rkv_evict of a 4-bit cache."""
+    n, n_kv, cap = _kv4(k_codes, k_scales, v_codes, v_scales)
+    return _evict("rkv_evict_kv4", (k_codes, k_scales, v_codes, v_scales), n, n_kv, cap, HEAD_DIM,
+                  length, weights, pos, seen, keep, recent, length_out, weights_out, pos_out,
+                  src_rows, ws, stream)
