@@ -543,49 +543,61 @@ def rkv_dense_decode_noalloc(q, k, v, length, scale: float, out, stream=None):
 # ------------------------------------------------------------------------------- 4-bit cache
 CODE_BYTES = HEAD_DIM // 2
 ROW_SCALES = HEAD_DIM // 16
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _shaped(t: torch.Tensor, name: str, dtype, shape):
-    """A tensor of the call: its type and its shape (None: any size)."""
-    if t.dtype != dtype:
+def _refuse(t, name, dtype, shape, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"{tuple('any' if w is None else w for w in shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: librkv takes device tensors only")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, others on cuda:{dev}")
+    raise ValueError(f"{name}: librkv takes contiguous tensors only")
 
 
-class _Call:
-    """One device for every tensor of a call, and the stream that it runs on: the one given, or
-    the current stream of that device. Inside the block that device is current, and a workspace
-    that the call makes belongs to that stream."""
+def _at(t, name, dtype, shape, dev):
+    """Address of a tensor of the call, after its type, shape, layout and device (a call's own
+    cost is what a small step waits for, so this is one chain of cheap tests)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == dev):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
 
-    def __init__(self, stream, *tensors):
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1 or next(iter(devices)).type != "cuda":
-            raise ValueError("librkv takes device tensors only, all on one device")
-        self.device = devices.pop()
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
-        self.given = stream
-        self.guard = None
 
-    def __enter__(self):
-        if self.given is not None or torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.stream(self.given or torch.cuda.current_stream(self.device))
-            self.guard.__enter__()
-        self.stream = ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-        return self
+def _at_or_none(t, name, dtype, shape, dev):
+    return None if t is None else _at(t, name, dtype, shape, dev)
 
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
 
-    def ws(self, ws, nbytes):
-        if ws is None:
-            return workspace(nbytes, self.device)
-        if ws.device != self.device:
-            raise ValueError("the workspace is on another device")
-        return ws
+def _dims(t, name, rank):
+    if not isinstance(t, torch.Tensor) or t.dim() != rank:
+        raise ValueError(f"{name} must be a tensor of {rank} dimensions")
+    return t.shape
+
+
+def _call(fn, args, ws, nbytes, dev, stream):
+    """Run entry point `fn` on the device of its tensors and the stream given (or that device's
+    current one). nbytes(): the workspace to make where none is given; it is made on that stream."""
+    if dev < 0:
+        raise ValueError("librkv takes device tensors only")
+    if stream is not None or torch.cuda.current_device() != dev:
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+        with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
+            return _call(fn, args, ws, nbytes, dev, None)
+    if ws is None:
+        ws = workspace(nbytes(), torch.device("cuda", dev))
+    elif ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous bytes on the tensors' device")
+    code = getattr(load(), fn)(*args, ws.data_ptr(), ws.numel(),
+                               torch._C._cuda_getCurrentRawStream(dev))
+    if code != RKV_OK:
+        raise RkvError(fn, code)
+    return ws
 
 
 def kv4_cache(n: int, n_kv: int, cap: int, device="cuda"):
@@ -594,63 +606,58 @@ def kv4_cache(n: int, n_kv: int, cap: int, device="cuda"):
     return z(CODE_BYTES), z(ROW_SCALES), z(CODE_BYTES), z(ROW_SCALES)
 
 
-def _kv4(k_codes, k_scales, v_codes, v_scales):
-    lead = tuple(k_codes.shape[:3])
-    for t, name, w in ((k_codes, "k_codes", CODE_BYTES), (k_scales, "k_scales", ROW_SCALES),
-                       (v_codes, "v_codes", CODE_BYTES), (v_scales, "v_scales", ROW_SCALES)):
-        _shaped(t, name, torch.uint8, lead + (w,))
-    return lead
+def _kv4(k_codes, k_scales, v_codes, v_scales, dev):
+    """Leading dimensions and addresses of a 4-bit cache."""
+    a, b, c, _ = _dims(k_codes, "k_codes", 4)
+    codes, scales = (a, b, c, CODE_BYTES), (a, b, c, ROW_SCALES)
+    return a, b, c, (_at(k_codes, "k_codes", _U8, codes, dev),
+                     _at(k_scales, "k_scales", _U8, scales, dev),
+                     _at(v_codes, "v_codes", _U8, codes, dev),
+                     _at(v_scales, "v_scales", _U8, scales, dev))
 
 
 def rkv_kv4_append_workspace_bytes(n: int) -> int:
     return int(load().rkv_kv4_append_workspace_bytes(n))
 
 
-def _kv4_append(fn, new_k, new_v, cache, lead, sizes, tables, length, length_out, new_len,
-                k_values, v_values, ws, stream):
-    n, n_kv, max_new, d = new_k.shape
-    _shaped(new_k, "new_k", torch.bfloat16, (n, lead[1], None, None))
-    _shaped(new_v, "new_v", torch.bfloat16, new_k.shape)
-    for t, name in ((length, "len"), (length_out, "len_out"), (new_len, "new_len")):
-        if t is not None:
-            _shaped(t, name, torch.int32, (n,))
-    for t, name in ((k_values, "k_values"), (v_values, "v_values")):
-        if t is not None:
-            _shaped(t, name, torch.bfloat16, new_k.shape)
-    with _Call(stream, new_k, new_v, *cache, *tables, length, length_out, new_len, k_values,
-               v_values) as call:
-        ws = call.ws(ws, rkv_kv4_append_workspace_bytes(n))
-        code = getattr(load(), fn)(
-            _ptr(new_k), _ptr(new_v), _ptr(new_len), n, n_kv, d, max_new,
-            *[_ptr(t) for t in cache], *sizes, _ptr(length), _ptr(length_out), _ptr(k_values),
-            _ptr(v_values), _ptr(ws), ws.numel(), call.stream)
-    _check(fn, code)
-    return ws
+def _kv4_append(fn, new_k, new_v, cache, table, length, length_out, new_len, k_values, v_values,
+                ws, stream):
+    n, n_kv, max_new, d = shape = _dims(new_k, "new_k", 4)
+    dev = new_k.get_device()
+    lead, heads, rows, ptrs = _kv4(*cache, dev)
+    if heads != n_kv:
+        raise ValueError(f"new_k has {n_kv} KV heads, the cache {heads}")
+    if table is None:
+        if lead != n:
+            raise ValueError(f"{n} units of new rows for a cache of {lead}")
+        size = (rows,)
+    else:
+        max_blocks = _dims(table, "block_table", 2)[1]
+        size = (lead, rows, _at(table, "block_table", _I32, (n, max_blocks), dev), max_blocks)
+    args = (_at(new_k, "new_k", _BF16, shape, dev), _at(new_v, "new_v", _BF16, shape, dev),
+            _at_or_none(new_len, "new_len", _I32, (n,), dev), n, n_kv, d, max_new, *ptrs, *size,
+            _at(length, "len", _I32, (n,), dev), _at(length_out, "len_out", _I32, (n,), dev),
+            _at_or_none(k_values, "k_values", _BF16, shape, dev),
+            _at_or_none(v_values, "v_values", _BF16, shape, dev))
+    return _call(fn, args, ws, lambda: rkv_kv4_append_workspace_bytes(n), dev, stream)
 
 
 def rkv_kv4_append(new_k, new_v, k_codes, k_scales, v_codes, v_scales, length, length_out,
                    new_len=None, k_values=None, v_values=None, ws=None, stream=None):
     """Quantise new rows ([n][n_kv][max_new][128] bf16) behind each unit's length[u] rows; see
     include/rkv.h. length_out may be length."""
-    lead = _kv4(k_codes, k_scales, v_codes, v_scales)
-    if lead[0] != new_k.shape[0]:
-        raise ValueError(f"{new_k.shape[0]} units of new rows for a cache of {lead[0]}")
     return _kv4_append("rkv_kv4_append", new_k, new_v, (k_codes, k_scales, v_codes, v_scales),
-                       lead, (lead[2],), (), length, length_out, new_len, k_values, v_values, ws,
-                       stream)
+                       None, length, length_out, new_len, k_values, v_values, ws, stream)
 
 
 def rkv_kv4_append_paged(new_k, new_v, k_codes, k_scales, v_codes, v_scales, block_table, length,
                          length_out, new_len=None, k_values=None, v_values=None, ws=None,
                          stream=None):
     """rkv_kv4_append into pools [num_blocks][n_kv][block][..] through block_table [n][max_blocks]."""
-    lead = _kv4(k_codes, k_scales, v_codes, v_scales)
-    _shaped(block_table, "block_table", torch.int32, (new_k.shape[0], None))
+    _dims(block_table, "block_table", 2)
     return _kv4_append("rkv_kv4_append_paged", new_k, new_v,
-                       (k_codes, k_scales, v_codes, v_scales), lead,
-                       (lead[0], lead[2], _ptr(block_table), block_table.shape[1]),
-                       (block_table,), length, length_out, new_len, k_values, v_values, ws,
-                       stream)
+                       (k_codes, k_scales, v_codes, v_scales), block_table, length, length_out,
+                       new_len, k_values, v_values, ws, stream)
 
 
 def rkv_kv4_decode_workspace_bytes(n: int, n_kv: int, gqa: int, cap: int,
@@ -658,39 +665,24 @@ def rkv_kv4_decode_workspace_bytes(n: int, n_kv: int, gqa: int, cap: int,
     return int(load().rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, int(with_weights)))
 
 
-def _decode_args(q, out, length, n, n_kv, cap, weights):
-    _shaped(q, "q", torch.bfloat16, (n, None, None))
-    _shaped(out, "out", torch.bfloat16, q.shape)
-    _shaped(length, "len", torch.int32, (n,))
-    if weights is not None:
-        _shaped(weights, "weights", torch.float32, (n, n_kv, cap))
-    return _group(q.shape[1], n_kv), q.shape[2]
-
-
-def _appended(new_k, new_v, length_out, n, n_kv, d):
-    for t, name in ((new_k, "new_k"), (new_v, "new_v")):
-        if t is not None:
-            _shaped(t, name, torch.bfloat16, (n, n_kv, d))
-    if length_out is not None:
-        _shaped(length_out, "len_out", torch.int32, (n,))
-
-
 def rkv_kv4_decode(q, k_codes, k_scales, v_codes, v_scales, length, scale: float, out, new_k=None,
                    new_v=None, length_out=None, weights=None, ws=None, stream=None):
     """One decode step over the 4-bit cache, optionally appending new_k / new_v first and adding
     each token's softmax weight to weights; see include/rkv.h. length_out may be length."""
-    n, n_kv, cap = _kv4(k_codes, k_scales, v_codes, v_scales)
-    gqa, d = _decode_args(q, out, length, n, n_kv, cap, weights)
-    _appended(new_k, new_v, length_out, n, n_kv, d)
-    with _Call(stream, q, out, length, k_codes, k_scales, v_codes, v_scales, new_k, new_v,
-               length_out, weights) as call:
-        ws = call.ws(ws, rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None))
-        code = load().rkv_kv4_decode(
-            _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
-            _ptr(v_scales), _ptr(length), _ptr(length_out), n, n_kv, gqa, d, cap, float(scale),
-            _ptr(out), _ptr(weights), _ptr(ws), ws.numel(), call.stream)
-    _check("rkv_kv4_decode", code)
-    return ws
+    shape = _dims(q, "q", 3)
+    dev = q.get_device()
+    n, n_kv, cap, ptrs = _kv4(k_codes, k_scales, v_codes, v_scales, dev)
+    gqa, d = _group(shape[1], n_kv), shape[2]
+    args = (_at(q, "q", _BF16, (n, shape[1], d), dev),
+            _at_or_none(new_k, "new_k", _BF16, (n, n_kv, d), dev),
+            _at_or_none(new_v, "new_v", _BF16, (n, n_kv, d), dev), *ptrs,
+            _at(length, "len", _I32, (n,), dev),
+            _at_or_none(length_out, "len_out", _I32, (n,), dev), n, n_kv, gqa, d, cap, scale,
+            _at(out, "out", _BF16, shape, dev),
+            _at_or_none(weights, "weights", _F32, (n, n_kv, cap), dev))
+    return _call("rkv_kv4_decode", args, ws,
+                 lambda: rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None),
+                 dev, stream)
 
 
 def rkv_kv4_decode_paged(q, k_codes, k_scales, v_codes, v_scales, block_table, length,
@@ -698,23 +690,22 @@ def rkv_kv4_decode_paged(q, k_codes, k_scales, v_codes, v_scales, block_table, l
                          ws=None, stream=None):
     """rkv_kv4_decode over pools [num_blocks][n_kv][block][..] through block_table
     [n][max_blocks]; weights [n][n_kv][max_blocks * block]."""
-    num_blocks, n_kv, block = _kv4(k_codes, k_scales, v_codes, v_scales)
-    n = q.shape[0]
-    _shaped(block_table, "block_table", torch.int32, (n, None))
-    max_blocks = block_table.shape[1]
-    cap = max_blocks * block
-    gqa, d = _decode_args(q, out, length, n, n_kv, cap, weights)
-    _appended(new_k, new_v, length_out, n, n_kv, d)
-    with _Call(stream, q, out, length, k_codes, k_scales, v_codes, v_scales, block_table, new_k,
-               new_v, length_out, weights) as call:
-        ws = call.ws(ws, rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None))
-        code = load().rkv_kv4_decode_paged(
-            _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
-            _ptr(v_scales), _ptr(block_table), _ptr(length), _ptr(length_out), n, n_kv, gqa, d,
-            num_blocks, block, max_blocks, float(scale), _ptr(out), _ptr(weights), _ptr(ws),
-            ws.numel(), call.stream)
-    _check("rkv_kv4_decode_paged", code)
-    return ws
+    n, hq, d = shape = _dims(q, "q", 3)
+    dev = q.get_device()
+    num_blocks, n_kv, block, ptrs = _kv4(k_codes, k_scales, v_codes, v_scales, dev)
+    max_blocks = _dims(block_table, "block_table", 2)[1]
+    gqa, cap = _group(hq, n_kv), max_blocks * block
+    args = (_at(q, "q", _BF16, shape, dev),
+            _at_or_none(new_k, "new_k", _BF16, (n, n_kv, d), dev),
+            _at_or_none(new_v, "new_v", _BF16, (n, n_kv, d), dev), *ptrs,
+            _at(block_table, "block_table", _I32, (n, max_blocks), dev),
+            _at(length, "len", _I32, (n,), dev),
+            _at_or_none(length_out, "len_out", _I32, (n,), dev), n, n_kv, gqa, d, num_blocks,
+            block, max_blocks, scale, _at(out, "out", _BF16, shape, dev),
+            _at_or_none(weights, "weights", _F32, (n, n_kv, cap), dev))
+    return _call("rkv_kv4_decode_paged", args, ws,
+                 lambda: rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None),
+                 dev, stream)
 
 
 # ------------------------------------------------------------------------------- weights, eviction
@@ -725,18 +716,16 @@ def rkv_dense_decode_weights_workspace_bytes(n: int, n_kv: int, gqa: int, max_le
 def rkv_dense_decode_weights(q, k, v, length, scale: float, out, weights, ws=None, stream=None):
     """Full-KV decode attention that adds each token's softmax weight (summed over the query heads
     of its group) to weights [n][n_kv][max_len] fp32."""
-    _shaped(k, "k", torch.bfloat16, (None, None, None, None))
-    _shaped(v, "v", torch.bfloat16, k.shape)
-    n, n_kv, max_len, _ = k.shape
-    gqa, d = _decode_args(q, out, length, n, n_kv, max_len, weights)
-    _shaped(k, "k", torch.bfloat16, (n, n_kv, max_len, d))
-    with _Call(stream, q, k, v, length, out, weights) as call:
-        ws = call.ws(ws, rkv_dense_decode_weights_workspace_bytes(n, n_kv, gqa, max_len))
-        code = load().rkv_dense_decode_weights(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(length), n, n_kv, gqa, d, max_len, float(scale),
-            _ptr(out), _ptr(weights), _ptr(ws), ws.numel(), call.stream)
-    _check("rkv_dense_decode_weights", code)
-    return ws
+    n, n_kv, max_len, d = shape = _dims(k, "k", 4)
+    hq = _dims(q, "q", 3)[1]
+    gqa, dev = _group(hq, n_kv), q.get_device()
+    args = (_at(q, "q", _BF16, (n, hq, d), dev), _at(k, "k", _BF16, shape, dev),
+            _at(v, "v", _BF16, shape, dev), _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d,
+            max_len, scale, _at(out, "out", _BF16, (n, hq, d), dev),
+            _at(weights, "weights", _F32, (n, n_kv, max_len), dev))
+    return _call("rkv_dense_decode_weights", args, ws,
+                 lambda: rkv_dense_decode_weights_workspace_bytes(n, n_kv, gqa, max_len), dev,
+                 stream)
 
 
 def rkv_prompt_weights_workspace_bytes(n: int, n_kv: int, gqa: int, max_q: int,
@@ -747,63 +736,49 @@ def rkv_prompt_weights_workspace_bytes(n: int, n_kv: int, gqa: int, max_q: int,
 def rkv_prompt_weights(q, q_len, k, length, scale: float, weights, ws=None, stream=None):
     """Adds the softmax weight that every key gets from the last q_len[u] positions' queries
     (q [n][Hq][max_q][128]) to weights [n][n_kv][max_len] fp32; see include/rkv.h."""
-    _shaped(k, "k", torch.bfloat16, (None, None, None, None))
-    n, n_kv, max_len, d = k.shape
-    _shaped(q, "q", torch.bfloat16, (n, None, None, d))
-    _shaped(q_len, "q_len", torch.int32, (n,))
-    _shaped(length, "len", torch.int32, (n,))
-    _shaped(weights, "weights", torch.float32, (n, n_kv, max_len))
-    gqa, max_q = _group(q.shape[1], n_kv), q.shape[2]
-    with _Call(stream, q, q_len, k, length, weights) as call:
-        ws = call.ws(ws, rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len))
-        code = load().rkv_prompt_weights(
-            _ptr(q), _ptr(q_len), _ptr(k), _ptr(length), n, n_kv, gqa, d, max_q, max_len,
-            float(scale), _ptr(weights), _ptr(ws), ws.numel(), call.stream)
-    _check("rkv_prompt_weights", code)
-    return ws
+    n, n_kv, max_len, d = shape = _dims(k, "k", 4)
+    _, hq, max_q, _ = _dims(q, "q", 4)
+    gqa, dev = _group(hq, n_kv), q.get_device()
+    args = (_at(q, "q", _BF16, (n, hq, max_q, d), dev), _at(q_len, "q_len", _I32, (n,), dev),
+            _at(k, "k", _BF16, shape, dev), _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d,
+            max_q, max_len, scale, _at(weights, "weights", _F32, (n, n_kv, max_len), dev))
+    return _call("rkv_prompt_weights", args, ws,
+                 lambda: rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len), dev,
+                 stream)
 
 
 def rkv_evict_workspace_bytes(n: int, n_kv: int, cap: int, keep: int) -> int:
     return int(load().rkv_evict_workspace_bytes(n, n_kv, cap, keep))
 
 
-def _evict(fn, cache, n, n_kv, cap, d, length, weights, pos, seen, keep, recent, length_out,
-           weights_out, pos_out, src_rows, ws, stream):
-    for t, name in ((length, "len"), (length_out, "len_out"), (seen, "seen")):
-        _shaped(t, name, torch.int32, (n,))
-    for t, name, dt in ((weights, "weights", torch.float32), (pos, "pos", torch.int32),
-                        (weights_out, "weights_out", torch.float32),
-                        (pos_out, "pos_out", torch.int32)):
-        _shaped(t, name, dt, (n, n_kv, cap))
-    if src_rows is not None:
-        _shaped(src_rows, "src_rows", torch.int32, (n, n_kv, keep))
-    with _Call(stream, *cache, length, weights, pos, seen, length_out, weights_out, pos_out,
-               src_rows) as call:
-        ws = call.ws(ws, rkv_evict_workspace_bytes(n, n_kv, cap, keep))
-        code = getattr(load(), fn)(
-            *[_ptr(t) for t in cache], _ptr(length), _ptr(length_out), _ptr(weights),
-            _ptr(weights_out), _ptr(pos), _ptr(pos_out), _ptr(seen), n, n_kv, d, cap, int(keep),
-            int(recent), _ptr(src_rows), _ptr(ws), ws.numel(), call.stream)
-    _check(fn, code)
-    return ws
+def _evict(fn, ptrs, n, n_kv, cap, d, length, weights, pos, seen, keep, recent, length_out,
+           weights_out, pos_out, src_rows, ws, dev, stream):
+    rows = (n, n_kv, cap)
+    args = (*ptrs, _at(length, "len", _I32, (n,), dev), _at(length_out, "len_out", _I32, (n,), dev),
+            _at(weights, "weights", _F32, rows, dev), _at(weights_out, "weights_out", _F32, rows, dev),
+            _at(pos, "pos", _I32, rows, dev), _at(pos_out, "pos_out", _I32, rows, dev),
+            _at(seen, "seen", _I32, (n,), dev), n, n_kv, d, cap, keep, recent,
+            _at_or_none(src_rows, "src_rows", _I32, (n, n_kv, keep), dev))
+    return _call(fn, args, ws, lambda: rkv_evict_workspace_bytes(n, n_kv, cap, keep), dev, stream)
 
 
 def rkv_evict(k, v, length, weights, pos, seen, keep: int, recent: int, length_out, weights_out,
               pos_out, src_rows=None, ws=None, stream=None):
     """Keep the `keep` rows of largest weight (the last `recent` positions always) of every
     (unit, KV head), in place; the *_out arrays may be the inputs. See include/rkv.h."""
-    _shaped(k, "k", torch.bfloat16, (None, None, None, None))
-    _shaped(v, "v", torch.bfloat16, k.shape)
-    n, n_kv, cap, d = k.shape
-    return _evict("rkv_evict", (k, v), n, n_kv, cap, d, length, weights, pos, seen, keep, recent,
-                  length_out, weights_out, pos_out, src_rows, ws, stream)
+    n, n_kv, cap, d = shape = _dims(k, "k", 4)
+    dev = k.get_device()
+    ptrs = (_at(k, "k", _BF16, shape, dev), _at(v, "v", _BF16, shape, dev))
+    return _evict("rkv_evict", ptrs, n, n_kv, cap, d, length, weights, pos, seen, keep, recent,
+                  length_out, weights_out, pos_out, src_rows, ws, dev, stream)
 
 
 def rkv_evict_kv4(k_codes, k_scales, v_codes, v_scales, length, weights, pos, seen, keep: int,
                   recent: int, length_out, weights_out, pos_out, src_rows=None, ws=None,
                   stream=None):
     """rkv_evict of a 4-bit cache."""
-    n, n_kv, cap = _kv4(k_codes, k_scales, v_codes, v_scales)
-    return _evict("rkv_evict_kv4", (k_codes, k_scales, v_codes, v_scales), n, n_kv, cap, HEAD_DIM,
-                  length, weights, pos, seen, keep, recent, length_out, weights_out, pos_out,
-                  src_rows, ws, stream)
+    _dims(k_codes, "k_codes", 4)
+    dev = k_codes.get_device()
+    n, n_kv, cap, ptrs = _kv4(k_codes, k_scales, v_codes, v_scales, dev)
+    return _evict("rkv_evict_kv4", ptrs, n, n_kv, cap, HEAD_DIM, length, weights, pos, seen, keep,
+                  recent, length_out, weights_out, pos_out, src_rows, ws, dev, stream)
