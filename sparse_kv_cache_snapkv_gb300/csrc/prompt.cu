@@ -28,14 +28,18 @@
 
 namespace rkv {
 
-constexpr int kPrThreads = 320;   // warp 0: TMA, warp 1: MMA, warps 2..9: accumulators
-constexpr int kPrEpi = 256;
+constexpr int kPrThreads = 576;   // warp 0: TMA, warp 1: MMA, warps 2..17: accumulators
+constexpr int kPrEpi = 512;       // two threads per stationary row, half of a tile's columns each
 constexpr int kPrStat = 256;      // stationary rows of an item
 constexpr int kPrTile = 128;      // streamed rows of a step
 constexpr int kPrStages = 3;
 constexpr int kPrStatBytes = kPrStat * kHeadDim * 2;   // 64 KB
 constexpr int kPrTileBytes = kPrTile * kHeadDim * 2;   // 32 KB
 constexpr uint32_t kPrCols = 512;
+// Slots of the streamed rows' log-sum-exps (pass 2). A tile is requested when the product three
+// tiles before it is done, which was issued when the accumulator five tiles before it was free: the
+// slot of that tile is free too, without a barrier of its own.
+constexpr int kPrNlSlots = kPrStages + 2;
 
 // Query rows of a (unit, KV head). With at least 256 queries a tile holds rows of one head (the
 // causal limits of a tile are then close together, and most of what it need not see is skipped);
@@ -81,7 +85,8 @@ struct PromptParams {
   float scale_log2;
   const int32_t* len;
   const int32_t* q_len;
-  float2* ml;            // [units][nsplit1][tiles1 * 256]: (max, sum) of every row
+  float* nl;             // [units][tiles1 * 256]: every row's negated log-sum-exp (log2 domain)
+  float2* ml;            // [units][nsplit1][tiles1 * 256]: (max, sum) of a split when nsplit1 > 1
   float* part;           // [nsplit2][units][max_len] when nsplit2 > 1
   float* weights;        // [units][max_len]
   uint32_t* status;
@@ -91,11 +96,15 @@ struct PrSmem {
   static constexpr size_t stat_off = 0;
   static constexpr size_t tile_off = 2 * (size_t)kPrStatBytes;
   static constexpr size_t bar_off = tile_off + (size_t)kPrStages * kPrTileBytes;
-  static constexpr size_t nl_off = bar_off + 128;          // [2][128] negated log-sum-exp
-  static constexpr size_t lim_off = nl_off + 2 * 128 * 4;  // [2][128] last visible key
-  static constexpr size_t total = lim_off + 2 * 128 * 4;   // below the 227 KB of a CTA
+  static constexpr size_t nl_off = bar_off + 256;  // [kPrNlSlots][128]
+  static constexpr size_t total = nl_off + (size_t)kPrNlSlots * kPrTile * 4;
 };
 static_assert(PrSmem::total <= 232448, "shared memory of a CTA");
+
+// -(max + log2 sum) of a row; -1e30 (its weights are 0) for one that sees nothing or is no query
+__device__ __forceinline__ float negated_lse(float m, float l) {
+  return l > 0.f ? -(m + log2f(l)) : (l == 0.f ? -1e30f : l);
+}
 
 struct PromptItem {
   int ukv, u, L, T;   // L = 0: nothing to do
@@ -178,9 +187,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* sfull = tempty + 2;
   uint64_t* sempty = sfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 2);
+  uint64_t* nfull = sempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(nfull + kPrNlSlots);
   float* nl_s = reinterpret_cast<float*>(smem + PrSmem::nl_off);
-  int* lim_s = reinterpret_cast<int*>(smem + PrSmem::lim_off);
 
   if (smem_addr(smem) & 1023u) {  // the swizzled tiles need it; a CTA's dynamic memory has it
     if (threadIdx.x == 0) set_status(p.status, RKV_DEV_SELECT_FAILED);
@@ -189,6 +198,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RowMap m1 = row_map(p.gqa, p.max_q, kPrStat), m2 = row_map(p.gqa, p.max_q, kPrTile);
   const int items = p.units * (PASS == 1 ? p.tiles1 * p.nsplit1 : p.tiles2 * p.nsplit2);
+
+  // Items come in waves of one per CTA, every second wave from the other end: the CTA that had the
+  // largest item of a wave gets the smallest of the next.
+  auto wave_item = [&](int w) {
+    return w * (int)gridDim.x + ((w & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+  };
 
   if (tid == 0) {
     for (int i = 0; i < kPrStages; ++i) {
@@ -201,6 +216,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], 1);
     }
+    for (int i = 0; i < kPrNlSlots; ++i) mbar_init(&nfull[i], 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -220,7 +236,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     // ------------------------------------------------------------------ loads
     if (lane == 0) {
       int step = 0, ic = 0, sent = 0;  // sent: stationary tiles requested
-      for (int i = blockIdx.x; i < items && !aborted; i += gridDim.x) {
+      for (int w = 0; w * gridDim.x < items && !aborted; ++w) {
+        const int i = wave_item(w);
+        if (i >= items) continue;
         const PromptItem it = prompt_item<PASS>(p, i);
         if (it.count == 0) continue;
         const int sb = ic & 1;
@@ -246,9 +264,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             aborted = true;
             break;
           }
-          const int y = PASS == 1
-                            ? kbase + (it.first + t) * kPrTile
-                            : qbase + tile_row0(m2, step_tile(p, it, it.first + t), kPrTile);
+          int y = kbase + (it.first + t) * kPrTile;
+          if (PASS == 2) {
+            const int x = step_tile(p, it, it.first + t);
+            y = qbase + tile_row0(m2, x, kPrTile);
+            // the same rows' log-sum-exps, as pass 1's tiles have them
+            const int row = m2.per_head ? (x / m2.per_head) * (m1.per_head * kPrStat) +
+                                              (x % m2.per_head) * kPrTile
+                                        : x * kPrTile;
+            const int ns = step % kPrNlSlots;
+            mbar_arrive_expect_tx(&nfull[ns], kPrTile * 4);
+            bulk_load(nl_s + ns * kPrTile, p.nl + (size_t)it.ukv * p.tiles1 * kPrStat + row,
+                      kPrTile * 4, &nfull[ns]);
+          }
           uint8_t* dst = tiles + (size_t)s * kPrTileBytes;
           mbar_arrive_expect_tx(&full[s], (uint32_t)kPrTileBytes);
           tma_load_2d(dst, PASS == 1 ? &kmap : &qmap, 0, y, &full[s]);
@@ -260,6 +288,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
         for (int j = max(0, step - kPrStages); j < step; ++j)  // let issued loads land
           mbar_wait(&full[j % kPrStages], (uint32_t)((j / kPrStages) & 1));
+        for (int j = max(0, step - kPrNlSlots); PASS == 2 && j < step; ++j)
+          mbar_wait(&nfull[j % kPrNlSlots], (uint32_t)((j / kPrNlSlots) & 1));
         for (int j = max(0, ic - 2); j < sent; ++j) mbar_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1));
       }
     }
@@ -267,7 +297,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     // ------------------------------------------------------------------ products
     if (lane == 0) {
       int step = 0, ic = 0;
-      for (int i = blockIdx.x; i < items && !aborted; i += gridDim.x) {
+      for (int w = 0; w * gridDim.x < items && !aborted; ++w) {
+        const int i = wave_item(w);
+        if (i >= items) continue;
         const PromptItem it = prompt_item<PASS>(p, i);
         if (it.count == 0) continue;
         const int sb = ic & 1;
@@ -307,16 +339,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ accumulators
-    const int rb = (warp - 2) >> 2;
+    const int e = warp - 2;
     const int quarter = warp & 3;       // TMEM lanes this warp may read
+    const int rb = (e >> 2) & 1, hf = e >> 3;
     const int srow = rb * 128 + quarter * 32 + lane;  // stationary row of this thread
+    const int c0 = hf * 64;             // its columns of a tile: c0 .. c0 + 63
     const int etid = tid - 64;
-    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb * kPrTile + c0);
+    // what the second half hands to the first, one item after the other
+    float2* xch = reinterpret_cast<float2*>(smem + PrSmem::nl_off);  // (pass 1: no log-sum-exps)
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     int step = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int w = 0; w * gridDim.x < items; ++w) {
+      const int i = wave_item(w);
+      if (i >= items) continue;
       const PromptItem it = prompt_item<PASS>(p, i);
       if (PASS == 1 && it.L == 0 && it.tile == 0 && it.ukv == it.u * p.n_kv && etid == 0) {
-        // (the first tile's split that comes first in the order reports; repeats do no harm)
         const int L = p.len[it.u], T = p.q_len[it.u];
         if (L < 0 || L > p.max_len)
           set_status(p.status, RKV_DEV_LEN_OVER_CAP);
@@ -335,133 +373,135 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             continue;
           }
           tc_fence_after();
-          const int k0 = (it.first + t) * kPrTile;
-          for (int cc = 0; cc < kPrTile; cc += 32) {
-            uint32_t r[32];
-            tmem_ld32(tmem + lane_addr + (uint32_t)((b * 2 + rb) * kPrTile + cc), r);
-            float mt = -INFINITY;
-            if (k0 + cc + 31 <= lim) {
+          const int k0 = (it.first + t) * kPrTile + c0;
+          const uint32_t ta = tmem + lane_addr + (uint32_t)(b * 2 * kPrTile);
+          uint32_t r[2][32];
+          tmem_ld32_start(ta, r[0]);
+          tmem_ld_wait(r[0]);
+          tmem_ld32_start(ta + 32, r[1]);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) mt = fmaxf(mt, __uint_as_float(r[j]));
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float x = (k0 + cc + j <= lim) ? __uint_as_float(r[j]) : -INFINITY;
-                r[j] = __float_as_uint(x);
-                mt = fmaxf(mt, x);
-              }
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) {
+              tmem_ld_wait(r[1]);
+              tc_fence_before();  // the accumulator is free once both halves are in registers
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&tempty[b]);
             }
-            const float mn = fmaxf(m, mt * p.scale_log2);
-            float a4[4] = {0.f, 0.f, 0.f, 0.f};
+            if (__any_sync(0xffffffffu, k0 + 32 * h + 31 > lim)) {  // (no divergence at the loads)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              a4[j & 3] += fast_exp2(fmaf(__uint_as_float(r[j]), p.scale_log2, -mn));
-            l = l * fast_exp2(m - mn) + ((a4[0] + a4[1]) + (a4[2] + a4[3]));
+              for (int j = 0; j < 32; ++j)
+                if (k0 + 32 * h + j > lim) r[h][j] = 0xff800000u;
+            }
+            float mt[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mt[j] = __uint_as_float(r[h][j]);
+#pragma unroll
+            for (int j = 4; j < 32; ++j) mt[j & 3] = fmaxf(mt[j & 3], __uint_as_float(r[h][j]));
+            const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * p.scale_log2;
+            const float mn = fmaxf(m, top);
+            const uint64_t off = pack2(-mn, -mn);
+            uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 y = unpack2(
+                  fma2(pack2(__uint_as_float(r[h][j]), __uint_as_float(r[h][j + 1])), scale2, off));
+              acc[(j >> 1) & 1] = add2(acc[(j >> 1) & 1], pack2(fast_exp2(y.x), fast_exp2(y.y)));
+            }
+            const float2 s = unpack2(add2(acc[0], acc[1]));
+            l = l * fast_exp2(m - mn) + (s.x + s.y);
             m = mn;
           }
+        }
+        if (hf == 1) xch[srow] = make_float2(m, l);
+        named_bar_sync(1, kPrEpi);
+        if (hf == 0) {
+          const float2 o = xch[srow];
+          const float mn = fmaxf(m, o.x);
+          l = l * fast_exp2(m - mn) + o.y * fast_exp2(o.x - mn);
+          m = mn;
+          // every row of every item is written, so that pass 2 never meets an old workspace
+          const size_t row = (size_t)it.tile * kPrStat + srow, rows = (size_t)p.tiles1 * kPrStat;
+          if (p.nsplit1 == 1) {
+            p.nl[it.ukv * rows + row] = negated_lse(m, l);
+          } else {
+            const int split = (i % (p.units * p.nsplit1)) % p.nsplit1;
+            p.ml[((size_t)it.ukv * p.nsplit1 + split) * rows + row] = make_float2(m, l);
+          }
+        }
+        named_bar_sync(1, kPrEpi);  // xch is rewritten by the next item
+      } else {
+        const int key = it.tile * kPrStat + srow;
+        uint64_t acc[2] = {0ull, 0ull};
+        for (int t = 0; t < it.count; ++t, ++step) {
+          const int b = step & 1, ns = step % kPrNlSlots;
+          if (aborted) continue;
+          if (!mbar_wait(&tfull[b], (uint32_t)((step >> 1) & 1)) ||
+              !mbar_wait(&nfull[ns], (uint32_t)((step / kPrNlSlots) & 1))) {
+            aborted = true;
+            continue;
+          }
+          tc_fence_after();
+          // a tile with rows that are no queries, or that do not see all of the stationary keys
+          const int x = step_tile(p, it, it.first + t);
+          int lo, hi;
+          tile_span(m2, x, kPrTile, &lo, &hi);
+          const bool mask = hi >= it.T || tile_query(m2, x, kPrTile, kPrTile - 1) < 0 ||
+                            it.L - it.T + lo < (it.tile + 1) * kPrStat - 1;
+          const uint32_t ta = tmem + lane_addr + (uint32_t)(b * 2 * kPrTile);
+          uint32_t r[2][32];
+          tmem_ld32_start(ta, r[0]);
+          tmem_ld_wait(r[0]);
+          tmem_ld32_start(ta + 32, r[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) tmem_ld_wait(r[1]);
+            if (mask) {
+              // row j of this half is query q + j of its head (wrapping at max_q where the rows run
+              // through the heads), and sees this key from query `from` on
+              const int base = c0 + 32 * h, from = key - (it.L - it.T);
+              if (m2.per_head) {
+                const int q = (x % m2.per_head) * kPrTile + base;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (q + j < from || q + j >= it.T) r[h][j] = 0xff800000u;
+              } else {
+                const int row = x * kPrTile + base, rows = p.gqa * p.max_q;
+                int q = row % p.max_q;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  if (q < from || q >= it.T || row + j >= rows) r[h][j] = 0xff800000u;
+                  q = q + 1 == p.max_q ? 0 : q + 1;
+                }
+              }
+            }
+            const ulonglong2* n2 =
+                reinterpret_cast<const ulonglong2*>(nl_s + ns * kPrTile + c0 + 32 * h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 v = n2[j];  // negated log-sum-exps of four rows
+              const float2 y0 = unpack2(fma2(pack2(__uint_as_float(r[h][4 * j]),
+                                                   __uint_as_float(r[h][4 * j + 1])), scale2, v.x));
+              const float2 y1 = unpack2(fma2(pack2(__uint_as_float(r[h][4 * j + 2]),
+                                                   __uint_as_float(r[h][4 * j + 3])), scale2, v.y));
+              acc[0] = add2(acc[0], pack2(fast_exp2(y0.x), fast_exp2(y0.y)));
+              acc[1] = add2(acc[1], pack2(fast_exp2(y1.x), fast_exp2(y1.y)));
+            }
+          }
+          // (the log-sum-exps are read before this too: their slot is free with the accumulator)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[b]);
         }
-        // every row of every item is written, so that pass 2 never meets an old workspace
-        const int per = p.units * p.nsplit1, split = (i % per) % p.nsplit1;
-        p.ml[((size_t)it.ukv * p.nsplit1 + split) * ((size_t)p.tiles1 * kPrStat) +
-             (size_t)it.tile * kPrStat + srow] = make_float2(m, l);
-      } else {
-        const int key = it.tile * kPrStat + srow;
-        // column e of streamed tile x: its negated log-sum-exp and its last visible key (a row
-        // without a query sees none)
-        auto column = [&](int t, float* nl, int* lim) {
-          const int x = step_tile(p, it, it.first + t);
-          const int qi = tile_query(m2, x, kPrTile, etid);
-          *nl = -1e30f;
-          *lim = -1;
-          if (qi < 0 || qi >= it.T) return;
-          *lim = it.L - it.T + qi;
-          // the same row in pass 1's tiles
-          const int h = m2.per_head ? x / m2.per_head : 0;
-          const int row = m2.per_head
-                              ? h * (m1.per_head * kPrStat) + qi
-                              : x * kPrTile + etid;
-          const float2* src = p.ml + (size_t)it.ukv * p.nsplit1 * p.tiles1 * kPrStat + row;
-          float m = -1e30f, l = 0.f;
-          for (int s = 0; s < p.nsplit1; ++s) {
-            const float2 y = src[(size_t)s * p.tiles1 * kPrStat];
-            const float mn = fmaxf(m, y.x);
-            l = l * fast_exp2(m - mn) + y.y * fast_exp2(y.x - mn);
-            m = mn;
-          }
-          *nl = l > 0.f ? -(m + log2f(l)) : (l == 0.f ? -1e30f : l);
-        };
-        float nl = 0.f;
-        int lim = 0;
-        if (it.count > 0) {
-          if (etid < kPrTile) {
-            column(0, &nl, &lim);
-            nl_s[etid] = nl;
-            lim_s[etid] = lim;
-          }
-          named_bar_sync(1, kPrEpi);
-        }
-        float acc = 0.f;
-        for (int t = 0; t < it.count; ++t, ++step) {
-          const int b = step & 1, cb = t & 1;
-          const bool more = t + 1 < it.count;
-          if (more && etid < kPrTile) column(t + 1, &nl, &lim);
-          if (!aborted && !mbar_wait(&tfull[b], (uint32_t)((step >> 1) & 1))) aborted = true;
-          if (!aborted) {
-            tc_fence_after();
-            // rows that are no queries, or that do not see all of the stationary keys
-            int lo, hi;
-            const int x = step_tile(p, it, it.first + t);
-            tile_span(m2, x, kPrTile, &lo, &hi);
-            const bool mask = hi >= it.T || tile_query(m2, x, kPrTile, kPrTile - 1) < 0 ||
-                              it.L - it.T + lo < (it.tile + 1) * kPrStat - 1;
-            float a4[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int cc = 0; cc < kPrTile; cc += 32) {
-              uint32_t r[32];
-              tmem_ld32(tmem + lane_addr + (uint32_t)((b * 2 + rb) * kPrTile + cc), r);
-              const float4* n4 = reinterpret_cast<const float4*>(nl_s + cb * kPrTile + cc);
-              const int4* l4 = reinterpret_cast<const int4*>(lim_s + cb * kPrTile + cc);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 v = n4[j];
-                float y0 = fmaf(__uint_as_float(r[4 * j + 0]), p.scale_log2, v.x);
-                float y1 = fmaf(__uint_as_float(r[4 * j + 1]), p.scale_log2, v.y);
-                float y2 = fmaf(__uint_as_float(r[4 * j + 2]), p.scale_log2, v.z);
-                float y3 = fmaf(__uint_as_float(r[4 * j + 3]), p.scale_log2, v.w);
-                if (mask) {
-                  const int4 q = l4[j];
-                  y0 = key <= q.x ? y0 : -INFINITY;
-                  y1 = key <= q.y ? y1 : -INFINITY;
-                  y2 = key <= q.z ? y2 : -INFINITY;
-                  y3 = key <= q.w ? y3 : -INFINITY;
-                }
-                a4[0] += fast_exp2(y0);
-                a4[1] += fast_exp2(y1);
-                a4[2] += fast_exp2(y2);
-                a4[3] += fast_exp2(y3);
-              }
-            }
-            acc += (a4[0] + a4[1]) + (a4[2] + a4[3]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[b]);
-          }
-          if (more && etid < kPrTile) {
-            nl_s[(cb ^ 1) * kPrTile + etid] = nl;
-            lim_s[(cb ^ 1) * kPrTile + etid] = lim;
-          }
-          named_bar_sync(1, kPrEpi);
-        }
-        if (key < it.L) {
-          if (p.nsplit2 == 1) {
-            if (it.count > 0 && !aborted) p.weights[(size_t)it.ukv * p.max_len + key] += acc;
-          } else {
-            const int per = p.units * p.nsplit2, split = (i % per) % p.nsplit2;
-            p.part[((size_t)split * p.units + it.ukv) * p.max_len + key] = acc;
-          }
-        }
+        const float2 s = unpack2(add2(acc[0], acc[1]));
+        // the two threads of a key add to it one after the other (shared memory is full)
+        const bool one = p.nsplit2 == 1;
+        const int split = (i % (p.units * p.nsplit2)) % p.nsplit2;
+        float* dst = one ? p.weights + (size_t)it.ukv * p.max_len + key
+                         : p.part + ((size_t)split * p.units + it.ukv) * p.max_len + key;
+        const bool mine = key < it.L && (!one || (it.count > 0 && !aborted));
+        if (hf == 0 && mine) *dst = (one ? *dst : 0.f) + (s.x + s.y);
+        named_bar_sync(1, kPrEpi);
+        if (hf == 1 && mine) *dst += s.x + s.y;
       }
     }
     if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
@@ -473,6 +513,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kPrCols) : "memory");
   }
+}
+
+// Joins the splits of pass 1 (grid: units x blocks of 256 rows).
+__global__ void __launch_bounds__(256) prompt_lse_kernel(PromptParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t rows = (size_t)p.tiles1 * kPrStat, row = (size_t)blockIdx.y * 256 + threadIdx.x;
+  const float2* src = p.ml + (size_t)blockIdx.x * p.nsplit1 * rows + row;
+  float m = -1e30f, l = 0.f;
+  for (int s = 0; s < p.nsplit1; ++s) {
+    const float2 y = src[s * rows];
+    const float mn = fmaxf(m, y.x);
+    l = l * fast_exp2(m - mn) + y.y * fast_exp2(y.x - mn);
+    m = mn;
+  }
+  p.nl[blockIdx.x * rows + row] = negated_lse(m, l);
 }
 
 // Sum of the splits, in their order.
@@ -493,32 +549,38 @@ struct PromptPlan {
   int tiles1, nsplit1, tiles2, nsplit2;
 };
 
-// Splits only where the items alone would leave SMs without work: a split costs its own
-// stationary load, and partial results that are read back.
+// Splits only where the items alone would leave SMs without work (a split costs its own stationary
+// load, and partial results that are read back). Pass 2 has few and uneven items (the first keys
+// are seen by every query): with fewer than four per SM the largest would outlast the rest.
 static PromptPlan prompt_plan(int n, int n_kv, int gqa, int max_q, int max_len) {
   PromptPlan p;
   const long long units = (long long)n * n_kv;
   const int sms = device_sm_count();
   p.tiles1 = row_tiles(row_map(gqa, max_q, kPrStat), kPrStat);
   p.tiles2 = (max_len + kPrStat - 1) / kPrStat;
-  auto splits = [&](long long items, int steps) {
-    if (items >= sms) return 1;
-    const int want = (int)(sms / items), most = (steps + 3) / 4;  // at least 4 steps a split
-    return want < most ? (want > 1 ? want : 1) : most;
+  auto splits = [](long long items, long long target, int steps) {
+    const long long want = target / items, most = (steps + 3) / 4;  // at least 4 steps a split
+    return (int)(want < 1 ? 1 : (want < most ? want : most));
   };
-  p.nsplit1 = splits(units * p.tiles1, (max_len + kPrTile - 1) / kPrTile);
-  p.nsplit2 = splits(units * p.tiles2, row_tiles(row_map(gqa, max_q, kPrTile), kPrTile));
+  p.nsplit1 = splits(units * p.tiles1, sms, (max_len + kPrTile - 1) / kPrTile);
+  const int steps2 = row_tiles(row_map(gqa, max_q, kPrTile), kPrTile);
+  const long long items2 = units * p.tiles2;
+  p.nsplit2 = items2 < sms ? splits(items2, sms, steps2)
+                           : splits(items2, 4LL * sms, steps2 > 64 ? steps2 : 1);
   return p;
 }
 
+static size_t nl_bytes(const PromptPlan& p, size_t units) {
+  return align_up(units * p.tiles1 * kPrStat * 4, 256);
+}
 static size_t ml_bytes(const PromptPlan& p, size_t units) {
-  return align_up(units * p.nsplit1 * p.tiles1 * kPrStat * 8, 256);
+  return p.nsplit1 > 1 ? align_up(units * p.nsplit1 * p.tiles1 * kPrStat * 8, 256) : 0;
 }
 
 size_t prompt_scratch_bytes(int n, int n_kv, int gqa, int max_q, int max_len) {
   const PromptPlan p = prompt_plan(n, n_kv, gqa, max_q, max_len);
   const size_t units = (size_t)n * n_kv;
-  return ml_bytes(p, units) +
+  return nl_bytes(p, units) + ml_bytes(p, units) +
          (p.nsplit2 > 1 ? align_up(units * p.nsplit2 * max_len * 4, 256) : 0);
 }
 
@@ -555,12 +617,18 @@ cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s) {
   p.len = a.len;
   p.q_len = a.q_len;
   unsigned char* w = static_cast<unsigned char*>(a.scratch);
+  p.nl = reinterpret_cast<float*>(w);
+  w += nl_bytes(pl, p.units);
   p.ml = reinterpret_cast<float2*>(w);
   p.part = reinterpret_cast<float*>(w + ml_bytes(pl, p.units));
   p.weights = a.weights;
   p.status = a.status;
   cudaError_t e = launch_prompt_pass<1>(km, qm, p, s);
   if (e != cudaSuccess) return e;
+  if (p.nsplit1 > 1) {
+    e = launch_pdl_kernel(prompt_lse_kernel, dim3(p.units, p.tiles1), dim3(256), 0, s, p);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_prompt_pass<2>(km, qm, p, s);
   if (e != cudaSuccess || p.nsplit2 == 1) return e;
   int y = (a.max_len + 255) / 256;
