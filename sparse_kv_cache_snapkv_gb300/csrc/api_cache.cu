@@ -92,7 +92,6 @@ rkv_status decode_impl(const CacheDecodeArgs& in, int head_dim, float scale, voi
   if (w != RKV_OK) return w;
   a.scale_log2 = scale * kLog2e;
   a.status = status_ptr(ws);
-  cache_decode_plan(a.n, a.n_kv, a.cap, &a.nsplit, &a.tokens_per_split);
   cache_decode_carve(&a, after_status(ws));
   return from_cuda(launch_cache_decode(a, as_stream(stream)));
 }

@@ -15,11 +15,10 @@
 // same heads' columns of O^T. A decode is bound by the cache's bytes; a tcgen05 tile of 128 rows
 // would need the operands unpacked into shared memory first, which costs more than the product.
 //
-// The fragments come straight from global memory into registers. A fragment's columns may be
-// any permutation of the dimensions as long as Q has the same one, and its rows any permutation of
-// the tokens, so every lane takes 16 contiguous bytes of K codes (or of bf16 K) and 8 (16) of V,
-// and no byte passes through shared memory. Each lane's next K is requested as soon as S^T is
-// done, its next V after O^T: a warp always has loads in flight.
+// A fragment's columns may be any permutation of the dimensions as long as Q has the same one, and
+// its rows any permutation of the tokens, so every lane unpacks 16 contiguous bytes of K codes and 8
+// of V straight into fragments. A 4-bit tile (2304 bytes) is copied to its warp's own ring in
+// shared memory four tiles ahead; bf16 fragments come from global memory directly.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,6 +27,7 @@
 #include "cache4.cuh"
 #include "common.cuh"
 #include "rkv_internal.h"
+#include "tensor_core.cuh"
 
 namespace rkv {
 
@@ -114,42 +114,61 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
 // ==========================================================================================
 // decode
 // ==========================================================================================
+// The work of a call is the sequence of all (unit, KV head)s' rounds of 128 tokens; CTA i of C
+// takes the i-th of C equal parts of it, whatever the lengths are. A part is a run of segments, each
+// within one (unit, KV head); only its first and its last can be shared with other CTAs, so two
+// slots of partial results per CTA are enough. The CTA that finishes a (unit, KV head) last (a
+// counter in the workspace, back at zero afterwards) joins the parts in their order: no second
+// launch, and no result depends on the order in which CTAs end.
 constexpr int kCdThreads = 256;
 constexpr int kCdWarps = kCdThreads / 32;
-constexpr int kCdTile = 16;                       // tokens a warp takes at a time
-constexpr int kCdRound = kCdTile * kCdWarps;      // tokens a CTA takes at a time
-constexpr int kCdWeightChunk = 1024;              // tokens a CTA of the join kernel turns into weights
+constexpr int kCdTile = 16;                   // tokens a warp takes at a time
+constexpr int kCdRound = kCdTile * kCdWarps;  // tokens a CTA takes at a time
+constexpr int kCdPerSm = 2;                   // CTAs that an SM holds
+constexpr int kCdDepth = 4;                   // tiles in flight per warp (4 bits)
+constexpr int kCdWeightChunk = 1024;          // tokens a CTA of the weights kernel takes
 
-void cache_decode_plan(int n, int n_kv, int cap, int* nsplit, int* tokens_per_split) {
-  const long long units = (long long)n * n_kv;
-  const long long target = 4LL * device_sm_count();  // two waves of two CTAs per SM
-  const int rounds = (cap + kCdRound - 1) / kCdRound;
-  long long ns = (target + units - 1) / units;
-  ns = ns > rounds ? rounds : ns;
-  const int per = (int)((rounds + ns - 1) / ns);
-  *tokens_per_split = per * kCdRound;
-  *nsplit = (rounds + per - 1) / per;
+static int cache_decode_ctas(int n, int n_kv, int cap) {
+  const long long rounds = (long long)n * n_kv * ((cap + kCdRound - 1) / kCdRound);
+  const long long slots = (long long)kCdPerSm * device_sm_count();
+  return (int)(rounds < slots ? rounds : slots);
+}
+
+// Who turns logits into weights: with many (unit, KV head)s the CTA that finishes one, while others
+// still stream (its logits are then in L2); with few, whose last CTA would be alone with a long
+// sequence, a second kernel over all SMs.
+static bool weights_apart(int n, int n_kv) { return (long long)n * n_kv * 2 < device_sm_count(); }
+
+struct CacheScratch {
+  size_t counters, lse, part_ml, part_o, logits, total;
+};
+static CacheScratch cache_scratch(int n, int n_kv, int gqa, int cap, bool with_weights) {
+  const size_t units = (size_t)n * n_kv, slots = 2 * (size_t)cache_decode_ctas(n, n_kv, cap);
+  CacheScratch c;
+  c.counters = 0;
+  c.lse = align_up((units + 1) * 4, 256);
+  c.part_ml = c.lse + align_up(units * gqa * 4, 256);
+  c.part_o = c.part_ml + align_up(slots * gqa * 8, 256);
+  c.logits = c.part_o + align_up(slots * gqa * kHeadDim * 4, 256);
+  c.total = c.logits + (with_weights ? align_up(units * cap * gqa * 4, 256) : 0);
+  return c;
 }
 
 size_t cache_decode_scratch_bytes(int n, int n_kv, int gqa, int cap, bool with_weights) {
-  int ns, tps;
-  cache_decode_plan(n, n_kv, cap, &ns, &tps);
-  const size_t units = (size_t)n * n_kv;
-  return align_up(units * ns * gqa * 8, 256) + align_up(units * ns * gqa * kHeadDim * 4, 256) +
-         (with_weights ? align_up(units * cap * gqa * 4, 256) : 0);
+  return cache_scratch(n, n_kv, gqa, cap, with_weights).total;
 }
 
 void cache_decode_carve(CacheDecodeArgs* a, void* scratch) {
   unsigned char* p = static_cast<unsigned char*>(scratch);
-  const size_t rows = (size_t)a->n * a->n_kv * a->nsplit * a->gqa;
-  a->part_ml = reinterpret_cast<float*>(p);
-  p += align_up(rows * 8, 256);
-  a->part_o = reinterpret_cast<float*>(p);
-  p += align_up(rows * kHeadDim * 4, 256);
-  a->logits = reinterpret_cast<float*>(p);
+  const CacheScratch c = cache_scratch(a->n, a->n_kv, a->gqa, a->cap, a->weights != nullptr);
+  a->counters = reinterpret_cast<int32_t*>(p + c.counters);
+  a->lse = reinterpret_cast<float*>(p + c.lse);
+  a->part_ml = reinterpret_cast<float*>(p + c.part_ml);
+  a->part_o = reinterpret_cast<float*>(p + c.part_o);
+  a->logits = reinterpret_cast<float*>(p + c.logits);
 }
 
-// Loads that do not stay in L1 (the cache is read once) and see what this CTA wrote before a barrier.
+// A load that does not stay in L1 (the cache is read once).
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -158,13 +177,21 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_stream8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p)
+
+// 8- and 16-byte asynchronous copies of which only the first `bytes` are read; the rest is zeroed.
+__device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(bytes)
                : "memory");
-  return v;
+}
+__device__ __forceinline__ void cp_async8_zfill(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <bool F16>
@@ -195,138 +222,107 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Lane roles of the fragments: r = lane / 4, c = lane % 4. As rows of K, lane (r, c) holds parts of
-// tokens tok(r) and 8 + tok(r) of the tile; as columns of V^T, tokens c, 4 + c, 8 + c, 12 + c.
-// tok() makes the two agree: fragment row 2 c is token c, row 2 c + 1 token 4 + c.
-__device__ __forceinline__ int frag_token(int r) { return (r >> 1) + 4 * (r & 1); }
+// Lane roles of the fragments: r = lane / 4, c = lane % 4. Row s of a 16-token tile's fragment is
+// token frag_token(s) (and s + 8 is frag_token(s) + 8): as rows of K, lane (r, c) holds parts of
+// tokens frag_token(r) and + 8; as columns of V^T, tokens frag_token(2 c), frag_token(2 c + 1) and
+// both + 8. The order makes the shared-memory reads below free of bank conflicts: rows are 64
+// bytes, so two tokens of different parity make one 128-byte line.
+__device__ __forceinline__ int frag_token(int s) { return s ^ ((s >> 1) & 1); }
 
-// One lane's share of a 16-token tile of K or V. Dimensions by fragment position:
-//   4 bits K: lane (., c) has dimensions 32 c .. 32 c + 31, four of them per 16-wide step;
-//   4 bits V: lane (r, .) has 16 r .. 16 r + 15, two of them per 16-high step;
-//   bf16 K: 32 i + 8 c .. + 7 (i = 0..3), bf16 V: 8 r .. + 7 and 64 + 8 r .. + 7.
-template <bool KV4>
-struct KTile;
-template <bool KV4>
-struct VTile;
-
-template <>
-struct KTile<true> {
-  uint4 w[2];
-  uint32_t sb[2];  // two scale bytes each
-  __device__ __forceinline__ void load(const CacheDecodeArgs& a, size_t row0, int left, int r, int c) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = frag_token(r) + 8 * h;
-      const size_t row = row0 + t;
-      w[h] = make_uint4(0u, 0u, 0u, 0u);
-      sb[h] = 0u;
-      if (t < left) {
-        w[h] = ld_stream16(static_cast<const uint8_t*>(a.k) + row * kCodeBytes + 16 * c);
-        sb[h] = *reinterpret_cast<const uint16_t*>(a.k_scales + row * kRowScales + 2 * c);
-      }
-    }
-  }
+// One warp's 16-token tile of a 4-bit cache in shared memory, as it lies in the cache but for V,
+// whose rows' 16-byte quarters are swapped in pairs in every other four tokens (again for the
+// banks). Dimensions by fragment position: K lane (., c): 32 c .. 32 c + 31, four per 16-wide step;
+// V lane (r, .): 16 r .. 16 r + 15, two per 16-high step.
+struct __align__(16) Kv4Tile {
+  uint8_t k[kCdTile * kCodeBytes];
+  uint8_t v[kCdTile * kCodeBytes];
+  uint8_t ks[kCdTile * kRowScales];
+  uint8_t vs[kCdTile * kRowScales];
 };
 
-template <>
-struct VTile<true> {
-  uint2 w[4];
-  uint32_t sb[4];
-  __device__ __forceinline__ void load(const CacheDecodeArgs& a, size_t row0, int left, int r, int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 4 * i + c;
-      const size_t row = row0 + t;
-      w[i] = make_uint2(0u, 0u);
-      sb[i] = 0u;
-      if (t < left) {
-        w[i] = ld_stream8(static_cast<const uint8_t*>(a.v) + row * kCodeBytes + 8 * r);
-        sb[i] = a.v_scales[row * kRowScales + r];
-      }
-    }
+// Starts the copies of a tile whose first row is `row`, of which `left` rows count (others zero).
+__device__ __forceinline__ void load_kv4(Kv4Tile* t, const CacheDecodeArgs& a, size_t row, int left,
+                                         int lane) {
+  const int tr = lane >> 2, q = lane & 3;
+  const size_t kb = row * kCodeBytes + 16 * lane;
+  const uint8_t* k = static_cast<const uint8_t*>(a.k) + kb;
+  const uint8_t* v = static_cast<const uint8_t*>(a.v) + kb;
+  const int vq = tr * kCodeBytes + 16 * (q ^ ((tr >> 1) & 2));
+  const int sr = lane & 15;
+  const uint8_t* s = (lane < 16 ? a.k_scales : a.v_scales) + (row + sr) * kRowScales;
+  if (left >= kCdTile) {
+    cp_async16(t->k + 16 * lane, k);
+    cp_async16(t->k + 16 * lane + 512, k + 512);
+    cp_async16(t->v + vq, v);
+    cp_async16(t->v + vq + 512, v + 512);
+    cp_async8_zfill(t->ks + 8 * lane, s, 8);  // (vs follows ks)
+  } else {
+    // rows past the end are not touched: their copies read nothing, from the tile's first row
+    const uint32_t lo = tr < left ? 16 : 0, hi = tr + 8 < left ? 16 : 0;
+    cp_async16_zfill(t->k + 16 * lane, lo ? k : static_cast<const uint8_t*>(a.k) + row * kCodeBytes, lo);
+    cp_async16_zfill(t->k + 16 * lane + 512,
+                     hi ? k + 512 : static_cast<const uint8_t*>(a.k) + row * kCodeBytes, hi);
+    cp_async16_zfill(t->v + vq, lo ? v : static_cast<const uint8_t*>(a.v) + row * kCodeBytes, lo);
+    cp_async16_zfill(t->v + vq + 512,
+                     hi ? v + 512 : static_cast<const uint8_t*>(a.v) + row * kCodeBytes, hi);
+    cp_async8_zfill(t->ks + 8 * lane,
+                    sr < left ? s : (lane < 16 ? a.k_scales : a.v_scales) + row * kRowScales,
+                    sr < left ? 8 : 0);
   }
-};
-
-template <>
-struct KTile<false> {
-  uint4 w[2][4];
-  __device__ __forceinline__ void load(const CacheDecodeArgs& a, size_t row0, int left, int r, int c) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = frag_token(r) + 8 * h;
-      const bf16* p = static_cast<const bf16*>(a.k) + (row0 + t) * kHeadDim + 8 * c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[h][i] = t < left ? ld_stream16(p + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-};
-
-template <>
-struct VTile<false> {
-  uint4 w[4][2];
-  __device__ __forceinline__ void load(const CacheDecodeArgs& a, size_t row0, int left, int r, int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 4 * i + c;
-      const bf16* p = static_cast<const bf16*>(a.v) + (row0 + t) * kHeadDim + 8 * r;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[i][h] = t < left ? ld_stream16(p + 64 * h) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-};
-
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// S^T (16 tokens x 8 heads) of a K tile with the Q fragments.
-__device__ __forceinline__ void scores_of(const KTile<true>& k, const uint2 (&q)[8], float (&s)[4]) {
-  uint32_t sc[2][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const uint32_t x = ((k.sb[h] >> (8 * b)) & 0xffu) << 7;
-      sc[h][b] = x | (x << 16);
-    }
+// A scale byte as the same fp16 number twice; two bytes as a pair.
+__device__ __forceinline__ uint32_t scale_twice(uint32_t b) { return b * 0x00800080u; }
+__device__ __forceinline__ uint32_t scale_pair(uint32_t lo, uint32_t hi) {
+  return (hi * 65536u + lo) * 128u;
+}
+
+// S^T (16 tokens x 8 heads) of a tile with the Q fragments.
+__device__ __forceinline__ void scores_kv4(const Kv4Tile* t, const uint2 (&q)[8], int r, int c,
+                                           float (&s)[4]) {
+  const int ta = frag_token(r);
+  const uint4 wa = *reinterpret_cast<const uint4*>(t->k + ta * kCodeBytes + 16 * c);
+  const uint4 wb = *reinterpret_cast<const uint4*>(t->k + (ta + 8) * kCodeBytes + 16 * c);
+  const uint32_t sa[2] = {scale_twice(t->ks[ta * kRowScales + 2 * c]),
+                          scale_twice(t->ks[ta * kRowScales + 2 * c + 1])};
+  const uint32_t sb[2] = {scale_twice(t->ks[(ta + 8) * kRowScales + 2 * c]),
+                          scale_twice(t->ks[(ta + 8) * kRowScales + 2 * c + 1])};
+  const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 8 dimensions: two 16-wide steps
     uint32_t lo[4], hi[4];
-    codes_to_half2(word_of(k.w[0], i), lo);
-    codes_to_half2(word_of(k.w[1], i), hi);
+    codes_to_half2(aw[i], lo);
+    codes_to_half2(bw[i], hi);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      lo[e] = hmul2(lo[e], sc[0][i >> 1]);
-      hi[e] = hmul2(hi[e], sc[1][i >> 1]);
+      lo[e] = hmul2(lo[e], sa[i >> 1]);
+      hi[e] = hmul2(hi[e], sb[i >> 1]);
     }
     mma16816<true>(s, lo[0], hi[0], lo[1], hi[1], q[2 * i].x, q[2 * i].y);
     mma16816<true>(s, lo[2], hi[2], lo[3], hi[3], q[2 * i + 1].x, q[2 * i + 1].y);
   }
 }
 
-__device__ __forceinline__ void scores_of(const KTile<false>& k, const uint2 (&q)[8], float (&s)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    mma16816<false>(s, k.w[0][i].x, k.w[1][i].x, k.w[0][i].y, k.w[1][i].y, q[2 * i].x, q[2 * i].y);
-    mma16816<false>(s, k.w[0][i].z, k.w[1][i].z, k.w[0][i].w, k.w[1][i].w, q[2 * i + 1].x,
-                    q[2 * i + 1].y);
-  }
-}
-
-// O^T += V^T P^T; p[row half][head of the pair] are the probabilities of this lane's S^T entries.
-// 4 bits: P in fp16 (11 significant bits; p <= 2^15, see kCdShift), V exact in fp16.
-__device__ __forceinline__ void accumulate(const VTile<true>& v, const float (&p)[4], float (&o)[8][4]) {
+// O^T += V^T P^T; p are the probabilities of this lane's S^T entries. P in fp16 (11 significant
+// bits, at most 2^15: see kCdShift), V exact in fp16.
+__device__ __forceinline__ void accumulate_kv4(const Kv4Tile* t, const float (&p)[4], int r, int c,
+                                               float (&o)[8][4]) {
   const __half2 p0 = __floats2half2_rn(p[0], p[1]), p1 = __floats2half2_rn(p[2], p[3]);
   const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
   const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
-  const uint32_t s01 = (v.sb[0] << 7) | (v.sb[1] << 23), s23 = (v.sb[2] << 7) | (v.sb[3] << 23);
+  const int t0 = frag_token(2 * c), t1 = frag_token(2 * c + 1);
+  const uint8_t* v0 = t->v + t0 * kCodeBytes + 16 * ((r >> 1) ^ ((t0 >> 1) & 2)) + 8 * (r & 1);
+  const uint8_t* v1 = t->v + t1 * kCodeBytes + 16 * ((r >> 1) ^ ((t1 >> 1) & 2)) + 8 * (r & 1);
+  const uint2 x0 = *reinterpret_cast<const uint2*>(v0), x1 = *reinterpret_cast<const uint2*>(v1);
+  const uint2 x2 = *reinterpret_cast<const uint2*>(v0 + 512), x3 = *reinterpret_cast<const uint2*>(v1 + 512);
+  const uint8_t* s = t->vs + r;
+  const uint32_t s01 = scale_pair(s[t0 * kRowScales], s[t1 * kRowScales]);
+  const uint32_t s23 = scale_pair(s[(t0 + 8) * kRowScales], s[(t1 + 8) * kRowScales]);
   constexpr uint32_t m = 0x0f0f0f0fu;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const uint32_t w0 = w ? v.w[0].y : v.w[0].x, w1 = w ? v.w[1].y : v.w[1].x;
-    const uint32_t w2 = w ? v.w[2].y : v.w[2].x, w3 = w ? v.w[3].y : v.w[3].x;
+    const uint32_t w0 = w ? x0.y : x0.x, w1 = w ? x1.y : x1.x;
+    const uint32_t w2 = w ? x2.y : x2.x, w3 = w ? x3.y : x3.x;
     uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd dimensions, tokens side by side
     codes_to_half2((w0 & m) | ((w1 << 4) & ~m), e01);
     codes_to_half2(((w0 >> 4) & m) | (w1 & ~m), d01);
@@ -339,9 +335,50 @@ __device__ __forceinline__ void accumulate(const VTile<true>& v, const float (&p
   }
 }
 
-// bf16: V is bf16, so P is too, as the sum of two bf16 numbers (17 significant bits): the second
-// product is free under the cache's bytes and keeps P's rounding out of the result.
-__device__ __forceinline__ void accumulate(const VTile<false>& v, const float (&p)[4], float (&o)[8][4]) {
+// The bf16 cache needs no unpacking: its fragments come straight from global memory, each lane's
+// next K requested as soon as S^T is done and its next V after O^T. Dimensions by fragment
+// position: K lane (., c): 32 i + 8 c .. + 7 (i = 0..3); V lane (r, .): 8 r .. + 7, 64 + 8 r .. + 7.
+struct BfTile {
+  uint4 k[2][4];
+  uint4 v[4][2];
+  __device__ __forceinline__ void load_k(const CacheDecodeArgs& a, size_t row, int left, int r, int c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = frag_token(r) + 8 * h;
+      const bf16* p = static_cast<const bf16*>(a.k) + (row + t) * kHeadDim + 8 * c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        k[h][i] = t < left ? ld_stream16(p + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void load_v(const CacheDecodeArgs& a, size_t row, int left, int r, int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = frag_token(2 * c + (i & 1)) + 8 * (i >> 1);
+      const bf16* p = static_cast<const bf16*>(a.v) + (row + t) * kHeadDim + 8 * r;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[i][h] = t < left ? ld_stream16(p + 64 * h) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+__device__ __forceinline__ void scores_bf(const BfTile& t, const uint2* q, float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint2 q0 = q[64 * i], q1 = q[64 * i + 32];
+    mma16816<false>(s, t.k[0][i].x, t.k[1][i].x, t.k[0][i].y, t.k[1][i].y, q0.x, q0.y);
+    mma16816<false>(s, t.k[0][i].z, t.k[1][i].z, t.k[0][i].w, t.k[1][i].w, q1.x, q1.y);
+  }
+}
+
+// V is bf16, so P is too, as the sum of two bf16 numbers (16 significant bits): the second product
+// is free under the cache's bytes and keeps P's rounding out of the result.
+__device__ __forceinline__ void accumulate_bf(const BfTile& t, const float (&p)[4], float (&o)[8][4]) {
   const __nv_bfloat162 h0 = __floats2bfloat162_rn(p[0], p[1]), h1 = __floats2bfloat162_rn(p[2], p[3]);
   const float2 f0 = __bfloat1622float2(h0), f1 = __bfloat1622float2(h1);
   const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&h0));
@@ -350,8 +387,8 @@ __device__ __forceinline__ void accumulate(const VTile<false>& v, const float (&
   const uint32_t c1 = transpose8x8(pack_bf16x2(p[2] - f1.x, p[3] - f1.y));
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t w0 = word_of(v.w[0][j >> 2], j & 3), w1 = word_of(v.w[1][j >> 2], j & 3);
-    const uint32_t w2 = word_of(v.w[2][j >> 2], j & 3), w3 = word_of(v.w[3][j >> 2], j & 3);
+    const uint32_t w0 = word_of(t.v[0][j >> 2], j & 3), w1 = word_of(t.v[1][j >> 2], j & 3);
+    const uint32_t w2 = word_of(t.v[2][j >> 2], j & 3), w3 = word_of(t.v[3][j >> 2], j & 3);
     const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
     const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
     mma16816<false>(o[j], a0, a1, a2, a3, b0, b1);
@@ -373,13 +410,71 @@ constexpr float kCdLazy = 8.0f;
 template <bool KV4>
 constexpr float kCdShift = KV4 ? 7.0f : 0.0f;
 
-template <int G>
-struct CdSmem {
-  float m[kCdWarps][8];
-  float l[kCdWarps][8];
-  float o[kCdWarps][G][kHeadDim];
-  float lse[8];
+// A warp's softmax state: maxima and sums of heads 2 c and 2 c + 1 (the sums per lane), O^T.
+struct CdState {
+  float m[2], l[2], o[8][4];
+  __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -1e30f;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  }
 };
+
+// Logits of a tile (log2 domain, rows past the end -inf), kept for the weights; then their
+// probabilities, after the maximum has followed.
+template <int G, bool KV4>
+__device__ __forceinline__ void softmax_tile(CdState& st, float (&s)[4], const float (&cs)[2], int left,
+                                             int r, int c, float* logits, float (&p)[4]) {
+  const int ta = frag_token(r);
+  s[0] *= cs[0];
+  s[1] *= cs[1];
+  s[2] *= cs[0];
+  s[3] *= cs[1];
+  if (left < kCdTile) {
+    if (ta >= left) s[0] = s[1] = -INFINITY;
+    if (ta + 8 >= left) s[2] = s[3] = -INFINITY;
+  }
+  if (logits && 2 * c < G) {
+    float* x = logits + ta * G + 2 * c;
+    if (G == 1) {
+      if (ta < left) x[0] = s[0];
+      if (ta + 8 < left) x[8] = s[2];
+    } else {
+      if (ta < left) *reinterpret_cast<float2*>(x) = make_float2(s[0], s[1]);
+      if (ta + 8 < left) *reinterpret_cast<float2*>(x + 8 * G) = make_float2(s[2], s[3]);
+    }
+  }
+  float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]);
+  if (__any_sync(0xffffffffu, m0 > st.m[0] + kCdLazy || m1 > st.m[1] + kCdLazy)) {
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+      m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+    }
+    m0 = fmaxf(m0, st.m[0]);
+    m1 = fmaxf(m1, st.m[1]);
+    const float f0 = fast_exp2(st.m[0] - m0), f1 = fast_exp2(st.m[1] - m1);
+    st.m[0] = m0;
+    st.m[1] = m1;
+    st.l[0] *= f0;
+    st.l[1] *= f1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      st.o[j][0] *= f0;
+      st.o[j][1] *= f1;
+      st.o[j][2] *= f0;
+      st.o[j][3] *= f1;
+    }
+  }
+  const float b0 = kCdShift<KV4> - st.m[0], b1 = kCdShift<KV4> - st.m[1];
+  p[0] = fast_exp2(s[0] + b0);
+  p[1] = fast_exp2(s[1] + b1);
+  p[2] = fast_exp2(s[2] + b0);
+  p[3] = fast_exp2(s[3] + b1);
+  st.l[0] += p[0] + p[2];
+  st.l[1] += p[1] + p[3];
+}
 
 // Length that the attention sees, and whether the step's token is appended.
 __device__ __forceinline__ int decode_length(const CacheDecodeArgs& a, int u, bool* append) {
@@ -393,76 +488,210 @@ __device__ __forceinline__ float neg_lse(float m, float l) {
   return l > 0.f ? -(m + log2f(l)) : (l == 0.f ? -INFINITY : l);
 }
 
-// weights of tokens [t0, t1) from their logits
+// weights of tokens [t0, t1) from their logits (L2, written by other SMs) and the heads' neg_lse
 template <int G>
 __device__ __forceinline__ void add_weights(const float* logits, float* weights, int t0, int t1,
                                             const float* nlse) {
   float nl[G];
 #pragma unroll
   for (int h = 0; h < G; ++h) nl[h] = nlse[h];
-  for (int t = t0 + threadIdx.x; t < t1; t += kCdThreads) {
-    const float* x = logits + (size_t)t * G;
-    float s = 0.f;
+  constexpr int kU = 4;  // tokens in flight per thread
+  for (int b = t0 + (int)threadIdx.x; b < t1; b += kU * kCdThreads) {
+    float x[kU][G], w[kU];
 #pragma unroll
-    for (int h = 0; h < G; ++h) s += fast_exp2(x[h] + nl[h]);
-    weights[t] += s;
+    for (int k = 0; k < kU; ++k) {
+      const int t = b + k * kCdThreads;
+      if (t < t1) {
+        const float* src = logits + (size_t)t * G;
+        w[k] = weights[t];
+        if (G % 4 == 0) {
+#pragma unroll
+          for (int h = 0; h < G; h += 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + h));
+            x[k][h] = y.x;
+            x[k][h + 1] = y.y;
+            x[k][h + 2] = y.z;
+            x[k][h + 3] = y.w;
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < G; ++h) x[k][h] = __ldcg(src + h);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int t = b + k * kCdThreads;
+      if (t < t1) {
+        float s = 0.f;
+#pragma unroll
+        for (int h = 0; h < G; ++h) s += fast_exp2(x[k][h] + nl[h]);
+        weights[t] = w[k] + s;
+      }
+    }
   }
 }
 
+template <int G>
+struct CdMerge {
+  float m[kCdWarps][8];
+  float l[kCdWarps][8];
+  float o[kCdWarps][G][kHeadDim];
+};
+constexpr size_t cd_ring_bytes(bool kv4) { return kv4 ? (size_t)kCdWarps * kCdDepth * sizeof(Kv4Tile) : 0; }
 template <int G, bool KV4>
-__global__ void __launch_bounds__(kCdThreads, 2) cache_decode_kernel(CacheDecodeArgs a) {
-  __shared__ CdSmem<G> sm;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = lane >> 2, c = lane & 3;
-  const int ukv = blockIdx.x, split = blockIdx.y;
-  const int u = ukv / a.n_kv, g = ukv - u * a.n_kv;
-  bool append;
-  const int L = decode_length(a, u, &append);
-  if (split == 0 && g == 0 && tid == 0) {
-    const int l = a.len[u];
-    if (l < 0 || l > a.cap || (a.new_k && !append)) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
-    // (len_out that is len itself is written by the join kernel, after every reader)
-    if (a.new_k && a.len_out != a.len) a.len_out[u] = append ? l + 1 : l;
-  }
-  const int tb = split * a.tokens_per_split;
-  const int te = min(L, tb + a.tokens_per_split);
+constexpr size_t cd_smem_bytes() {
+  return sizeof(CdMerge<G>) > cd_ring_bytes(KV4) ? sizeof(CdMerge<G>) : cd_ring_bytes(KV4);
+}
 
-  if (KV4 && append && L - 1 >= tb && L - 1 < te) {  // this CTA's tokens include the new one
-    if (tid < 16) {
-      const bool v = tid >= 8;
-      const int blk = tid & 7, at = L - 1;
-      const size_t dst = a.pm.table
-                             ? paged_row(a.pm, paged_block(a.pm, u, at, a.status), a.n_kv, g, at)
-                             : (size_t)ukv * a.cap + at;
-      uint32_t w[8], sb;
-      load32((v ? a.new_v : a.new_k) + (size_t)ukv * kHeadDim + blk * kScaleGroup, w);
-      const uint2 cd = quantise16(w, &sb);
-      uint8_t* codes = static_cast<uint8_t*>(const_cast<void*>(v ? a.v : a.k));
-      *reinterpret_cast<uint2*>(codes + dst * kCodeBytes + blk * 8) = cd;
-      const_cast<uint8_t*>(v ? a.v_scales : a.k_scales)[dst * kRowScales + blk] = (uint8_t)sb;
+// Where a CTA begins: its first round's unit, KV head and round, and how much there is in all.
+struct CdStart {
+  long long total;  // rounds of the call
+  long long begin, end;  // this CTA's part
+  int ctas;         // CTAs with work
+  int u, g, round;
+};
+
+__device__ __forceinline__ int rounds_of(int L) { return (L + kCdRound - 1) / kCdRound; }
+
+// first round of CTA i, and the CTA that has round x
+__device__ __forceinline__ long long part_begin(const CdStart& s, int i) { return s.total * i / s.ctas; }
+__device__ __forceinline__ int part_of(const CdStart& s, long long x) {
+  return (int)(((x + 1) * s.ctas - 1) / s.total);
+}
+
+// Every CTA adds up the units' rounds (each thread a run of units) and finds its own part.
+__device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* out,
+                                           unsigned long long* tmp) {
+  const int tid = threadIdx.x;
+  const int per = (a.n + kCdThreads - 1) / kCdThreads;
+  const int u0 = min(a.n, tid * per), u1 = min(a.n, u0 + per);
+  bool ap;
+  unsigned long long mine = 0;
+  for (int u = u0; u < u1; ++u) mine += rounds_of(decode_length(a, u, &ap));
+  const unsigned long long before = block_excl_scan64(mine, tmp);
+  if (tid == kCdThreads - 1) out->total = (long long)(before + mine) * a.n_kv;
+  __syncthreads();
+  const long long total = out->total;
+  const int ctas = (int)min((long long)gridDim.x, total);
+  if (ctas == 0 || (int)blockIdx.x >= ctas) {
+    if (tid == 0) out->ctas = ctas;
+    if (tid == 0) out->begin = out->end = 0;
+  } else {
+    const long long b = total * blockIdx.x / ctas;
+    if (tid == 0) {
+      out->ctas = ctas;
+      out->begin = b;
+      out->end = total * (blockIdx.x + 1) / ctas;
     }
-    __syncthreads();
-  }
-
-  // Q fragments: lane (r, c) holds head r. 4 bits: fp16, each head scaled by a power of two that
-  // puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it is exact, and
-  // what is lost below is far under the fp32 rounding of the sum.
-  uint2 q[8];
-  float cs[2];  // logit scale of heads 2 c, 2 c + 1
-  {
-    const bf16* qr = a.q + ((size_t)ukv * G + r) * kHeadDim;
-    uint2 x[8];
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int d = KV4 ? 32 * c + 4 * j : 32 * (j >> 1) + 8 * c + 4 * (j & 1);
-      x[j] = r < G ? *reinterpret_cast<const uint2*>(qr + d) : make_uint2(0u, 0u);
-      if (KV4) {
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[j].x)), fabsf(bf16_hi(x[j].x))));
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[j].y)), fabsf(bf16_hi(x[j].y))));
+    long long at = (long long)before * a.n_kv;
+    if (b >= at && b < at + (long long)mine * a.n_kv) {
+      for (int u = u0; u < u1; ++u) {
+        const int R = rounds_of(decode_length(a, u, &ap));
+        const long long all = (long long)R * a.n_kv;
+        if (b < at + all) {
+          out->u = u;
+          out->g = (int)((b - at) / R);
+          out->round = (int)((b - at) - (long long)out->g * R);
+          break;
+        }
+        at += all;
       }
     }
+  }
+  __syncthreads();
+}
+
+template <int G, bool KV4>
+__global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(CacheDecodeArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ CdStart start;
+  __shared__ unsigned long long scan[33];
+  __shared__ uint2 qf[KV4 ? 1 : 8 * 32];
+  __shared__ float lse[8];
+  __shared__ int flag;
+  CdMerge<G>& mg = *reinterpret_cast<CdMerge<G>*>(dyn);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const int units = a.n * a.n_kv;
+  bool append;
+  pdl_trigger();
+
+  find_start(a, &start, scan);
+  // units without tokens have no CTA of their own; bad lengths are told once
+  for (int ukv = blockIdx.x; ukv < units; ukv += gridDim.x) {
+    const int u = ukv / a.n_kv, L = decode_length(a, u, &append);
+    if (L == 0)
+      for (int i = tid; i < G * kHeadDim; i += kCdThreads)
+        a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(0.f);
+    if (tid == 0 && ukv == u * a.n_kv) {
+      const int l = a.len[u];
+      if (l < 0 || l > a.cap || (a.new_k && !append)) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
+    }
+  }
+
+  Kv4Tile* ring = reinterpret_cast<Kv4Tile*>(dyn) + warp * kCdDepth;
+  int u = start.u, g = start.g, round = start.round;
+  bool first = true;
+  for (long long at = start.begin; at < start.end; first = false) {
+    const int L = decode_length(a, u, &append);
+    const int R = rounds_of(L);
+    if (R == 0) {  // (a unit without tokens)
+      ++u;
+      continue;
+    }
+    const int rounds = (int)min((long long)(R - round), start.end - at);
+    const int ukv = u * a.n_kv + g;
+    const int tb = round * kCdRound, te = min(L, (round + rounds) * kCdRound);
+    const bool whole = rounds == R;
+
+    if (KV4 && append && round + rounds == R) {  // this segment's tokens include the new one
+      if (tid < 16) {
+        const bool v = tid >= 8;
+        const int blk = tid & 7, row = L - 1;
+        const size_t dst = a.pm.table
+                               ? paged_row(a.pm, paged_block(a.pm, u, row, a.status), a.n_kv, g, row)
+                               : (size_t)ukv * a.cap + row;
+        uint32_t w[8], sb;
+        load32((v ? a.new_v : a.new_k) + (size_t)ukv * kHeadDim + blk * kScaleGroup, w);
+        const uint2 cd = quantise16(w, &sb);
+        uint8_t* codes = static_cast<uint8_t*>(const_cast<void*>(v ? a.v : a.k));
+        *reinterpret_cast<uint2*>(codes + dst * kCodeBytes + blk * 8) = cd;
+        const_cast<uint8_t*>(v ? a.v_scales : a.k_scales)[dst * kRowScales + blk] = (uint8_t)sb;
+        __threadfence();
+      }
+      __syncthreads();
+    }
+
+    auto row_of = [&](int t0) -> size_t {  // row of the first token of a tile (it lies in one block)
+      return a.pm.table ? paged_row(a.pm, paged_block(a.pm, u, t0, a.status), a.n_kv, g, t0)
+                        : (size_t)ukv * a.cap + t0;
+    };
+    int t0 = tb + warp * kCdTile;
+    const int tiles = t0 < te ? (te - t0 + kCdRound - 1) / kCdRound : 0;
     if (KV4) {
+#pragma unroll
+      for (int d = 0; d < kCdDepth - 1; ++d) {
+        const int t = t0 + d * kCdRound;
+        if (t < te) load_kv4(ring + d, a, row_of(t), te - t, lane);
+        cp_async_commit();
+      }
+    }
+
+    // Q fragments: lane (r, c) holds head r. 4 bits: fp16, each head scaled by a power of two that
+    // puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it is exact, and
+    // what is lost below is far under the fp32 rounding of the sum.
+    uint2 q[KV4 ? 8 : 1];
+    float cs[2] = {a.scale_log2, a.scale_log2};  // logit scale of heads 2 c, 2 c + 1
+    const bf16* qr = a.q + ((size_t)ukv * G + r) * kHeadDim;
+    if (KV4) {
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q[j] = r < G ? *reinterpret_cast<const uint2*>(qr + 32 * c + 4 * j) : make_uint2(0u, 0u);
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j].x)), fabsf(bf16_hi(q[j].x))));
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j].y)), fabsf(bf16_hi(q[j].y))));
+      }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // exponent of amax, kept where both 2^(8 - e) and 2^(e - 8) are normal numbers
@@ -471,233 +700,224 @@ __global__ void __launch_bounds__(kCdThreads, 2) cache_decode_kernel(CacheDecode
       const float down = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const __half2 lo = __floats2half2_rn(bf16_lo(x[j].x) * up, bf16_hi(x[j].x) * up);
-        const __half2 hi = __floats2half2_rn(bf16_lo(x[j].y) * up, bf16_hi(x[j].y) * up);
+        const __half2 lo = __floats2half2_rn(bf16_lo(q[j].x) * up, bf16_hi(q[j].x) * up);
+        const __half2 hi = __floats2half2_rn(bf16_lo(q[j].y) * up, bf16_hi(q[j].y) * up);
         q[j] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                           *reinterpret_cast<const uint32_t*>(&hi));
       }
       cs[0] = __shfl_sync(0xffffffffu, down, 8 * c);
       cs[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
     } else {
+      if (warp == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = x[j];
-      cs[0] = cs[1] = a.scale_log2;
+        for (int j = 0; j < 8; ++j)
+          qf[(j % (KV4 ? 1 : 8)) * 32 + lane] =
+              r < G ? *reinterpret_cast<const uint2*>(qr + 32 * (j >> 1) + 8 * c + 4 * (j & 1))
+                    : make_uint2(0u, 0u);
+      }
+      __syncthreads();
     }
-  }
 
-  float m[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, o[8][4];
+    CdState st;
+    st.clear();
+    float* logits = a.weights ? a.logits + ((size_t)ukv * a.cap + t0) * G : nullptr;
+    if (KV4) {
+      for (int i = 0; i < tiles; ++i, t0 += kCdRound) {
+        cp_async_wait<kCdDepth - 2>();
+        __syncwarp();  // this tile has landed for every lane, and every lane is done with the last
+        const int tn = t0 + (kCdDepth - 1) * kCdRound;
+        if (tn < te) load_kv4(ring + (i + kCdDepth - 1) % kCdDepth, a, row_of(tn), te - tn, lane);
+        cp_async_commit();
+        const Kv4Tile* t = ring + i % kCdDepth;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, p[4];
+        scores_kv4(t, reinterpret_cast<const uint2(&)[8]>(q), r, c, s);
+        softmax_tile<G, true>(st, s, cs, te - t0, r, c, logits, p);
+        if (logits) logits += kCdRound * G;
+        accumulate_kv4(t, p, r, c, st.o);
+      }
+    } else {
+      BfTile t;
+      if (tiles > 0) {
+        const size_t row = row_of(t0);
+        t.load_k(a, row, te - t0, r, c);
+        t.load_v(a, row, te - t0, r, c);
+      }
+      for (int i = 0; i < tiles; ++i, t0 += kCdRound) {
+        const int tn = t0 + kCdRound;
+        const size_t next = tn < te ? row_of(tn) : 0;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, p[4];
+        scores_bf(t, qf + lane, s);
+        if (tn < te) t.load_k(a, next, te - tn, r, c);
+        softmax_tile<G, false>(st, s, cs, te - t0, r, c, logits, p);
+        if (logits) logits += kCdRound * G;
+        accumulate_bf(t, p, st.o);
+        if (tn < te) t.load_v(a, next, te - tn, r, c);
+      }
+    }
+
+    // join the warps: lane (r, c) holds dimensions out_dim(., r, .) of heads 2 c, 2 c + 1
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float* logits = a.weights ? a.logits + (size_t)ukv * a.cap * G : nullptr;
+    for (int d = 4; d < 32; d <<= 1) {
+      st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], d);
+      st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], d);
+    }
+    __syncthreads();  // the ring is the merge area's memory
+    if (r == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mg.m[warp][2 * c + e] = st.m[e];
+        mg.l[warp][2 * c + e] = st.l[e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int h = 2 * c + (e & 1);
+        if (h < G) mg.o[warp][h][out_dim<KV4>(j, r, e >> 1)] = st.o[j][e];
+      }
+    __syncthreads();
+    const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
+    for (int i = tid; i < G * kHeadDim; i += kCdThreads) {
+      const int h = i / kHeadDim, d = i % kHeadDim;
+      float M = -1e30f, S = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < kCdWarps; ++w) M = fmaxf(M, mg.m[w][h]);
+#pragma unroll
+      for (int w = 0; w < kCdWarps; ++w) {
+        const float f = fast_exp2(mg.m[w][h] - M);
+        S = fmaf(mg.l[w][h], f, S);
+        O = fmaf(mg.o[w][h][d], f, O);
+      }
+      M -= kCdShift<KV4>;  // p was 2^(s - m + shift)
+      if (whole) {
+        a.out[((size_t)ukv * G + h) * kHeadDim + d] = __float2bfloat16_rn(S == 0.f ? 0.f : O / S);
+        if (d == 0) lse[h] = neg_lse(M, S);
+      } else {
+        a.part_o[(slot * G + h) * kHeadDim + d] = O;
+        if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(M, S);
+      }
+    }
 
-  auto row_of = [&](int t0) -> size_t {  // row of the first token of a tile (it lies in one block)
-    return a.pm.table ? paged_row(a.pm, paged_block(a.pm, u, t0, a.status), a.n_kv, g, t0)
-                      : (size_t)ukv * a.cap + t0;
-  };
-  KTile<KV4> kt;
-  VTile<KV4> vt;
-  int t0 = tb + warp * kCdTile;
-  if (t0 < te) {
-    const size_t row = row_of(t0);
-    kt.load(a, row, te - t0, r, c);
-    vt.load(a, row, te - t0, r, c);
-  }
-  while (t0 < te) {
-    const int left = te - t0, tn = t0 + kCdRound;
-    const size_t next = tn < te ? row_of(tn) : 0;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    scores_of(kt, q, s);
-    if (tn < te) kt.load(a, next, te - tn, r, c);
-    const int ra = frag_token(r), rb = ra + 8;
-    s[0] = ra < left ? s[0] * cs[0] : -INFINITY;
-    s[1] = ra < left ? s[1] * cs[1] : -INFINITY;
-    s[2] = rb < left ? s[2] * cs[0] : -INFINITY;
-    s[3] = rb < left ? s[3] * cs[1] : -INFINITY;
-    if (logits) {
-      if (2 * c < G) {
-        float* x = logits + (size_t)(t0 + ra) * G + 2 * c;
-        if (G == 1) {
-          if (ra < left) x[0] = s[0];
-          if (rb < left) x[8 * G] = s[2];
-        } else {
-          if (ra < left) *reinterpret_cast<float2*>(x) = make_float2(s[0], s[1]);
-          if (rb < left) *reinterpret_cast<float2*>(x + 8 * G) = make_float2(s[2], s[3]);
+    bool done = whole;
+    if (!whole) {
+      // the CTAs that share this (unit, KV head): those of its first and its last round
+      const long long z0 = at - round, z1 = z0 + R - 1;
+      const int i0 = part_of(start, z0), i1 = part_of(start, z1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        flag = atomicAdd(a.counters + ukv, 1) == i1 - i0;
+        if (flag) a.counters[ukv] = 0;
+      }
+      __syncthreads();
+      done = flag != 0;
+      if (done) {
+        __threadfence();
+        const size_t s0 = 2 * (size_t)i0 + (part_begin(start, i0) == z0 ? 0 : 1);
+        const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+        float* mx = reinterpret_cast<float*>(dyn);  // [8] maxima
+        if (warp < G) {
+          float M = -1e30f;
+          for (int k = i0 + lane; k <= i1; k += 32)
+            M = fmaxf(M, __ldcg(ml + (k == i0 ? s0 : 2 * (size_t)k) * G + warp).x);
+#pragma unroll
+          for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+          float S = 0.f;
+          for (int k = i0 + lane; k <= i1; k += 32) {
+            const float2 x = __ldcg(ml + (k == i0 ? s0 : 2 * (size_t)k) * G + warp);
+            S = fmaf(x.y, fast_exp2(x.x - M), S);
+          }
+#pragma unroll
+          for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
+          if (lane == 0) {
+            mx[warp] = M;
+            mx[8 + warp] = S;
+            lse[warp] = neg_lse(M, S);
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < G * kHeadDim; i += kCdThreads) {
+          const int h = i / kHeadDim;
+          const float M = mx[h], S = mx[8 + h];
+          float O = 0.f;
+#pragma unroll 4
+          for (int k = i0; k <= i1; ++k) {
+            const size_t sl = k == i0 ? s0 : 2 * (size_t)k;
+            O = fmaf(__ldcg(a.part_o + sl * G * kHeadDim + i),
+                     fast_exp2(__ldcg(ml + sl * G + h).x - M), O);
+          }
+          a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(S == 0.f ? 0.f : O / S);
         }
       }
     }
-    float mt0 = fmaxf(s[0], s[2]), mt1 = fmaxf(s[1], s[3]);
-    if (__any_sync(0xffffffffu, mt0 > m[0] + kCdLazy || mt1 > m[1] + kCdLazy)) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        mt0 = fmaxf(mt0, __shfl_xor_sync(0xffffffffu, mt0, d));
-        mt1 = fmaxf(mt1, __shfl_xor_sync(0xffffffffu, mt1, d));
-      }
-      mt0 = fmaxf(mt0, m[0]);
-      mt1 = fmaxf(mt1, m[1]);
-      const float f0 = fast_exp2(m[0] - mt0), f1 = fast_exp2(m[1] - mt1);
-      m[0] = mt0;
-      m[1] = mt1;
-      l[0] *= f0;
-      l[1] *= f1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        o[j][0] *= f0;
-        o[j][1] *= f1;
-        o[j][2] *= f0;
-        o[j][3] *= f1;
+    if (done && a.weights) {
+      __syncthreads();
+      if (a.weights_apart) {
+        if (tid < G) a.lse[(size_t)ukv * G + tid] = lse[tid];
+      } else {
+        add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, 0, L, lse);
       }
     }
-    const float b0 = kCdShift<KV4> - m[0], b1 = kCdShift<KV4> - m[1];
-    const float p[4] = {fast_exp2(s[0] + b0), fast_exp2(s[1] + b1), fast_exp2(s[2] + b0),
-                        fast_exp2(s[3] + b1)};
-    l[0] += p[0] + p[2];
-    l[1] += p[1] + p[3];
-    accumulate(vt, p, o);
-    if (tn < te) vt.load(a, next, te - tn, r, c);
-    t0 = tn;
+    __syncthreads();  // shared memory is used again
+    at += rounds;
+    round = 0;
+    if (++g == a.n_kv) {
+      g = 0;
+      ++u;
+    }
   }
 
-  // join the warps: lane (r, c) holds dimensions out_dim(., r, .) of heads 2 c, 2 c + 1
-#pragma unroll
-  for (int d = 4; d < 32; d <<= 1) {
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
-    l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
-  }
-  if (r == 0) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      sm.m[warp][2 * c + e] = m[e];
-      sm.l[warp][2 * c + e] = l[e];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int h = 2 * c + (e & 1);
-      if (h < G) sm.o[warp][h][out_dim<KV4>(j, r, e >> 1)] = o[j][e];
-    }
-  __syncthreads();
-  for (int i = tid; i < G * kHeadDim; i += kCdThreads) {
-    const int h = i / kHeadDim, d = i % kHeadDim;
-    float M = -1e30f, S = 0.f, O = 0.f;
-#pragma unroll
-    for (int w = 0; w < kCdWarps; ++w) M = fmaxf(M, sm.m[w][h]);
-#pragma unroll
-    for (int w = 0; w < kCdWarps; ++w) {
-      const float f = fast_exp2(sm.m[w][h] - M);
-      S = fmaf(sm.l[w][h], f, S);
-      O = fmaf(sm.o[w][h][d], f, O);
-    }
-    M -= kCdShift<KV4>;  // p was 2^(s - m + shift)
-    if (a.nsplit == 1) {
-      a.out[((size_t)ukv * G + h) * kHeadDim + d] = __float2bfloat16_rn(S == 0.f ? 0.f : O / S);
-      if (d == 0) sm.lse[h] = neg_lse(M, S);
-    } else {
-      const size_t row = ((size_t)ukv * a.nsplit + split) * G + h;
-      a.part_o[row * kHeadDim + d] = O;
-      if (d == 0) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(M, S);
-    }
-  }
-  if (a.nsplit == 1 && a.weights) {
+  // the lengths move on when every CTA has read them (they may be their own inputs)
+  if (a.len_out) {
     __syncthreads();
-    add_weights<G>(logits, a.weights + (size_t)ukv * a.cap, tb, te, sm.lse);
-  }
-}
-
-// Joins the splits: blockIdx.y = 0 writes the outputs (and a length that is its own input), the
-// others turn kCdWeightChunk logits at a time into weights.
-template <int G>
-__global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs a) {
-  __shared__ float nlse[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ukv = blockIdx.x, u = ukv / a.n_kv;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (size_t)ukv * a.nsplit * G;
-  bool append;
-  int L;
-  if (a.new_k && a.len_out != a.len) {
-    L = max(0, min(a.len_out[u], a.cap));
-  } else {
-    L = decode_length(a, u, &append);
-  }
-  if (blockIdx.y == 0) {
-    if (a.nsplit == 1) return;
-    const float* po = a.part_o + (size_t)ukv * a.nsplit * G * kHeadDim;
-    for (int i = tid; i < G * kHeadDim; i += kCdThreads) {
-      const int h = i / kHeadDim;
-      float M = -1e30f, S = 0.f, O = 0.f;
-      for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, ml[s * G + h].x);
-      for (int s = 0; s < a.nsplit; ++s) {
-        const float2 x = ml[s * G + h];
-        const float f = fast_exp2(x.x - M);
-        S = fmaf(x.y, f, S);
-        O = fmaf(po[(size_t)s * G * kHeadDim + i], f, O);
+    if (tid == 0) {
+      __threadfence();
+      flag = atomicAdd(a.counters + units, 1) == (int)gridDim.x - 1;
+      if (flag) a.counters[units] = 0;
+    }
+    __syncthreads();
+    if (flag)
+      for (int i = tid; i < a.n; i += kCdThreads) {
+        const int l = a.len[i];
+        a.len_out[i] = l >= 0 && l < a.cap ? l + 1 : l;
       }
-      a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(S == 0.f ? 0.f : O / S);
-    }
-    return;
   }
-  const int first = (blockIdx.y - 1) * kCdWeightChunk;
-  if (first >= L) return;
-  if (warp < G) {
-    float M = -1e30f, S = 0.f;
-    for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, ml[s * G + warp].x);
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 4));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
-    for (int s = lane; s < a.nsplit; s += 32) {
-      const float2 x = ml[s * G + warp];
-      S = fmaf(x.y, fast_exp2(x.x - M), S);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
-    if (lane == 0) nlse[warp] = neg_lse(M, S);
-  }
-  __syncthreads();
-  for (int t0 = first; t0 < L; t0 += (int)(gridDim.y - 1) * kCdWeightChunk)
-    add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, t0,
-                   min(L, t0 + kCdWeightChunk), nlse);
 }
 
-// A length that is its own input moves on after every reader.
-__global__ void cache_length_kernel(CacheDecodeArgs a) {
-  const int u = blockIdx.x * blockDim.x + threadIdx.x;
-  if (u >= a.n) return;
-  bool append;
-  const int L = decode_length(a, u, &append);
-  if (append) a.len_out[u] = L;
-}
-
+// Weights of a few long (unit, KV head)s, kCdWeightChunk tokens per CTA.
 template <int G>
-static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
-  const dim3 grid(a.n * a.n_kv, a.nsplit);
-  if (a.kv4)
-    cache_decode_kernel<G, true><<<grid, kCdThreads, 0, s>>>(a);
-  else
-    cache_decode_kernel<G, false><<<grid, kCdThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.nsplit > 1) {
-    const int chunks = a.weights ? (a.cap + kCdWeightChunk - 1) / kCdWeightChunk : 0;
-    cache_join_kernel<G><<<dim3(a.n * a.n_kv, 1 + (chunks < 4096 ? chunks : 4096)), kCdThreads, 0, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (a.new_k && a.len_out == a.len) {
-    cache_length_kernel<<<(a.n + 255) / 256, 256, 0, s>>>(a);
-    e = cudaGetLastError();
-  }
-  return e;
+__global__ void __launch_bounds__(kCdThreads) cache_weights_kernel(CacheDecodeArgs a) {
+  pdl_wait();
+  const int ukv = blockIdx.x, u = ukv / a.n_kv;
+  const int L = max(0, min((a.len_out ? a.len_out : a.len)[u], a.cap));
+  for (int t0 = blockIdx.y * kCdWeightChunk; t0 < L; t0 += gridDim.y * kCdWeightChunk)
+    add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, t0,
+                   min(L, t0 + kCdWeightChunk), a.lse + (size_t)ukv * G);
 }
 
-cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t s) {
+template <int G, bool KV4>
+static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
+  constexpr size_t smem = cd_smem_bytes<G, KV4>();
+  cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4>, smem);
+  if (e != cudaSuccess) return e;
+  cache_decode_kernel<G, KV4>
+      <<<cache_decode_ctas(a.n, a.n_kv, a.cap), kCdThreads, smem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.weights || !a.weights_apart) return e;
+  const int chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;
+  return launch_pdl_kernel(cache_weights_kernel<G>, dim3(a.n * a.n_kv, chunks < 4096 ? chunks : 4096),
+                           dim3(kCdThreads), 0, s, a);
+}
+
+cudaError_t launch_cache_decode(const CacheDecodeArgs& in, cudaStream_t s) {
+  CacheDecodeArgs a = in;
+  a.weights_apart = weights_apart(a.n, a.n_kv);
   switch (a.gqa) {
-    case 1: return launch_group<1>(a, s);
-    case 2: return launch_group<2>(a, s);
-    case 4: return launch_group<4>(a, s);
-    case 8: return launch_group<8>(a, s);
+    case 1: return a.kv4 ? launch_group<1, true>(a, s) : launch_group<1, false>(a, s);
+    case 2: return a.kv4 ? launch_group<2, true>(a, s) : launch_group<2, false>(a, s);
+    case 4: return a.kv4 ? launch_group<4, true>(a, s) : launch_group<4, false>(a, s);
+    case 8: return a.kv4 ? launch_group<8, true>(a, s) : launch_group<8, false>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -229,19 +229,19 @@ struct CacheDecodeArgs {
   const bf16* new_v;
   PagedMap pm;
   int n, n_kv, gqa, cap;
-  int nsplit, tokens_per_split;
   float scale_log2;
   bf16* out;
-  float* weights;  // nullptr: not asked for
-  float* logits;   // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
-  float* part_ml;  // workspace [n*n_kv][nsplit][gqa][2]
-  float* part_o;   // workspace [n*n_kv][nsplit][gqa][128]
+  float* weights;      // nullptr: not asked for
+  int32_t* counters;   // workspace [n*n_kv + 1], zero between calls
+  float* lse;          // workspace [n*n_kv][gqa]: negated log-sum-exps (log2 domain)
+  float* part_ml;      // workspace [2 per CTA][gqa][2]
+  float* part_o;       // workspace [2 per CTA][gqa][128]
+  float* logits;       // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
   uint32_t* status;
-  bool kv4;
+  bool kv4, weights_apart;
 };
-void cache_decode_plan(int n, int n_kv, int cap, int* nsplit, int* tokens_per_split);
 size_t cache_decode_scratch_bytes(int n, int n_kv, int gqa, int cap, bool with_weights);
-// places logits and the partials in the scratch area (after the status word)
+// places the workspace's parts in the scratch area (after the status word)
 void cache_decode_carve(CacheDecodeArgs* a, void* scratch);
 cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t s);
 
