@@ -18,7 +18,7 @@
 // A fragment's columns may be any permutation of the dimensions as long as Q has the same one, and
 // its rows any permutation of the tokens, so every lane unpacks 16 contiguous bytes of K codes and 8
 // of V straight into fragments. A 4-bit tile (2304 bytes) is copied to its warp's own ring in
-// shared memory four tiles ahead; bf16 fragments come from global memory directly.
+// shared memory a step of two tiles ahead; bf16 fragments come from global memory directly.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -122,14 +122,19 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
 // launch, and no result depends on the order in which CTAs end.
 constexpr int kCdThreads = 256;
 constexpr int kCdWarps = kCdThreads / 32;
-constexpr int kCdTile = 16;                   // tokens a warp takes at a time
-constexpr int kCdRound = kCdTile * kCdWarps;  // tokens a CTA takes at a time
+constexpr int kCdTile = 16;                   // tokens of a fragment tile
 constexpr int kCdPerSm = 2;                   // CTAs that an SM holds
-constexpr int kCdDepth = 4;                   // tiles in flight per warp (4 bits)
+// Tokens that a warp takes at a time: two tiles of 4 bits (their products are independent, and the
+// bookkeeping of a step is shared), one of bf16; and that a CTA takes at a time.
+template <bool KV4>
+constexpr int kCdStep = KV4 ? 2 * kCdTile : kCdTile;
+template <bool KV4>
+constexpr int kCdRound = kCdStep<KV4>* kCdWarps;
 constexpr int kCdWeightChunk = 1024;          // tokens a CTA of the weights kernel takes
 
-static int cache_decode_ctas(int n, int n_kv, int cap) {
-  const long long rounds = (long long)n * n_kv * ((cap + kCdRound - 1) / kCdRound);
+static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
+  const int round = kv4 ? kCdRound<true> : kCdRound<false>;
+  const long long rounds = (long long)n * n_kv * ((cap + round - 1) / round);
   const long long slots = (long long)kCdPerSm * device_sm_count();
   return (int)(rounds < slots ? rounds : slots);
 }
@@ -143,7 +148,8 @@ struct CacheScratch {
   size_t counters, lse, part_ml, part_o, logits, total;
 };
 static CacheScratch cache_scratch(int n, int n_kv, int gqa, int cap, bool with_weights) {
-  const size_t units = (size_t)n * n_kv, slots = 2 * (size_t)cache_decode_ctas(n, n_kv, cap);
+  const size_t units = (size_t)n * n_kv;
+  const size_t slots = 2 * (size_t)cache_decode_ctas(n, n_kv, cap, false);  // (never fewer than 4 bits')
   CacheScratch c;
   c.counters = 0;
   c.lse = align_up((units + 1) * 4, 256);
@@ -176,22 +182,6 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
                : "l"(p)
                : "memory");
   return v;
-}
-
-// 8- and 16-byte asynchronous copies of which only the first `bytes` are read; the rest is zeroed.
-__device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8_zfill(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(dst)), "l"(src),
-               "r"(bytes)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <bool F16>
@@ -240,36 +230,51 @@ struct __align__(16) Kv4Tile {
   uint8_t vs[kCdTile * kRowScales];
 };
 
-// Starts the copies of a tile whose first row is `row`, of which `left` rows count (others zero).
-__device__ __forceinline__ void load_kv4(Kv4Tile* t, const CacheDecodeArgs& a, size_t row, int left,
-                                         int lane) {
-  const int tr = lane >> 2, q = lane & 3;
-  const size_t kb = row * kCodeBytes + 16 * lane;
-  const uint8_t* k = static_cast<const uint8_t*>(a.k) + kb;
-  const uint8_t* v = static_cast<const uint8_t*>(a.v) + kb;
-  const int vq = tr * kCodeBytes + 16 * (q ^ ((tr >> 1) & 2));
-  const int sr = lane & 15;
-  const uint8_t* s = (lane < 16 ? a.k_scales : a.v_scales) + (row + sr) * kRowScales;
-  if (left >= kCdTile) {
-    cp_async16(t->k + 16 * lane, k);
-    cp_async16(t->k + 16 * lane + 512, k + 512);
-    cp_async16(t->v + vq, v);
-    cp_async16(t->v + vq + 512, v + 512);
-    cp_async8_zfill(t->ks + 8 * lane, s, 8);  // (vs follows ks)
-  } else {
-    // rows past the end are not touched: their copies read nothing, from the tile's first row
-    const uint32_t lo = tr < left ? 16 : 0, hi = tr + 8 < left ? 16 : 0;
-    cp_async16_zfill(t->k + 16 * lane, lo ? k : static_cast<const uint8_t*>(a.k) + row * kCodeBytes, lo);
-    cp_async16_zfill(t->k + 16 * lane + 512,
-                     hi ? k + 512 : static_cast<const uint8_t*>(a.k) + row * kCodeBytes, hi);
-    cp_async16_zfill(t->v + vq, lo ? v : static_cast<const uint8_t*>(a.v) + row * kCodeBytes, lo);
-    cp_async16_zfill(t->v + vq + 512,
-                     hi ? v + 512 : static_cast<const uint8_t*>(a.v) + row * kCodeBytes, hi);
-    cp_async8_zfill(t->ks + 8 * lane,
-                    sr < left ? s : (lane < 16 ? a.k_scales : a.v_scales) + row * kRowScales,
-                    sr < left ? 8 : 0);
+// A lane's part of the copies of a tile: where it reads (from the tile's first row) and writes.
+struct Kv4Lane {
+  const uint8_t *k, *v, *s;  // this lane's 16 bytes of the codes, 8 of the scales, at row 0
+  uint32_t dk, dv, ds;       // the same in a Kv4Tile
+  int row, srow;             // rows they belong to (the second 16 bytes: row + 8)
+  __device__ __forceinline__ void init(const CacheDecodeArgs& a, int lane) {
+    row = lane >> 2;
+    srow = lane & 15;
+    k = static_cast<const uint8_t*>(a.k) + 16 * lane;
+    v = static_cast<const uint8_t*>(a.v) + 16 * lane;
+    s = (lane < 16 ? a.k_scales : a.v_scales) + 8 * srow;
+    dk = 16 * lane;
+    dv = 1024 + row * kCodeBytes + 16 * ((lane & 3) ^ ((row >> 1) & 2));
+    ds = 2048 + 8 * lane;
   }
-}
+  // a whole tile from row `at`
+  __device__ __forceinline__ void full(uint32_t tile, size_t at) const {
+    const uint8_t *pk = k + at * kCodeBytes, *pv = v + at * kCodeBytes, *ps = s + at * kRowScales;
+    copy16(tile + dk, pk);
+    copy16(tile + dk + 512, pk + 512);
+    copy16(tile + dv, pv);
+    copy16(tile + dv + 512, pv + 512);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tile + ds), "l"(ps) : "memory");
+  }
+  // the first `left` rows of it (0 or less: none), zeros for the others, which are not touched
+  __device__ __forceinline__ void part(uint32_t tile, size_t at, int left) const {
+    const bool lo = row < left, hi = row + 8 < left, sc = srow < left;
+    const uint8_t *pk = k + at * kCodeBytes, *pv = v + at * kCodeBytes, *ps = s + at * kRowScales;
+    zfill16(tile + dk, lo ? pk : k, lo);
+    zfill16(tile + dk + 512, hi ? pk + 512 : k, hi);
+    zfill16(tile + dv, lo ? pv : v, lo);
+    zfill16(tile + dv + 512, hi ? pv + 512 : v, hi);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tile + ds), "l"(sc ? ps : s),
+                 "r"(sc ? 8 : 0)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  }
+  static __device__ __forceinline__ void zfill16(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(read ? 16 : 0)
+                 : "memory");
+  }
+};
 
 // A scale byte as the same fp16 number twice; two bytes as a pair.
 __device__ __forceinline__ uint32_t scale_twice(uint32_t b) { return b * 0x00800080u; }
@@ -421,31 +426,45 @@ struct CdState {
   }
 };
 
-// Logits of a tile (log2 domain, rows past the end -inf), kept for the weights; then their
-// probabilities, after the maximum has followed.
-template <int G, bool KV4>
-__device__ __forceinline__ void softmax_tile(CdState& st, float (&s)[4], const float (&cs)[2], int left,
-                                             int r, int c, float* logits, float (&p)[4]) {
+// NT tiles' products -> their probabilities, after the maximum has followed. Logits (log2 domain,
+// rows past the end -inf) are kept for the weights at `logits`, which is the step's first row.
+template <int G, bool KV4, int NT>
+__device__ __forceinline__ void softmax_step(CdState& st, float (&s)[NT][4], const float (&cs)[2],
+                                             int left, int r, int c, float* logits) {
   const int ta = frag_token(r);
-  s[0] *= cs[0];
-  s[1] *= cs[1];
-  s[2] *= cs[0];
-  s[3] *= cs[1];
-  if (left < kCdTile) {
-    if (ta >= left) s[0] = s[1] = -INFINITY;
-    if (ta + 8 >= left) s[2] = s[3] = -INFINITY;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    s[n][0] *= cs[0];
+    s[n][1] *= cs[1];
+    s[n][2] *= cs[0];
+    s[n][3] *= cs[1];
+  }
+  if (left < NT * kCdTile) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (ta + 16 * n >= left) s[n][0] = s[n][1] = -INFINITY;
+      if (ta + 16 * n + 8 >= left) s[n][2] = s[n][3] = -INFINITY;
+    }
   }
   if (logits && 2 * c < G) {
     float* x = logits + ta * G + 2 * c;
-    if (G == 1) {
-      if (ta < left) x[0] = s[0];
-      if (ta + 8 < left) x[8] = s[2];
-    } else {
-      if (ta < left) *reinterpret_cast<float2*>(x) = make_float2(s[0], s[1]);
-      if (ta + 8 < left) *reinterpret_cast<float2*>(x + 8 * G) = make_float2(s[2], s[3]);
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) {  // eight rows each
+      if (ta + 8 * n < left) {
+        if (G == 1)
+          x[8 * n] = s[n >> 1][2 * (n & 1)];
+        else
+          *reinterpret_cast<float2*>(x + 8 * n * G) =
+              make_float2(s[n >> 1][2 * (n & 1)], s[n >> 1][2 * (n & 1) + 1]);
+      }
     }
   }
-  float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]);
+  float m0 = fmaxf(s[0][0], s[0][2]), m1 = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+  for (int n = 1; n < NT; ++n) {
+    m0 = fmaxf(m0, fmaxf(s[n][0], s[n][2]));
+    m1 = fmaxf(m1, fmaxf(s[n][1], s[n][3]));
+  }
   if (__any_sync(0xffffffffu, m0 > st.m[0] + kCdLazy || m1 > st.m[1] + kCdLazy)) {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
@@ -468,12 +487,15 @@ __device__ __forceinline__ void softmax_tile(CdState& st, float (&s)[4], const f
     }
   }
   const float b0 = kCdShift<KV4> - st.m[0], b1 = kCdShift<KV4> - st.m[1];
-  p[0] = fast_exp2(s[0] + b0);
-  p[1] = fast_exp2(s[1] + b1);
-  p[2] = fast_exp2(s[2] + b0);
-  p[3] = fast_exp2(s[3] + b1);
-  st.l[0] += p[0] + p[2];
-  st.l[1] += p[1] + p[3];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    s[n][0] = fast_exp2(s[n][0] + b0);
+    s[n][1] = fast_exp2(s[n][1] + b1);
+    s[n][2] = fast_exp2(s[n][2] + b0);
+    s[n][3] = fast_exp2(s[n][3] + b1);
+    st.l[0] += s[n][0] + s[n][2];
+    st.l[1] += s[n][1] + s[n][3];
+  }
 }
 
 // Length that the attention sees, and whether the step's token is appended.
@@ -538,7 +560,8 @@ struct CdMerge {
   float l[kCdWarps][8];
   float o[kCdWarps][G][kHeadDim];
 };
-constexpr size_t cd_ring_bytes(bool kv4) { return kv4 ? (size_t)kCdWarps * kCdDepth * sizeof(Kv4Tile) : 0; }
+// two steps of two tiles per warp: one read, one on its way
+constexpr size_t cd_ring_bytes(bool kv4) { return kv4 ? (size_t)kCdWarps * 4 * sizeof(Kv4Tile) : 0; }
 template <int G, bool KV4>
 constexpr size_t cd_smem_bytes() {
   return sizeof(CdMerge<G>) > cd_ring_bytes(KV4) ? sizeof(CdMerge<G>) : cd_ring_bytes(KV4);
@@ -552,7 +575,10 @@ struct CdStart {
   int u, g, round;
 };
 
-__device__ __forceinline__ int rounds_of(int L) { return (L + kCdRound - 1) / kCdRound; }
+template <bool KV4>
+__device__ __forceinline__ int rounds_of(int L) {
+  return (L + kCdRound<KV4> - 1) / kCdRound<KV4>;
+}
 
 // first round of CTA i, and the CTA that has round x
 __device__ __forceinline__ long long part_begin(const CdStart& s, int i) { return s.total * i / s.ctas; }
@@ -561,6 +587,7 @@ __device__ __forceinline__ int part_of(const CdStart& s, long long x) {
 }
 
 // Every CTA adds up the units' rounds (each thread a run of units) and finds its own part.
+template <bool KV4>
 __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* out,
                                            unsigned long long* tmp) {
   const int tid = threadIdx.x;
@@ -568,7 +595,7 @@ __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* ou
   const int u0 = min(a.n, tid * per), u1 = min(a.n, u0 + per);
   bool ap;
   unsigned long long mine = 0;
-  for (int u = u0; u < u1; ++u) mine += rounds_of(decode_length(a, u, &ap));
+  for (int u = u0; u < u1; ++u) mine += rounds_of<KV4>(decode_length(a, u, &ap));
   const unsigned long long before = block_excl_scan64(mine, tmp);
   if (tid == kCdThreads - 1) out->total = (long long)(before + mine) * a.n_kv;
   __syncthreads();
@@ -587,7 +614,7 @@ __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* ou
     long long at = (long long)before * a.n_kv;
     if (b >= at && b < at + (long long)mine * a.n_kv) {
       for (int u = u0; u < u1; ++u) {
-        const int R = rounds_of(decode_length(a, u, &ap));
+        const int R = rounds_of<KV4>(decode_length(a, u, &ap));
         const long long all = (long long)R * a.n_kv;
         if (b < at + all) {
           out->u = u;
@@ -602,7 +629,7 @@ __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* ou
   __syncthreads();
 }
 
-template <int G, bool KV4>
+template <int G, bool KV4, bool PAGED>
 __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(CacheDecodeArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ CdStart start;
@@ -617,7 +644,7 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
   bool append;
   pdl_trigger();
 
-  find_start(a, &start, scan);
+  find_start<KV4>(a, &start, scan);
   // units without tokens have no CTA of their own; bad lengths are told once
   for (int ukv = blockIdx.x; ukv < units; ukv += gridDim.x) {
     const int u = ukv / a.n_kv, L = decode_length(a, u, &append);
@@ -630,26 +657,29 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     }
   }
 
-  Kv4Tile* ring = reinterpret_cast<Kv4Tile*>(dyn) + warp * kCdDepth;
+  constexpr int kStep = kCdStep<KV4>, kRound = kCdRound<KV4>;
+  Kv4Tile* ring = reinterpret_cast<Kv4Tile*>(dyn) + warp * 4;
+  Kv4Lane my;
+  if (KV4) my.init(a, lane);
   int u = start.u, g = start.g, round = start.round;
   bool first = true;
   for (long long at = start.begin; at < start.end; first = false) {
     const int L = decode_length(a, u, &append);
-    const int R = rounds_of(L);
+    const int R = rounds_of<KV4>(L);
     if (R == 0) {  // (a unit without tokens)
       ++u;
       continue;
     }
     const int rounds = (int)min((long long)(R - round), start.end - at);
     const int ukv = u * a.n_kv + g;
-    const int tb = round * kCdRound, te = min(L, (round + rounds) * kCdRound);
+    const int tb = round * kCdRound<KV4>, te = min(L, (round + rounds) * kCdRound<KV4>);
     const bool whole = rounds == R;
 
     if (KV4 && append && round + rounds == R) {  // this segment's tokens include the new one
       if (tid < 16) {
         const bool v = tid >= 8;
         const int blk = tid & 7, row = L - 1;
-        const size_t dst = a.pm.table
+        const size_t dst = PAGED
                                ? paged_row(a.pm, paged_block(a.pm, u, row, a.status), a.n_kv, g, row)
                                : (size_t)ukv * a.cap + row;
         uint32_t w[8], sb;
@@ -663,20 +693,24 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       __syncthreads();
     }
 
-    auto row_of = [&](int t0) -> size_t {  // row of the first token of a tile (it lies in one block)
-      return a.pm.table ? paged_row(a.pm, paged_block(a.pm, u, t0, a.status), a.n_kv, g, t0)
-                        : (size_t)ukv * a.cap + t0;
+    auto row_of = [&](int t) -> size_t {  // row of the first token of a tile (it lies in one block)
+      return PAGED ? paged_row(a.pm, paged_block(a.pm, u, t, a.status), a.n_kv, g, t)
+                   : (size_t)ukv * a.cap + t;
     };
-    int t0 = tb + warp * kCdTile;
-    const int tiles = t0 < te ? (te - t0 + kCdRound - 1) / kCdRound : 0;
-    if (KV4) {
-#pragma unroll
-      for (int d = 0; d < kCdDepth - 1; ++d) {
-        const int t = t0 + d * kCdRound;
-        if (t < te) load_kv4(ring + d, a, row_of(t), te - t, lane);
-        cp_async_commit();
+    int t0 = tb + warp * kStep;
+    // the copies of the step from token t (one commit group, empty past the end)
+    auto fetch = [&](int t, int half) {
+      const uint32_t dst = smem_addr(ring + 2 * half);
+      if (te - t >= kStep) {
+        my.full(dst, row_of(t));
+        my.full(dst + sizeof(Kv4Tile), PAGED ? row_of(t + kCdTile) : row_of(t) + kCdTile);
+      } else if (t < te) {
+        my.part(dst, row_of(t), te - t);
+        my.part(dst + sizeof(Kv4Tile), te - t > kCdTile ? row_of(t + kCdTile) : 0, te - t - kCdTile);
       }
-    }
+      cp_async_commit();
+    };
+    if (KV4) fetch(t0, 0);
 
     // Q fragments: lane (r, c) holds head r. 4 bits: fp16, each head scaled by a power of two that
     // puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it is exact, and
@@ -722,35 +756,35 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     st.clear();
     float* logits = a.weights ? a.logits + ((size_t)ukv * a.cap + t0) * G : nullptr;
     if (KV4) {
-      for (int i = 0; i < tiles; ++i, t0 += kCdRound) {
-        cp_async_wait<kCdDepth - 2>();
-        __syncwarp();  // this tile has landed for every lane, and every lane is done with the last
-        const int tn = t0 + (kCdDepth - 1) * kCdRound;
-        if (tn < te) load_kv4(ring + (i + kCdDepth - 1) % kCdDepth, a, row_of(tn), te - tn, lane);
-        cp_async_commit();
-        const Kv4Tile* t = ring + i % kCdDepth;
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, p[4];
-        scores_kv4(t, reinterpret_cast<const uint2(&)[8]>(q), r, c, s);
-        softmax_tile<G, true>(st, s, cs, te - t0, r, c, logits, p);
-        if (logits) logits += kCdRound * G;
-        accumulate_kv4(t, p, r, c, st.o);
+      for (int half = 0; t0 < te; t0 += kRound, half ^= 1) {
+        cp_async_wait_all();
+        __syncwarp();  // this step has landed for every lane, and every lane is done with the last
+        fetch(t0 + kRound, half ^ 1);
+        const Kv4Tile* t = ring + 2 * half;
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        scores_kv4(t, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[0]);
+        scores_kv4(t + 1, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[1]);
+        softmax_step<G, true, 2>(st, s, cs, te - t0, r, c, logits);
+        if (logits) logits += kRound * G;
+        accumulate_kv4(t, s[0], r, c, st.o);
+        accumulate_kv4(t + 1, s[1], r, c, st.o);
       }
     } else {
       BfTile t;
-      if (tiles > 0) {
+      if (t0 < te) {
         const size_t row = row_of(t0);
         t.load_k(a, row, te - t0, r, c);
         t.load_v(a, row, te - t0, r, c);
       }
-      for (int i = 0; i < tiles; ++i, t0 += kCdRound) {
-        const int tn = t0 + kCdRound;
+      for (; t0 < te; t0 += kRound) {
+        const int tn = t0 + kRound;
         const size_t next = tn < te ? row_of(tn) : 0;
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, p[4];
-        scores_bf(t, qf + lane, s);
+        float s[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+        scores_bf(t, qf + lane, s[0]);
         if (tn < te) t.load_k(a, next, te - tn, r, c);
-        softmax_tile<G, false>(st, s, cs, te - t0, r, c, logits, p);
-        if (logits) logits += kCdRound * G;
-        accumulate_bf(t, p, st.o);
+        softmax_step<G, false, 1>(st, s, cs, te - t0, r, c, logits);
+        if (logits) logits += kRound * G;
+        accumulate_bf(t, s[0], st.o);
         if (tn < te) t.load_v(a, next, te - tn, r, c);
       }
     }
@@ -896,13 +930,13 @@ __global__ void __launch_bounds__(kCdThreads) cache_weights_kernel(CacheDecodeAr
                    min(L, t0 + kCdWeightChunk), a.lse + (size_t)ukv * G);
 }
 
-template <int G, bool KV4>
+template <int G, bool KV4, bool PAGED>
 static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
   constexpr size_t smem = cd_smem_bytes<G, KV4>();
-  cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4>, smem);
+  cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4, PAGED>, smem);
   if (e != cudaSuccess) return e;
-  cache_decode_kernel<G, KV4>
-      <<<cache_decode_ctas(a.n, a.n_kv, a.cap), kCdThreads, smem, s>>>(a);
+  cache_decode_kernel<G, KV4, PAGED>
+      <<<cache_decode_ctas(a.n, a.n_kv, a.cap, KV4), kCdThreads, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.weights || !a.weights_apart) return e;
   const int chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;
@@ -910,14 +944,20 @@ static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
                            dim3(kCdThreads), 0, s, a);
 }
 
+template <int G>
+static cudaError_t launch_kind(const CacheDecodeArgs& a, cudaStream_t s) {
+  if (!a.kv4) return launch_group<G, false, false>(a, s);
+  return a.pm.table ? launch_group<G, true, true>(a, s) : launch_group<G, true, false>(a, s);
+}
+
 cudaError_t launch_cache_decode(const CacheDecodeArgs& in, cudaStream_t s) {
   CacheDecodeArgs a = in;
   a.weights_apart = weights_apart(a.n, a.n_kv);
   switch (a.gqa) {
-    case 1: return a.kv4 ? launch_group<1, true>(a, s) : launch_group<1, false>(a, s);
-    case 2: return a.kv4 ? launch_group<2, true>(a, s) : launch_group<2, false>(a, s);
-    case 4: return a.kv4 ? launch_group<4, true>(a, s) : launch_group<4, false>(a, s);
-    case 8: return a.kv4 ? launch_group<8, true>(a, s) : launch_group<8, false>(a, s);
+    case 1: return launch_kind<1>(a, s);
+    case 2: return launch_kind<2>(a, s);
+    case 4: return launch_kind<4>(a, s);
+    case 8: return launch_kind<8>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
