@@ -132,11 +132,18 @@ template <bool KV4>
 constexpr int kCdRound = kCdStep<KV4>* kCdWarps;
 constexpr int kCdWeightChunk = 1024;          // tokens a CTA of the weights kernel takes
 
+// CTAs of a call: one per slot of the SMs. Fewer where a part would be less than kCdMinRounds
+// rounds, which is what joining parts costs (a 1021-token call: 11.0 us in four parts per KV head,
+// XX us in one); and while every (unit, KV head) can have its own, the same number for each, so that
+// parts of equal lengths end with them.
+constexpr int kCdMinRounds = 4;
 static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
   const int round = kv4 ? kCdRound<true> : kCdRound<false>;
-  const long long rounds = (long long)n * n_kv * ((cap + round - 1) / round);
+  const long long units = (long long)n * n_kv, rounds = (cap + round - 1) / round;
   const long long slots = (long long)kCdPerSm * device_sm_count();
-  return (int)(rounds < slots ? rounds : slots);
+  if (units >= slots) return (int)slots;
+  const long long most = (rounds + kCdMinRounds - 1) / kCdMinRounds, each = slots / units;
+  return (int)(units * (each < most ? each : most));
 }
 
 // Who turns logits into weights: with many (unit, KV head)s the CTA that finishes one, while others
@@ -188,14 +195,12 @@ template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   if (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -560,11 +565,17 @@ struct CdMerge {
   float l[kCdWarps][8];
   float o[kCdWarps][G][kHeadDim];
 };
-// two steps of two tiles per warp: one read, one on its way
-constexpr size_t cd_ring_bytes(bool kv4) { return kv4 ? (size_t)kCdWarps * 4 * sizeof(Kv4Tile) : 0; }
+// three steps of two tiles per warp: one read, two on their way
+constexpr int kCdRing = 3;
+constexpr size_t cd_ring_bytes(bool kv4) {
+  return kv4 ? (size_t)kCdWarps * kCdRing * 2 * sizeof(Kv4Tile) : 0;
+}
+// the ring, the warps' join and the parts' join use the same memory one after the other
 template <int G, bool KV4>
-constexpr size_t cd_smem_bytes() {
-  return sizeof(CdMerge<G>) > cd_ring_bytes(KV4) ? sizeof(CdMerge<G>) : cd_ring_bytes(KV4);
+size_t cd_smem_bytes(int ctas) {
+  const size_t join = (size_t)kCdThreads * 16 + 32 + (size_t)ctas * G * 4;
+  size_t b = sizeof(CdMerge<G>) > cd_ring_bytes(KV4) ? sizeof(CdMerge<G>) : cd_ring_bytes(KV4);
+  return b > join ? b : join;
 }
 
 // Where a CTA begins: its first round's unit, KV head and round, and how much there is in all.
@@ -591,6 +602,31 @@ template <bool KV4>
 __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* out,
                                            unsigned long long* tmp) {
   const int tid = threadIdx.x;
+  if (a.n <= 32) {  // one warp, no barrier but the last
+    if (tid < 32) {
+      bool ap;
+      const int R = tid < a.n ? rounds_of<KV4>(decode_length(a, tid, &ap)) : 0;
+      const int incl = warp_incl_scan(R);  // (32 units of at most 2^23 rounds)
+      const long long total = (long long)__shfl_sync(0xffffffffu, incl, 31) * a.n_kv;
+      const int ctas = (int)min((long long)gridDim.x, total);
+      const bool work = (int)blockIdx.x < ctas;
+      const long long b = work ? total * blockIdx.x / ctas : 0;
+      const long long at = (long long)(incl - R) * a.n_kv;
+      if (tid == 0) {
+        out->total = total;
+        out->ctas = ctas;
+        out->begin = b;
+        out->end = work ? total * (blockIdx.x + 1) / ctas : 0;
+      }
+      if (work && b >= at && b < at + (long long)R * a.n_kv) {
+        out->u = tid;
+        out->g = (int)((b - at) / R);
+        out->round = (int)((b - at) - (long long)out->g * R);
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const int per = (a.n + kCdThreads - 1) / kCdThreads;
   const int u0 = min(a.n, tid * per), u1 = min(a.n, u0 + per);
   bool ap;
@@ -658,7 +694,7 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
   }
 
   constexpr int kStep = kCdStep<KV4>, kRound = kCdRound<KV4>;
-  Kv4Tile* ring = reinterpret_cast<Kv4Tile*>(dyn) + warp * 4;
+  Kv4Tile* ring = reinterpret_cast<Kv4Tile*>(dyn) + warp * (2 * kCdRing);
   Kv4Lane my;
   if (KV4) my.init(a, lane);
   int u = start.u, g = start.g, round = start.round;
@@ -699,8 +735,8 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     };
     int t0 = tb + warp * kStep;
     // the copies of the step from token t (one commit group, empty past the end)
-    auto fetch = [&](int t, int half) {
-      const uint32_t dst = smem_addr(ring + 2 * half);
+    auto fetch = [&](int t, int place) {
+      const uint32_t dst = smem_addr(ring + 2 * place);
       if (te - t >= kStep) {
         my.full(dst, row_of(t));
         my.full(dst + sizeof(Kv4Tile), PAGED ? row_of(t + kCdTile) : row_of(t) + kCdTile);
@@ -710,7 +746,10 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       }
       cp_async_commit();
     };
-    if (KV4) fetch(t0, 0);
+    if (KV4) {
+      fetch(t0, 0);
+      fetch(t0 + kRound, 1);
+    }
 
     // Q fragments: lane (r, c) holds head r. 4 bits: fp16, each head scaled by a power of two that
     // puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it is exact, and
@@ -756,11 +795,12 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     st.clear();
     float* logits = a.weights ? a.logits + ((size_t)ukv * a.cap + t0) * G : nullptr;
     if (KV4) {
-      for (int half = 0; t0 < te; t0 += kRound, half ^= 1) {
-        cp_async_wait_all();
+      for (int place = 0; t0 < te; t0 += kRound) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();  // this step has landed for every lane, and every lane is done with the last
-        fetch(t0 + kRound, half ^ 1);
-        const Kv4Tile* t = ring + 2 * half;
+        fetch(t0 + 2 * kRound, place == 0 ? 2 : place - 1);
+        const Kv4Tile* t = ring + 2 * place;
+        place = place == kCdRing - 1 ? 0 : place + 1;
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         scores_kv4(t, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[0]);
         scores_kv4(t + 1, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[1]);
@@ -849,39 +889,62 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       if (done) {
         __threadfence();
         const size_t s0 = 2 * (size_t)i0 + (part_begin(start, i0) == z0 ? 0 : 1);
+        auto slot_of = [&](int k) { return k == 0 ? s0 : 2 * (size_t)(i0 + k); };
+        const int parts = i1 - i0 + 1;
         const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-        float* mx = reinterpret_cast<float*>(dyn);  // [8] maxima
+        float4* sums = reinterpret_cast<float4*>(dyn);                     // [kCdThreads]
+        float* total = reinterpret_cast<float*>(dyn + kCdThreads * 16);    // [8] sums of the heads
+        float* factor = total + 8;                                         // [parts][G]
         if (warp < G) {
           float M = -1e30f;
-          for (int k = i0 + lane; k <= i1; k += 32)
-            M = fmaxf(M, __ldcg(ml + (k == i0 ? s0 : 2 * (size_t)k) * G + warp).x);
+          for (int k = lane; k < parts; k += 32)
+            M = fmaxf(M, __ldcg(ml + slot_of(k) * G + warp).x);
 #pragma unroll
           for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
           float S = 0.f;
-          for (int k = i0 + lane; k <= i1; k += 32) {
-            const float2 x = __ldcg(ml + (k == i0 ? s0 : 2 * (size_t)k) * G + warp);
-            S = fmaf(x.y, fast_exp2(x.x - M), S);
+          for (int k = lane; k < parts; k += 32) {
+            const float2 x = __ldcg(ml + slot_of(k) * G + warp);
+            const float f = fast_exp2(x.x - M);
+            factor[k * G + warp] = f;
+            S = fmaf(x.y, f, S);
           }
 #pragma unroll
           for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
           if (lane == 0) {
-            mx[warp] = M;
-            mx[8 + warp] = S;
+            total[warp] = S;
             lse[warp] = neg_lse(M, S);
           }
         }
         __syncthreads();
-        for (int i = tid; i < G * kHeadDim; i += kCdThreads) {
-          const int h = i / kHeadDim;
-          const float M = mx[h], S = mx[8 + h];
-          float O = 0.f;
-#pragma unroll 4
-          for (int k = i0; k <= i1; ++k) {
-            const size_t sl = k == i0 ? s0 : 2 * (size_t)k;
-            O = fmaf(__ldcg(a.part_o + sl * G * kHeadDim + i),
-                     fast_exp2(__ldcg(ml + sl * G + h).x - M), O);
-          }
-          a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(S == 0.f ? 0.f : O / S);
+        // four outputs per thread; with fewer than eight heads the threads also share the parts
+        constexpr int kQuads = G * kHeadDim / 4, kShare = kCdThreads / kQuads;
+        const int quad = tid % kQuads, share = tid / kQuads, h = quad / (kHeadDim / 4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = share; k < parts; k += kShare) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_of(k) * G * kHeadDim) + quad);
+          const float f = factor[k * G + h];
+          o.x = fmaf(x.x, f, o.x);
+          o.y = fmaf(x.y, f, o.y);
+          o.z = fmaf(x.z, f, o.z);
+          o.w = fmaf(x.w, f, o.w);
+        }
+        if (kShare > 1) {
+          sums[tid] = o;
+          __syncthreads();
+          if (share == 0)
+            for (int e = 1; e < kShare; ++e) {
+              const float4 x = sums[e * kQuads + quad];
+              o.x += x.x;
+              o.y += x.y;
+              o.z += x.z;
+              o.w += x.w;
+            }
+        }
+        if (share == 0) {
+          const float S = total[h], inv = S == 0.f ? 0.f : 1.f / S;
+          uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          *reinterpret_cast<uint2*>(a.out + (size_t)ukv * G * kHeadDim + 4 * quad) = w;
         }
       }
     }
@@ -932,11 +995,12 @@ __global__ void __launch_bounds__(kCdThreads) cache_weights_kernel(CacheDecodeAr
 
 template <int G, bool KV4, bool PAGED>
 static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
-  constexpr size_t smem = cd_smem_bytes<G, KV4>();
+  const int ctas = cache_decode_ctas(a.n, a.n_kv, a.cap, KV4);
+  const size_t smem = cd_smem_bytes<G, KV4>(ctas);
   cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4, PAGED>, smem);
   if (e != cudaSuccess) return e;
   cache_decode_kernel<G, KV4, PAGED>
-      <<<cache_decode_ctas(a.n, a.n_kv, a.cap, KV4), kCdThreads, smem, s>>>(a);
+      <<<ctas, kCdThreads, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.weights || !a.weights_apart) return e;
   const int chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;

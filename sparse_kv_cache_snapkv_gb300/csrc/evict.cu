@@ -11,12 +11,17 @@
 
 #include "common.cuh"
 #include "rkv_internal.h"
+#include "tensor_core.cuh"
 
 namespace rkv {
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvMoveThreads = 256;
 constexpr int kEvMoveWarps = kEvMoveThreads / 32;
+// Up to this many rows a unit's keys stay in its CTA's shared memory through the select; beyond, they
+// are made again from the weights for each pass.
+constexpr int kEvSmemRows = 40960;
+constexpr int kEvBins = 2048;
 
 // free rows and kept rows past keep of one (unit, KV head); at most `most` of each
 static inline int most_moves(int cap, int keep) {
@@ -25,6 +30,7 @@ static inline int most_moves(int cap, int keep) {
 }
 
 struct EvictLists {
+  int32_t* done;   // CTAs that are through (zero between calls)
   int32_t* count;  // [n*n_kv]
   int32_t* dst;    // [n*n_kv][most]
   int32_t* src;    // [n*n_kv][most]
@@ -35,7 +41,8 @@ static EvictLists lists_of(const EvictArgs& a) {
   EvictLists l;
   const size_t units = (size_t)a.n * a.n_kv;
   l.most = most_moves(a.cap, a.keep);
-  l.count = static_cast<int32_t*>(a.scratch);
+  l.done = static_cast<int32_t*>(a.scratch);
+  l.count = l.done + 64;
   l.dst = l.count + align_up(units * 4, 256) / 4;
   l.src = l.dst + align_up(units * l.most * 4, 256) / 4;
   return l;
@@ -43,7 +50,7 @@ static EvictLists lists_of(const EvictArgs& a) {
 
 size_t evict_scratch_bytes(int n, int n_kv, int cap, int keep) {
   const size_t units = (size_t)n * n_kv;
-  return align_up(units * 4, 256) + 2 * align_up(units * most_moves(cap, keep) * 4, 256);
+  return 256 + align_up(units * 4, 256) + 2 * align_up(units * most_moves(cap, keep) * 4, 256);
 }
 
 struct EvSmem {
@@ -58,41 +65,336 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0xfffffffeu : ordered_key(w);
 }
 
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, EvictLists ls) {
-  __shared__ EvSmem sm;
-  const int ukv = blockIdx.x, u = ukv / a.n_kv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int L = a.len[u], keep = a.keep;
-  const bool bad = L < 0 || L > a.cap;
-  if (tid == 0) {
-    ls.count[ukv] = 0;
-    if (bad) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
-  }
-  if (bad) return;
-  const size_t row0 = (size_t)ukv * a.cap;
-  const float* w = a.weights + row0;
-  const int32_t* pos = a.pos + row0;
-  float* wo = a.weights_out + row0;
-  int32_t* po = a.pos_out + row0;
-  int32_t* from = a.src_rows ? a.src_rows + (size_t)ukv * keep : nullptr;
-  if (L <= keep) {
-    for (int i = tid; i < L; i += kEvThreads) {
-      wo[i] = w[i];
-      po[i] = pos[i];
-    }
-    if (from)
-      for (int i = tid; i < keep; i += kEvThreads) from[i] = i < L ? i : -1;
-    return;
-  }
-  const int seen = a.seen[u];
-  auto position = [&](int i) {
+// What a CTA needs of its (unit, KV head).
+struct EvUnit {
+  const float* w;
+  const int32_t* pos;
+  float* wo;
+  int32_t* po;
+  int32_t* from;
+  int L, keep, seen;
+  long long recent_from;
+  __device__ __forceinline__ int position(int i) const {
     const int p = pos[i];
     return p >= 0 ? p : seen - (L - i);
-  };
-  // 64-bit sums: positions and seen are the caller's, and their difference may be anything
-  auto key_of = [&](int i) {
-    return (long long)position(i) >= (long long)seen - a.recent ? 0xffffffffu : weight_key(w[i]);
-  };
+  }
+  // (64-bit: the positions and `seen` are the caller's, their difference may be anything)
+  __device__ __forceinline__ uint32_t key(int i) const {
+    return (long long)position(i) >= recent_from ? 0xffffffffu : weight_key(w[i]);
+  }
+};
+
+// The unit's arrays; false when there is nothing to evict (then everything has been done).
+__device__ __forceinline__ bool evict_unit(const EvictArgs& a, int ukv, EvUnit* x) {
+  const int u = ukv / a.n_kv, tid = threadIdx.x, nt = blockDim.x;
+  const size_t row0 = (size_t)ukv * a.cap;
+  x->L = a.len[u];
+  x->keep = a.keep;
+  x->w = a.weights + row0;
+  x->pos = a.pos + row0;
+  x->wo = a.weights_out + row0;
+  x->po = a.pos_out + row0;
+  x->from = a.src_rows ? a.src_rows + (size_t)ukv * a.keep : nullptr;
+  if (x->L < 0 || x->L > a.cap) {
+    if (tid == 0) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
+    return false;
+  }
+  if (x->L <= a.keep) {
+    for (int i = tid; i < x->L; i += nt) {
+      x->wo[i] = x->w[i];
+      x->po[i] = x->pos[i];
+    }
+    if (x->from)
+      for (int i = tid; i < a.keep; i += nt) x->from[i] = i < x->L ? i : -1;
+    return false;
+  }
+  x->seen = a.seen[u];
+  x->recent_from = (long long)x->seen - a.recent;
+  return true;
+}
+
+// Moved rows' weights and positions, and the reset of the rows past keep (after a barrier, with the
+// lists written).
+__device__ __forceinline__ void evict_finish(const EvUnit& x, const int32_t* dst, const int32_t* src,
+                                             int moves) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  for (int m = tid; m < moves; m += nt) {
+    const int d = dst[m], s = src[m];
+    const int p = x.position(s);
+    const float w = x.w[s];
+    x.wo[d] = w;
+    x.po[d] = p;
+    if (x.from) x.from[d] = s;
+  }
+  __syncthreads();
+  for (int i = x.keep + tid; i < x.L; i += nt) {
+    x.wo[i] = 0.f;
+    x.po[i] = -1;
+  }
+}
+
+// Copies moved rows: one warp takes kB rows at a time, its lanes the 16-byte words of a row of every
+// array (bf16: 16 + 16; 4 bits: 4 + 4, and the scales' 8 + 8 bytes as one word each).
+template <int kB>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int ukv, const int32_t* dst,
+                                          const int32_t* src, int first, int step, int count) {
+  const int lane = threadIdx.x & 31;
+  const bool bf = a.row_bytes[2] == 0;
+  // bf16: a lane's word is fixed; 4 bits: 10 lanes a row, three rows side by side
+  const int sub = bf ? 0 : lane / 10, l = bf ? lane : lane % 10;
+  const int side = bf ? 1 : 3;
+  int arr, off;
+  bool eight = false;
+  if (bf) {
+    arr = l >> 4;
+    off = 16 * (l & 15);
+  } else if (l < 8) {
+    arr = l >> 2;
+    off = 16 * (l & 3);
+  } else {
+    arr = l - 6;
+    off = 0;
+    eight = true;
+  }
+  if (sub >= side) return;  // (two lanes idle)
+  uint8_t* base = a.rows[arr] + (size_t)ukv * a.cap * a.row_bytes[arr] + off;
+  const int rb = a.row_bytes[arr];
+  for (int m0 = first * kB * side; m0 < count; m0 += step * kB * side) {
+    uint4 v[kB];
+#pragma unroll
+    for (int k = 0; k < kB; ++k) {
+      const int m = m0 + k * side + sub;
+      if (m < count) {
+        const uint8_t* p = base + (size_t)src[m] * rb;
+        if (eight) {
+          const uint2 y = *reinterpret_cast<const uint2*>(p);
+          v[k] = make_uint4(y.x, y.y, 0u, 0u);
+        } else {
+          v[k] = *reinterpret_cast<const uint4*>(p);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kB; ++k) {
+      const int m = m0 + k * side + sub;
+      if (m < count) {
+        uint8_t* p = base + (size_t)dst[m] * rb;
+        if (eight)
+          *reinterpret_cast<uint2*>(p) = make_uint2(v[k].x, v[k].y);
+        else
+          *reinterpret_cast<uint4*>(p) = v[k];
+      }
+    }
+  }
+}
+
+// Lengths move on when every CTA has read them (they may be their own inputs).
+__device__ __forceinline__ void evict_lengths(const EvictArgs& a, int32_t* done) {
+  __shared__ int last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(done, 1) == (int)gridDim.x - 1;
+    if (last) *done = 0;
+  }
+  __syncthreads();
+  if (last)
+    for (int u = threadIdx.x; u < a.n; u += blockDim.x) {
+      const int L = a.len[u];
+      a.len_out[u] = (L >= 0 && L <= a.cap) ? min(L, a.keep) : L;
+    }
+}
+
+struct EvDigit {
+  int wsum[32];
+  int digit, above, in_bin;
+};
+
+// Finds the bin of the `remaining`-th largest key in a histogram of kEvBins counts.
+__device__ __forceinline__ void find_digit(const uint32_t* hist, int remaining, EvDigit& d) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const int per = kEvBins / nt;  // 2 or 4 bins per thread, from the top
+  int mine = 0;
+  for (int j = 0; j < per; ++j) mine += (int)hist[kEvBins - 1 - tid * per - j];
+  const int incl_w = warp_incl_scan(mine);
+  if (lane == 31) d.wsum[warp] = incl_w;
+  __syncthreads();
+  int before = 0;
+  const int ws = lane < nw ? d.wsum[lane] : 0;
+  const int wi = warp_incl_scan(ws);
+  before = __shfl_sync(0xffffffffu, wi - ws, warp);
+  int acc = before + incl_w - mine;
+  if (acc < remaining && acc + mine >= remaining) {
+    for (int j = 0; j < per; ++j) {
+      const int b = kEvBins - 1 - tid * per - j, c = (int)hist[b];
+      if (acc + c >= remaining) {
+        d.digit = b;
+        d.above = acc;
+        d.in_bin = c;
+        break;
+      }
+      acc += c;
+    }
+  }
+  __syncthreads();
+}
+
+// Exclusive prefix sums of cnt[0..n) in place (packed counters that do not overflow); returns the sum.
+__device__ __forceinline__ uint32_t scan_counts(uint32_t* cnt, int n, uint32_t* tmp) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const int per = (n + nt - 1) / nt;
+  const int b = min(n, tid * per), e = min(n, b + per);
+  uint32_t mine = 0;
+  for (int i = b; i < e; ++i) mine += cnt[i];
+  const uint32_t incl = (uint32_t)warp_incl_scan((int)mine);
+  if (lane == 31) tmp[warp] = incl;
+  __syncthreads();
+  const uint32_t ws = lane < nw ? tmp[lane] : 0u;
+  const uint32_t wi = (uint32_t)warp_incl_scan((int)ws);
+  uint32_t at = __shfl_sync(0xffffffffu, wi - ws, warp) + incl - mine;
+  const uint32_t total = __shfl_sync(0xffffffffu, wi, 31);
+  for (int i = b; i < e; ++i) {
+    const uint32_t c = cnt[i];
+    cnt[i] = at;
+    at += c;
+  }
+  __syncthreads();
+  return total;
+}
+
+// One CTA per (unit, KV head), keys in shared memory: three histogram passes of 11, 11 and 10 bits
+// (fewer when a bin is taken whole), then the kept rows as one bit each and the lists from prefix
+// sums over groups of 32 rows. FUSED: the CTA also moves its rows.
+template <bool FUSED>
+__global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLists ls) {
+  extern __shared__ __align__(16) uint32_t ev_dyn[];
+  __shared__ uint32_t hist[kEvBins];
+  __shared__ EvDigit dg;
+  __shared__ uint32_t tmp[32];
+  const int groups_cap = (a.cap + 31) / 32;
+  uint32_t* keys = ev_dyn;                      // [cap]
+  uint32_t* cnt = keys + groups_cap * 32;       // [groups]
+  uint32_t* kept = cnt + groups_cap;            // [groups]
+  const int ukv = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+  EvUnit x;
+  pdl_trigger();
+  int moves = 0;
+  int32_t* dst = ls.dst + (size_t)ukv * ls.most;
+  int32_t* src = ls.src + (size_t)ukv * ls.most;
+  if (evict_unit(a, ukv, &x)) {
+    const int L = x.L, keep = x.keep, groups = (L + 31) / 32;
+    for (int b = tid; b < kEvBins; b += nt) hist[b] = 0;
+    __syncthreads();
+    // keys, and their top 11 bits counted
+    for (int i0 = 0; i0 < L; i0 += 4 * nt) {
+      uint32_t k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * nt + tid;
+        k[e] = i < L ? x.key(i) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * nt + tid;
+        if (i < L) {
+          keys[i] = k[e];
+          atomicAdd(&hist[k[e] >> 21], 1u);
+        }
+      }
+    }
+    __syncthreads();
+    find_digit(hist, keep, dg);
+    uint32_t prefix = (uint32_t)dg.digit << 21;
+    int remaining = keep - dg.above;
+    bool all = dg.in_bin == remaining;  // every key of the bin is kept
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      if (all) break;
+      const int shift = pass == 0 ? 10 : 0;
+      const uint32_t high = pass == 0 ? 0xffe00000u : 0xfffffc00u;
+      const uint32_t bins = pass == 0 ? 2047u : 1023u;
+      for (int b = tid; b < kEvBins; b += nt) hist[b] = 0;
+      __syncthreads();
+      for (int i = tid; i < L; i += nt) {
+        const uint32_t k = keys[i];
+        if ((k & high) == prefix) atomicAdd(&hist[(k >> shift) & bins], 1u);
+      }
+      __syncthreads();
+      find_digit(hist, remaining, dg);
+      prefix |= (uint32_t)dg.digit << shift;
+      remaining -= dg.above;
+      all = dg.in_bin == remaining;
+    }
+    // kept: key above prefix, and of those equal the first `remaining` (all: every key from prefix on)
+    const int span = (L + nt - 1) / nt * nt;
+    if (!all) {
+      for (int i = tid; i < span; i += nt) {
+        const uint32_t m = __ballot_sync(0xffffffffu, i < L && keys[i] == prefix);
+        if (lane == 0 && i < groups * 32) cnt[i >> 5] = __popc(m);
+      }
+      __syncthreads();
+      scan_counts(cnt, groups, tmp);
+    }
+    for (int i = tid; i < span; i += nt) {
+      const uint32_t k = i < L ? keys[i] : 0u;
+      bool take = i < L && (all ? k >= prefix : k > prefix);
+      if (!all) {
+        const uint32_t m = __ballot_sync(0xffffffffu, i < L && k == prefix);
+        if (i < L && k == prefix)
+          take = (int)(cnt[i >> 5] + __popc(m & ((1u << lane) - 1u))) < remaining;
+      }
+      const uint32_t t = __ballot_sync(0xffffffffu, take);
+      if (lane == 0 && i < groups * 32) kept[i >> 5] = t;
+    }
+    __syncthreads();
+    for (int g = tid; g < groups; g += nt) {
+      const int r0 = g * 32;
+      const uint32_t low = r0 + 32 <= keep ? 0xffffffffu : (r0 >= keep ? 0u : (1u << (keep - r0)) - 1u);
+      const uint32_t t = kept[g];
+      cnt[g] = __popc(~t & low) | (__popc(t & ~low) << 16);  // (at most kEvSmemRows / 2 of each)
+    }
+    __syncthreads();
+    moves = (int)(scan_counts(cnt, groups, tmp) & 0xffffu);
+    for (int i = tid; i < L; i += nt) {
+      const int g = i >> 5, r0 = g * 32, b = i & 31;
+      const uint32_t low = r0 + 32 <= keep ? 0xffffffffu : (r0 >= keep ? 0u : (1u << (keep - r0)) - 1u);
+      const uint32_t t = kept[g], under = (1u << b) - 1u;
+      const bool k = (t >> b) & 1u;
+      if (i < keep) {
+        if (!k) {
+          dst[(cnt[g] & 0xffffu) + __popc(~t & low & under)] = i;
+        } else {
+          if (x.from) x.from[i] = i;
+          const int q = x.pos[i];
+          if (x.wo != x.w) x.wo[i] = x.w[i];
+          if (x.po != x.pos || q < 0) x.po[i] = q >= 0 ? q : x.seen - (L - i);
+        }
+      } else if (k) {
+        src[(cnt[g] >> 16) + __popc(t & ~low & under)] = i;
+      }
+    }
+    __syncthreads();
+    if (FUSED) move_rows<4>(a, ukv, dst, src, tid >> 5, nt >> 5, moves);
+    evict_finish(x, dst, src, moves);
+  }
+  if (!FUSED && tid == 0) ls.count[ukv] = moves;
+  if (FUSED) evict_lengths(a, ls.done);
+}
+
+// The same for units of more rows than shared memory holds: 8 bits at a time, the keys made again for
+// each pass, the lists 1024 rows at a time.
+__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, EvictLists ls) {
+  __shared__ EvSmem sm;
+  const int ukv = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  EvUnit x;
+  pdl_trigger();
+  if (!evict_unit(a, ukv, &x)) {
+    if (tid == 0) ls.count[ukv] = 0;
+    return;
+  }
+  const int L = x.L, keep = x.keep;
+  auto key_of = [&](int i) { return x.key(i); };
   // the keep-th largest key, 8 bits at a time
   uint32_t prefix = 0, mask = 0;
   int remaining = keep;
@@ -141,20 +443,20 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
     const bool kept = i < L && (k > prefix || (eq && eq_before + (int)e < remaining));
     const bool hole = i < keep && !kept;
     const bool mover = i >= keep && kept;
-    const unsigned long long x =
+    const unsigned long long y =
         block_excl_scan64((hole ? 1ull : 0ull) | (mover ? 1ull << 32 : 0ull), sm.tmp);
-    if (hole) dst[free_before + (int)(x & 0xffffffffull)] = i;
-    if (mover) src[past_before + (int)(x >> 32)] = i;
+    if (hole) dst[free_before + (int)(y & 0xffffffffull)] = i;
+    if (mover) src[past_before + (int)(y >> 32)] = i;
     if (tid == kEvThreads - 1) {
-      sm.base[0] = (int)(x & 0xffffffffull) + (hole ? 1 : 0);
-      sm.base[1] = (int)(x >> 32) + (mover ? 1 : 0);
+      sm.base[0] = (int)(y & 0xffffffffull) + (hole ? 1 : 0);
+      sm.base[1] = (int)(y >> 32) + (mover ? 1 : 0);
       sm.in_bin = (int)e + (eq ? 1 : 0);
     }
     if (kept && i < keep) {
-      if (from) from[i] = i;
-      const int p = position(i);
-      wo[i] = w[i];
-      po[i] = p;
+      if (x.from) x.from[i] = i;
+      const int p = x.position(i);
+      x.wo[i] = x.w[i];
+      x.po[i] = p;
     }
     __syncthreads();
     free_before += sm.base[0];
@@ -162,53 +464,51 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
     eq_before += sm.in_bin;
     __syncthreads();
   }
-  for (int m = tid; m < past_before; m += kEvThreads) {
-    const int d = dst[m], s = src[m];
-    const int p = position(s);
-    const float x = w[s];
-    wo[d] = x;
-    po[d] = p;
-    if (from) from[d] = s;
-  }
-  __syncthreads();
-  for (int i = keep + tid; i < L; i += kEvThreads) {
-    wo[i] = 0.f;
-    po[i] = -1;
-  }
+  evict_finish(x, dst, src, past_before);
   if (tid == 0) ls.count[ukv] = past_before;
 }
 
-// One warp per moved row; the lanes split its bytes in words of 8.
+// The moves of all (unit, KV head)s over the whole GPU.
 __global__ void __launch_bounds__(kEvMoveThreads) evict_move_kernel(EvictArgs a, EvictLists ls) {
+  pdl_wait();
   const int ukv = blockIdx.x, u = ukv / a.n_kv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.y == 0 && ukv == u * a.n_kv && threadIdx.x == 0) {
     const int L = a.len[u];
     a.len_out[u] = (L >= 0 && L <= a.cap) ? min(L, a.keep) : L;
   }
-  const int count = ls.count[ukv];
-  const int32_t* dst = ls.dst + (size_t)ukv * ls.most;
-  const int32_t* src = ls.src + (size_t)ukv * ls.most;
-  for (int m = blockIdx.y * kEvMoveWarps + warp; m < count; m += gridDim.y * kEvMoveWarps) {
-    const size_t d = (size_t)ukv * a.cap + dst[m], s = (size_t)ukv * a.cap + src[m];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (lane * 8 < a.row_bytes[k])
-        *reinterpret_cast<uint2*>(a.rows[k] + d * a.row_bytes[k] + lane * 8) =
-            *reinterpret_cast<const uint2*>(a.rows[k] + s * a.row_bytes[k] + lane * 8);
-    }
-  }
+  move_rows<4>(a, ukv, ls.dst + (size_t)ukv * ls.most, ls.src + (size_t)ukv * ls.most,
+               blockIdx.y * kEvMoveWarps + (threadIdx.x >> 5), gridDim.y * kEvMoveWarps,
+               ls.count[ukv]);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const EvictLists ls = lists_of(a);
-  evict_select_kernel<<<a.n * a.n_kv, kEvThreads, 0, s>>>(a, ls);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  int y = (ls.most + 4 * kEvMoveWarps - 1) / (4 * kEvMoveWarps);
+  const int units = a.n * a.n_kv;
+  cudaError_t e;
+  // With a CTA for every SM, each moves its own rows; fewer leave that to a second kernel.
+  const bool fused = a.cap <= kEvSmemRows && units >= device_sm_count();
+  if (a.cap <= kEvSmemRows) {
+    const int groups = (a.cap + 31) / 32;
+    const size_t smem = (size_t)groups * (32 + 2) * 4;
+    const int threads = a.cap <= 8192 ? 512 : kEvThreads;
+    if (fused) {
+      e = ensure_dyn_smem((const void*)evict_kernel<true>, smem);
+      if (e != cudaSuccess) return e;
+      evict_kernel<true><<<units, threads, smem, s>>>(a, ls);
+    } else {
+      e = ensure_dyn_smem((const void*)evict_kernel<false>, smem);
+      if (e != cudaSuccess) return e;
+      evict_kernel<false><<<units, threads, smem, s>>>(a, ls);
+    }
+  } else {
+    evict_select_kernel<<<units, kEvThreads, 0, s>>>(a, ls);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess || fused) return e;
+  const int rows = 4 * kEvMoveWarps * (a.row_bytes[2] ? 3 : 1);  // of a CTA at a time
+  int y = (ls.most + rows - 1) / rows;
   y = y < 1 ? 1 : (y > 1024 ? 1024 : y);
-  evict_move_kernel<<<dim3(a.n * a.n_kv, y), kEvMoveThreads, 0, s>>>(a, ls);
-  return cudaGetLastError();
+  return launch_pdl_kernel(evict_move_kernel, dim3(units, y), dim3(kEvMoveThreads), 0, s, a, ls);
 }
 
 }  // namespace rkv

@@ -490,6 +490,40 @@ def test_evict(rkv, n, n_kv, cap, lens, keep, recent, ties, kv4):
                     assert torch.equal(now[u, g, m:].view(torch.uint8), was[u, g, m:].view(torch.uint8))
 
 
+@pytest.mark.parametrize("n,n_kv,cap,lens,keep,recent", [
+    (40, 8, 300, [300 - 7 * u for u in range(40)], 100, 20),   # a CTA of its own for every SM
+    (1, 2, 45000, [45000], 20000, 100),                        # more rows than shared memory holds
+    (1, 1, 40960, [40959], 33, 32),
+    (2, 1, 9000, [9000, 8999], 8998, 0),
+])
+@pytest.mark.parametrize("kv4", [False, True])
+def test_evict_many_and_long(rkv, n, n_kv, cap, lens, keep, recent, kv4):
+    w, pos = _evict_case(n, n_kv, cap, lens, keep, 125)
+    w[:, :, ::3] = w[:, :, :1]  # many equal weights
+    seen = [t + 50 for t in lens]
+    cache = (_filled_cache(rkv, n, n_kv, cap, 126) if kv4 else
+             [_normal(127, n, n_kv, cap, D), _normal(128, n, n_kv, cap, D)])
+    rows = [x.clone() for x in cache]
+    length, win, pin = _ints(lens), w.clone(), pos.clone()
+    src = torch.full((n, n_kv, keep), -9, dtype=I32, device="cuda")
+    call = rkv.rkv_evict_kv4 if kv4 else rkv.rkv_evict
+    rkv.rkv_check_status(call(*rows, length, win, pin, _ints(seen), keep, recent, length, win, pin,
+                              src_rows=src))
+    assert length.tolist() == [min(t, keep) for t in lens]
+    for u, t in enumerate(lens):
+        m = min(t, keep)
+        for g in range(n_kv):
+            want, at = C.evict(_f64(w[u, g, :t]), _np(pos[u, g, :t]), seen[u], keep, recent)
+            assert np.array_equal(_np(src[u, g, :m]), want)
+            ix = torch.tensor(want, device="cuda", dtype=torch.long)
+            assert torch.equal(win[u, g, :m], w[u, g, ix])
+            assert np.array_equal(_np(pin[u, g, :m]), at)
+            assert (win[u, g, m:t] == 0).all() and (pin[u, g, m:t] == -1).all()
+            for now, was in zip(rows, cache):
+                assert torch.equal(now[u, g, :m].view(torch.uint8), was[u, g, ix].view(torch.uint8))
+                assert torch.equal(now[u, g, m:].view(torch.uint8), was[u, g, m:].view(torch.uint8))
+
+
 def test_evict_special_weights(rkv):
     """Zeros of either sign tie, infinities and NaN are largest, the newest rows come first."""
     w = torch.tensor([0.0, -0.0, float("nan"), 1.0, float("inf"), 2.0, 0.0, 0.0], device="cuda").view(1, 1, 8)
