@@ -58,6 +58,8 @@ __device__ __forceinline__ int append_count(const Kv4AppendArgs& a, int u, int* 
 // One thread = one block of 16 values (32 bytes in, 8 + 1 out); blockIdx.y: K or V. Bound by the
 // copy: 8 neighbouring threads make one row of codes and one of scales.
 __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArgs a) {
+  pdl_wait();
+  pdl_trigger();
   const long long item = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
   const long long row = item >> 3;
   const int blk = (int)(item & 7);
@@ -93,6 +95,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArg
 }
 
 __global__ void kv4_length_kernel(Kv4AppendArgs a) {
+  pdl_wait();
+  pdl_trigger();
   const int u = blockIdx.x * blockDim.x + threadIdx.x;
   if (u >= a.n) return;
   int have;
@@ -104,11 +108,10 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
   const long long items = (long long)a.n * a.n_kv * a.max_new * kRowScales;
   const long long ctas = (items + kAppendThreads - 1) / kAppendThreads;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  kv4_append_kernel<<<dim3((unsigned)ctas, 2), kAppendThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl_kernel(kv4_append_kernel, dim3((unsigned)ctas, 2),
+                                          dim3(kAppendThreads), 0, s, a);
   if (e != cudaSuccess || a.len_out != a.len) return e;
-  kv4_length_kernel<<<(a.n + 255) / 256, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl_kernel(kv4_length_kernel, dim3((a.n + 255) / 256), dim3(256), 0, s, a);
 }
 
 // ==========================================================================================
@@ -132,18 +135,16 @@ template <bool KV4>
 constexpr int kCdRound = kCdStep<KV4>* kCdWarps;
 constexpr int kCdWeightChunk = 1024;          // tokens a CTA of the weights kernel takes
 
-// CTAs of a call: one per slot of the SMs. Fewer where a part would be less than kCdMinRounds
-// rounds, which is what joining parts costs (a 1021-token call: 11.0 us in four parts per KV head,
-// XX us in one); and while every (unit, KV head) can have its own, the same number for each, so that
-// parts of equal lengths end with them.
-constexpr int kCdMinRounds = 4;
+// CTAs of a call: one per slot of the SMs; where that leaves a part fewer than kCdMinRounds rounds,
+// the same number for each (unit, KV head), so that parts of equal lengths end with them.
+constexpr int kCdMinRounds = 2;
 static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
   const int round = kv4 ? kCdRound<true> : kCdRound<false>;
   const long long units = (long long)n * n_kv, rounds = (cap + round - 1) / round;
   const long long slots = (long long)kCdPerSm * device_sm_count();
-  if (units >= slots) return (int)slots;
-  const long long most = (rounds + kCdMinRounds - 1) / kCdMinRounds, each = slots / units;
-  return (int)(units * (each < most ? each : most));
+  if (units * rounds >= slots * kCdMinRounds || units >= slots) return (int)slots;
+  const long long each = slots / units;
+  return (int)(units * (each < rounds ? each : rounds));
 }
 
 // Who turns logits into weights: with many (unit, KV head)s the CTA that finishes one, while others
@@ -250,9 +251,9 @@ struct Kv4Lane {
     dv = 1024 + row * kCodeBytes + 16 * ((lane & 3) ^ ((row >> 1) & 2));
     ds = 2048 + 8 * lane;
   }
-  // a whole tile from row `at`
-  __device__ __forceinline__ void full(uint32_t tile, size_t at) const {
-    const uint8_t *pk = k + at * kCodeBytes, *pv = v + at * kCodeBytes, *ps = s + at * kRowScales;
+  // a whole tile; pk, pv, ps: k, v and s moved to its first row
+  __device__ __forceinline__ void full(uint32_t tile, const uint8_t* pk, const uint8_t* pv,
+                                       const uint8_t* ps) const {
     copy16(tile + dk, pk);
     copy16(tile + dk + 512, pk + 512);
     copy16(tile + dv, pv);
@@ -565,8 +566,9 @@ struct CdMerge {
   float l[kCdWarps][8];
   float o[kCdWarps][G][kHeadDim];
 };
-// three steps of two tiles per warp: one read, two on their way
-constexpr int kCdRing = 3;
+// two steps of two tiles per warp: one read, one on its way (a third step in flight took 1 to 8 %
+// longer)
+constexpr int kCdRing = 2;
 constexpr size_t cd_ring_bytes(bool kv4) {
   return kv4 ? (size_t)kCdWarps * kCdRing * 2 * sizeof(Kv4Tile) : 0;
 }
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
   const int r = lane >> 2, c = lane & 3;
   const int units = a.n * a.n_kv;
   bool append;
-  pdl_trigger();
+  pdl_wait();
 
   find_start<KV4>(a, &start, scan);
   // units without tokens have no CTA of their own; bad lengths are told once
@@ -734,22 +736,36 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
                    : (size_t)ukv * a.cap + t;
     };
     int t0 = tb + warp * kStep;
+    // (contiguous: addresses of the next step's first row)
+    const uint8_t* pk = my.k + ((size_t)ukv * a.cap + t0) * kCodeBytes;
+    const uint8_t* pv = my.v + ((size_t)ukv * a.cap + t0) * kCodeBytes;
+    const uint8_t* ps = my.s + ((size_t)ukv * a.cap + t0) * kRowScales;
     // the copies of the step from token t (one commit group, empty past the end)
     auto fetch = [&](int t, int place) {
       const uint32_t dst = smem_addr(ring + 2 * place);
       if (te - t >= kStep) {
-        my.full(dst, row_of(t));
-        my.full(dst + sizeof(Kv4Tile), PAGED ? row_of(t + kCdTile) : row_of(t) + kCdTile);
+        if (PAGED) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const size_t row = row_of(t + h * kCdTile);
+            my.full(dst + h * sizeof(Kv4Tile), my.k + row * kCodeBytes, my.v + row * kCodeBytes,
+                    my.s + row * kRowScales);
+          }
+        } else {
+          my.full(dst, pk, pv, ps);
+          my.full(dst + sizeof(Kv4Tile), pk + kCdTile * kCodeBytes, pv + kCdTile * kCodeBytes,
+                  ps + kCdTile * kRowScales);
+          pk += kRound * kCodeBytes;
+          pv += kRound * kCodeBytes;
+          ps += kRound * kRowScales;
+        }
       } else if (t < te) {
         my.part(dst, row_of(t), te - t);
         my.part(dst + sizeof(Kv4Tile), te - t > kCdTile ? row_of(t + kCdTile) : 0, te - t - kCdTile);
       }
       cp_async_commit();
     };
-    if (KV4) {
-      fetch(t0, 0);
-      fetch(t0 + kRound, 1);
-    }
+    if (KV4) fetch(t0, 0);
 
     // Q fragments: lane (r, c) holds head r. 4 bits: fp16, each head scaled by a power of two that
     // puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it is exact, and
@@ -796,11 +812,11 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     float* logits = a.weights ? a.logits + ((size_t)ukv * a.cap + t0) * G : nullptr;
     if (KV4) {
       for (int place = 0; t0 < te; t0 += kRound) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        cp_async_wait_all();
         __syncwarp();  // this step has landed for every lane, and every lane is done with the last
-        fetch(t0 + 2 * kRound, place == 0 ? 2 : place - 1);
+        fetch(t0 + kRound, place ^ 1);
         const Kv4Tile* t = ring + 2 * place;
-        place = place == kCdRing - 1 ? 0 : place + 1;
+        place ^= 1;
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         scores_kv4(t, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[0]);
         scores_kv4(t + 1, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[1]);
@@ -965,6 +981,9 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     }
   }
 
+  // (a launch that follows may take this CTA's place from here; from the start, its CTAs did so unevenly
+  // and a 245 us call took 263)
+  pdl_trigger();
   // the lengths move on when every CTA has read them (they may be their own inputs)
   if (a.len_out) {
     __syncthreads();
@@ -999,9 +1018,7 @@ static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
   const size_t smem = cd_smem_bytes<G, KV4>(ctas);
   cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4, PAGED>, smem);
   if (e != cudaSuccess) return e;
-  cache_decode_kernel<G, KV4, PAGED>
-      <<<ctas, kCdThreads, smem, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_pdl_kernel(cache_decode_kernel<G, KV4, PAGED>, dim3(ctas), dim3(kCdThreads), smem, s, a);
   if (e != cudaSuccess || !a.weights || !a.weights_apart) return e;
   const int chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;
   return launch_pdl_kernel(cache_weights_kernel<G>, dim3(a.n * a.n_kv, chunks < 4096 ? chunks : 4096),

@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
   uint32_t* kept = cnt + groups_cap;            // [groups]
   const int ukv = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   EvUnit x;
+  pdl_wait();
   pdl_trigger();
   int moves = 0;
   int32_t* dst = ls.dst + (size_t)ukv * ls.most;
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
   const int ukv = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   EvUnit x;
+  pdl_wait();
   pdl_trigger();
   if (!evict_unit(a, ukv, &x)) {
     if (tid == 0) ls.count[ukv] = 0;
@@ -494,16 +496,15 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
     if (fused) {
       e = ensure_dyn_smem((const void*)evict_kernel<true>, smem);
       if (e != cudaSuccess) return e;
-      evict_kernel<true><<<units, threads, smem, s>>>(a, ls);
+      e = launch_pdl_kernel(evict_kernel<true>, dim3(units), dim3(threads), smem, s, a, ls);
     } else {
       e = ensure_dyn_smem((const void*)evict_kernel<false>, smem);
       if (e != cudaSuccess) return e;
-      evict_kernel<false><<<units, threads, smem, s>>>(a, ls);
+      e = launch_pdl_kernel(evict_kernel<false>, dim3(units), dim3(threads), smem, s, a, ls);
     }
   } else {
-    evict_select_kernel<<<units, kEvThreads, 0, s>>>(a, ls);
+    e = launch_pdl_kernel(evict_select_kernel, dim3(units), dim3(kEvThreads), 0, s, a, ls);
   }
-  e = cudaGetLastError();
   if (e != cudaSuccess || fused) return e;
   const int rows = 4 * kEvMoveWarps * (a.row_bytes[2] ? 3 : 1);  // of a CTA at a time
   int y = (ls.most + rows - 1) / rows;
