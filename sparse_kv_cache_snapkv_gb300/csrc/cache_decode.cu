@@ -147,11 +147,6 @@ static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
   return (int)(units * (each < rounds ? each : rounds));
 }
 
-// Who turns logits into weights: with many (unit, KV head)s the CTA that finishes one, while others
-// still stream (its logits are then in L2); with few, whose last CTA would be alone with a long
-// sequence, a second kernel over all SMs.
-static bool weights_apart(int n, int n_kv) { return (long long)n * n_kv * 2 < device_sm_count(); }
-
 struct CacheScratch {
   size_t counters, lse, part_ml, part_o, logits, total;
 };
@@ -407,10 +402,12 @@ __device__ __forceinline__ void accumulate_bf(const BfTile& t, const float (&p)[
   }
 }
 
-// Dimension of row r (hi: r + 8) of the j-th 16-high step of O^T.
+// A (unit, KV head)'s outputs are joined in the order of the fragments: output i is head i % G and
+// dimension out_dim(i / G). i / G = 8 (2 j + hi) + r for row r (hi: r + 8) of O^T's j-th step.
 template <bool KV4>
-__device__ __forceinline__ int out_dim(int j, int r, int hi) {
-  return KV4 ? 16 * r + 2 * j + hi : 64 * (j >> 2) + 8 * r + 2 * (j & 3) + hi;
+__device__ __forceinline__ int out_dim(int x) {
+  const int jh = x >> 3, r = x & 7;
+  return KV4 ? 16 * r + jh : 64 * (jh >> 3) + 8 * r + (jh & 7);
 }
 
 // The running maximum follows the true one only when that has grown by more than 2^kCdLazy, so
@@ -560,25 +557,28 @@ __device__ __forceinline__ void add_weights(const float* logits, float* weights,
   }
 }
 
-template <int G>
+// Joining the warps: their O^T fragments as they are (row (j, e), lane), padded so that neither the
+// lanes' stores nor the reads meet in a bank more than twice.
+constexpr int kCdORow = 34;
 struct CdMerge {
   float m[kCdWarps][8];
   float l[kCdWarps][8];
-  float o[kCdWarps][G][kHeadDim];
+  float o[kCdWarps][32 * kCdORow];
+};
+// Joining the parts; the factors of more parts than this are made again for each output.
+constexpr int kCdFactors = 512;
+struct CdJoin {
+  float4 sums[kCdThreads];
+  float total[8], top[8];  // sums and maxima of the heads
+  float factor[kCdFactors * 8];
 };
 // two steps of two tiles per warp: one read, one on its way (a third step in flight took 1 to 8 %
 // longer)
 constexpr int kCdRing = 2;
-constexpr size_t cd_ring_bytes(bool kv4) {
-  return kv4 ? (size_t)kCdWarps * kCdRing * 2 * sizeof(Kv4Tile) : 0;
-}
 // the ring, the warps' join and the parts' join use the same memory one after the other
-template <int G, bool KV4>
-size_t cd_smem_bytes(int ctas) {
-  const size_t join = (size_t)kCdThreads * 16 + 32 + (size_t)ctas * G * 4;
-  size_t b = sizeof(CdMerge<G>) > cd_ring_bytes(KV4) ? sizeof(CdMerge<G>) : cd_ring_bytes(KV4);
-  return b > join ? b : join;
-}
+template <bool KV4>
+constexpr size_t kCdSmemBytes = KV4 ? (size_t)kCdWarps * kCdRing * 2 * sizeof(Kv4Tile) : sizeof(CdMerge);
+static_assert(kCdSmemBytes<true> >= sizeof(CdMerge) && sizeof(CdMerge) >= sizeof(CdJoin), "sizes");
 
 // Where a CTA begins: its first round's unit, KV head and round, and how much there is in all.
 struct CdStart {
@@ -675,7 +675,8 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
   __shared__ uint2 qf[KV4 ? 1 : 8 * 32];
   __shared__ float lse[8];
   __shared__ int flag;
-  CdMerge<G>& mg = *reinterpret_cast<CdMerge<G>*>(dyn);
+  CdMerge& mg = *reinterpret_cast<CdMerge*>(dyn);
+  CdJoin& jn = *reinterpret_cast<CdJoin*>(dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
   const int units = a.n * a.n_kv;
@@ -683,18 +684,6 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
   pdl_wait();
 
   find_start<KV4>(a, &start, scan);
-  // units without tokens have no CTA of their own; bad lengths are told once
-  for (int ukv = blockIdx.x; ukv < units; ukv += gridDim.x) {
-    const int u = ukv / a.n_kv, L = decode_length(a, u, &append);
-    if (L == 0)
-      for (int i = tid; i < G * kHeadDim; i += kCdThreads)
-        a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(0.f);
-    if (tid == 0 && ukv == u * a.n_kv) {
-      const int l = a.len[u];
-      if (l < 0 || l > a.cap || (a.new_k && !append)) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
-    }
-  }
-
   constexpr int kStep = kCdStep<KV4>, kRound = kCdRound<KV4>;
   Kv4Tile* ring = reinterpret_cast<Kv4Tile*>(dyn) + warp * (2 * kCdRing);
   Kv4Lane my;
@@ -851,7 +840,7 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], d);
       st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], d);
     }
-    __syncthreads();  // the ring is the merge area's memory
+    __syncthreads();  // the join's memory is the ring's
     if (r == 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -862,30 +851,40 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int h = 2 * c + (e & 1);
-        if (h < G) mg.o[warp][h][out_dim<KV4>(j, r, e >> 1)] = st.o[j][e];
-      }
+      for (int e = 0; e < 4; ++e) mg.o[warp][(4 * j + e) * kCdORow + lane] = st.o[j][e];
     __syncthreads();
     const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
-    for (int i = tid; i < G * kHeadDim; i += kCdThreads) {
-      const int h = i / kHeadDim, d = i % kHeadDim;
-      float M = -1e30f, S = 0.f, O = 0.f;
+    {
+      // a thread's outputs all belong to one head
+      const int h = tid % G;
+      float f[kCdWarps], M = -1e30f, S = 0.f;
 #pragma unroll
       for (int w = 0; w < kCdWarps; ++w) M = fmaxf(M, mg.m[w][h]);
 #pragma unroll
       for (int w = 0; w < kCdWarps; ++w) {
-        const float f = fast_exp2(mg.m[w][h] - M);
-        S = fmaf(mg.l[w][h], f, S);
-        O = fmaf(mg.o[w][h][d], f, O);
+        f[w] = fast_exp2(mg.m[w][h] - M);
+        S = fmaf(mg.l[w][h], f[w], S);
       }
       M -= kCdShift<KV4>;  // p was 2^(s - m + shift)
-      if (whole) {
-        a.out[((size_t)ukv * G + h) * kHeadDim + d] = __float2bfloat16_rn(S == 0.f ? 0.f : O / S);
-        if (d == 0) lse[h] = neg_lse(M, S);
-      } else {
-        a.part_o[(slot * G + h) * kHeadDim + d] = O;
-        if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(M, S);
+      const float inv = S == 0.f ? 0.f : 1.f / S;
+#pragma unroll
+      for (int i0 = 0; i0 < G * kHeadDim; i0 += kCdThreads) {
+        const int i = i0 + tid, x = i / G, jh = x >> 3, row = x & 7;
+        if (G * kHeadDim % kCdThreads != 0 && i >= G * kHeadDim) break;
+        const int at = (2 * jh + (h & 1)) * kCdORow + 4 * row + (h >> 1);  // 4 j + e, e = 2 hi + h % 2
+        float O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kCdWarps; ++w) O = fmaf(mg.o[w][at], f[w], O);
+        if (whole)
+          a.out[((size_t)ukv * G + h) * kHeadDim + out_dim<KV4>(x)] = __float2bfloat16_rn(O * inv);
+        else
+          a.part_o[slot * G * kHeadDim + i] = O;
+      }
+      if (tid < G) {
+        if (whole)
+          lse[tid] = neg_lse(M, S);
+        else
+          reinterpret_cast<float2*>(a.part_ml)[slot * G + tid] = make_float2(M, S);
       }
     }
 
@@ -908,9 +907,6 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
         auto slot_of = [&](int k) { return k == 0 ? s0 : 2 * (size_t)(i0 + k); };
         const int parts = i1 - i0 + 1;
         const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-        float4* sums = reinterpret_cast<float4*>(dyn);                     // [kCdThreads]
-        float* total = reinterpret_cast<float*>(dyn + kCdThreads * 16);    // [8] sums of the heads
-        float* factor = total + 8;                                         // [parts][G]
         if (warp < G) {
           float M = -1e30f;
           for (int k = lane; k < parts; k += 32)
@@ -921,36 +917,43 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
           for (int k = lane; k < parts; k += 32) {
             const float2 x = __ldcg(ml + slot_of(k) * G + warp);
             const float f = fast_exp2(x.x - M);
-            factor[k * G + warp] = f;
+            if (k < kCdFactors) jn.factor[k * G + warp] = f;
             S = fmaf(x.y, f, S);
           }
 #pragma unroll
           for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
           if (lane == 0) {
-            total[warp] = S;
+            jn.total[warp] = S;
+            jn.top[warp] = M;
             lse[warp] = neg_lse(M, S);
           }
         }
         __syncthreads();
         // four outputs per thread; with fewer than eight heads the threads also share the parts
         constexpr int kQuads = G * kHeadDim / 4, kShare = kCdThreads / kQuads;
-        const int quad = tid % kQuads, share = tid / kQuads, h = quad / (kHeadDim / 4);
+        const int quad = tid % kQuads, share = tid / kQuads;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int k = share; k < parts; k += kShare) {
           const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_of(k) * G * kHeadDim) + quad);
-          const float f = factor[k * G + h];
-          o.x = fmaf(x.x, f, o.x);
-          o.y = fmaf(x.y, f, o.y);
-          o.z = fmaf(x.z, f, o.z);
-          o.w = fmaf(x.w, f, o.w);
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int h = (4 * quad + e) % G;
+            f[e] = k < kCdFactors ? jn.factor[k * G + h]
+                                  : fast_exp2(__ldcg(ml + slot_of(k) * G + h).x - jn.top[h]);
+          }
+          o.x = fmaf(x.x, f[0], o.x);
+          o.y = fmaf(x.y, f[1], o.y);
+          o.z = fmaf(x.z, f[2], o.z);
+          o.w = fmaf(x.w, f[3], o.w);
         }
         if (kShare > 1) {
-          sums[tid] = o;
+          jn.sums[tid] = o;
           __syncthreads();
           if (share == 0)
             for (int e = 1; e < kShare; ++e) {
-              const float4 x = sums[e * kQuads + quad];
+              const float4 x = jn.sums[e * kQuads + quad];
               o.x += x.x;
               o.y += x.y;
               o.z += x.z;
@@ -958,26 +961,37 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
             }
         }
         if (share == 0) {
-          const float S = total[h], inv = S == 0.f ? 0.f : 1.f / S;
-          uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-          *reinterpret_cast<uint2*>(a.out + (size_t)ukv * G * kHeadDim + 4 * quad) = w;
+          const float y[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * quad + e, h = i % G;
+            const float S = jn.total[h];
+            a.out[((size_t)ukv * G + h) * kHeadDim + out_dim<KV4>(i / G)] =
+                __float2bfloat16_rn(S == 0.f ? 0.f : y[e] / S);
+          }
         }
       }
     }
-    if (done && a.weights) {
-      __syncthreads();
-      if (a.weights_apart) {
-        if (tid < G) a.lse[(size_t)ukv * G + tid] = lse[tid];
-      } else {
-        add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, 0, L, lse);
-      }
-    }
+    __syncthreads();  // (lse is written)
+    if (done && a.weights && tid < G) a.lse[(size_t)ukv * G + tid] = lse[tid];
     __syncthreads();  // shared memory is used again
     at += rounds;
     round = 0;
     if (++g == a.n_kv) {
       g = 0;
       ++u;
+    }
+  }
+
+  // units without tokens have no CTA of their own; bad lengths are told once
+  for (int ukv = blockIdx.x; ukv < units; ukv += gridDim.x) {
+    const int u = ukv / a.n_kv, L = decode_length(a, u, &append);
+    if (L == 0)
+      for (int i = tid; i < G * kHeadDim; i += kCdThreads)
+        a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(0.f);
+    if (tid == 0 && ukv == u * a.n_kv) {
+      const int l = a.len[u];
+      if (l < 0 || l > a.cap || (a.new_k && !append)) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
     }
   }
 
@@ -1001,7 +1015,9 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
   }
 }
 
-// Weights of a few long (unit, KV head)s, kCdWeightChunk tokens per CTA.
+// Weights from the logits and the joined sums, kCdWeightChunk tokens per CTA. A kernel of its own: done
+// by the CTA that finishes a (unit, KV head), the 32 units of 32K took 251 us instead of 238, the ragged
+// bf16 batch 259 instead of 241.
 template <int G>
 __global__ void __launch_bounds__(kCdThreads) cache_weights_kernel(CacheDecodeArgs a) {
   pdl_wait();
@@ -1015,11 +1031,11 @@ __global__ void __launch_bounds__(kCdThreads) cache_weights_kernel(CacheDecodeAr
 template <int G, bool KV4, bool PAGED>
 static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
   const int ctas = cache_decode_ctas(a.n, a.n_kv, a.cap, KV4);
-  const size_t smem = cd_smem_bytes<G, KV4>(ctas);
+  constexpr size_t smem = kCdSmemBytes<KV4>;
   cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4, PAGED>, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl_kernel(cache_decode_kernel<G, KV4, PAGED>, dim3(ctas), dim3(kCdThreads), smem, s, a);
-  if (e != cudaSuccess || !a.weights || !a.weights_apart) return e;
+  if (e != cudaSuccess || !a.weights) return e;
   const int chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;
   return launch_pdl_kernel(cache_weights_kernel<G>, dim3(a.n * a.n_kv, chunks < 4096 ? chunks : 4096),
                            dim3(kCdThreads), 0, s, a);
@@ -1031,9 +1047,7 @@ static cudaError_t launch_kind(const CacheDecodeArgs& a, cudaStream_t s) {
   return a.pm.table ? launch_group<G, true, true>(a, s) : launch_group<G, true, false>(a, s);
 }
 
-cudaError_t launch_cache_decode(const CacheDecodeArgs& in, cudaStream_t s) {
-  CacheDecodeArgs a = in;
-  a.weights_apart = weights_apart(a.n, a.n_kv);
+cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t s) {
   switch (a.gqa) {
     case 1: return launch_kind<1>(a, s);
     case 2: return launch_kind<2>(a, s);

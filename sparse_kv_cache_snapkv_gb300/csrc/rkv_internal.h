@@ -238,7 +238,7 @@ struct CacheDecodeArgs {
   float* part_o;       // workspace [2 per CTA][gqa][128]
   float* logits;       // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
   uint32_t* status;
-  bool kv4, weights_apart;
+  bool kv4;
 };
 size_t cache_decode_scratch_bytes(int n, int n_kv, int gqa, int cap, bool with_weights);
 // places the workspace's parts in the scratch area (after the status word)
