@@ -174,7 +174,8 @@ __device__ __forceinline__ int step_tile(const PromptParams& p, const PromptItem
   return h * m2.per_head + it.q0 + (step - h * it.span);
 }
 
-template <int PASS>
+// HEADS: a tile's query rows are of one head (row_map's per_head is not 0).
+template <int PASS, bool HEADS>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap qmap, PromptParams p) {
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     // what the second half hands to the first, one item after the other
     float2* xch = reinterpret_cast<float2*>(smem + PrSmem::nl_off);  // (pass 1: no log-sum-exps)
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    int step = 0;
+    int step = 0, nslot = 0;
+    uint32_t nphase = 0;
     for (int w = 0; w * gridDim.x < items; ++w) {
       const int i = wave_item(w);
       if (i >= items) continue;
@@ -365,52 +367,64 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int qi = tile_query(m1, it.tile, kPrStat, srow);
         const int lim = (qi >= 0 && qi < it.T) ? it.L - it.T + qi : -1;  // last visible key
         float m = -1e30f, l = 0.f;
-        for (int t = 0; t < it.count; ++t, ++step) {
-          const int b = step & 1;
-          if (aborted) continue;
-          if (!mbar_wait(&tfull[b], (uint32_t)((step >> 1) & 1))) {
-            aborted = true;
-            continue;
+        // one half of the columns after the other, the second's load under the first's work
+        uint32_t r[2][32];
+        auto chunk = [&](uint32_t (&x)[32], int key0) {
+          if (__any_sync(0xffffffffu, key0 + 31 > lim)) {  // (no divergence at the loads)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (key0 + j > lim) x[j] = 0xff800000u;
           }
-          tc_fence_after();
-          const int k0 = (it.first + t) * kPrTile + c0;
-          const uint32_t ta = tmem + lane_addr + (uint32_t)(b * 2 * kPrTile);
-          uint32_t r[2][32];
-          tmem_ld32_start(ta, r[0]);
-          tmem_ld_wait(r[0]);
-          tmem_ld32_start(ta + 32, r[1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) {
-              tmem_ld_wait(r[1]);
-              tc_fence_before();  // the accumulator is free once both halves are in registers
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&tempty[b]);
-            }
-            if (__any_sync(0xffffffffu, k0 + 32 * h + 31 > lim)) {  // (no divergence at the loads)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (k0 + 32 * h + j > lim) r[h][j] = 0xff800000u;
-            }
-            float mt[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mt[j] = __uint_as_float(r[h][j]);
-#pragma unroll
-            for (int j = 4; j < 32; ++j) mt[j & 3] = fmaxf(mt[j & 3], __uint_as_float(r[h][j]));
-            const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * p.scale_log2;
-            const float mn = fmaxf(m, top);
-            const uint64_t off = pack2(-mn, -mn);
+          // Terms relative to a reference m that need not be the maximum: it is set by the first
+          // keys, and again by a chunk whose terms come out huge. So most chunks look for no
+          // maximum; a sum stays below 2^60 of its reference, far inside fp32.
+          float sum;
+          auto terms = [&]() {
+            const uint64_t off = pack2(-m, -m);
             uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               const float2 y = unpack2(
-                  fma2(pack2(__uint_as_float(r[h][j]), __uint_as_float(r[h][j + 1])), scale2, off));
+                  fma2(pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale2, off));
               acc[(j >> 1) & 1] = add2(acc[(j >> 1) & 1], pack2(fast_exp2(y.x), fast_exp2(y.y)));
             }
             const float2 s = unpack2(add2(acc[0], acc[1]));
-            l = l * fast_exp2(m - mn) + (s.x + s.y);
+            sum = s.x + s.y;
+          };
+          terms();
+          if (__any_sync(0xffffffffu, !(sum < 1.152921504606847e18f))) {  // 2^60; NaN too
+            float mt[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+#pragma unroll
+            for (int j = 2; j < 32; ++j) mt[j & 1] = fmaxf(mt[j & 1], __uint_as_float(x[j]));
+            const float mn = fmaxf(m, fmaxf(mt[0], mt[1]) * p.scale_log2);
+            l *= fast_exp2(m - mn);
             m = mn;
+            terms();
           }
+          l += sum;
+        };
+        // waits for a tile's product and starts its first half (started under the half before it,
+        // instead of after that, the loads made the 8K prompt take 513 us instead of 447)
+        auto start_tile = [&](int st) {
+          if (!mbar_wait(&tfull[st & 1], (uint32_t)((st >> 1) & 1))) {
+            aborted = true;
+            return false;
+          }
+          tc_fence_after();
+          tmem_ld32_start(tmem + lane_addr + (uint32_t)((st & 1) * 2 * kPrTile), r[0]);
+          return true;
+        };
+        for (int t = 0; t < it.count; ++t, ++step) {
+          if (aborted || !start_tile(step)) continue;
+          const int b = step & 1, k0 = (it.first + t) * kPrTile + c0;
+          tmem_ld_wait(r[0]);
+          tmem_ld32_start(tmem + lane_addr + (uint32_t)(b * 2 * kPrTile) + 32, r[1]);
+          chunk(r[0], k0);
+          tmem_ld_wait(r[1]);
+          tc_fence_before();  // the accumulator is free once both halves are in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[b]);
+          chunk(r[1], k0 + 32);
         }
         if (hf == 1) xch[srow] = make_float2(m, l);
         named_bar_sync(1, kPrEpi);
@@ -432,61 +446,77 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       } else {
         const int key = it.tile * kPrStat + srow;
         uint64_t acc[2] = {0ull, 0ull};
-        for (int t = 0; t < it.count; ++t, ++step) {
-          const int b = step & 1, ns = step % kPrNlSlots;
-          if (aborted) continue;
-          if (!mbar_wait(&tfull[b], (uint32_t)((step >> 1) & 1)) ||
-              !mbar_wait(&nfull[ns], (uint32_t)((step / kPrNlSlots) & 1))) {
+        uint32_t r[2][32];
+        auto chunk = [&](uint32_t (&x)[32], int tile, bool mask, int base, const float* nl) {
+          if (mask) {
+            // row j of this half is query q + j of its head (wrapping at max_q where the rows run
+            // through the heads), and sees this key from query `from` on
+            const int from = key - (it.L - it.T);
+            uint32_t sees;  // a bit for each row
+            if (HEADS) {
+              const int q = tile * kPrTile + base, b0 = from - q, b1 = it.T - q;
+              sees = b0 >= 32 ? 0u : (0xffffffffu << max(b0, 0));
+              sees &= b1 >= 32 ? 0xffffffffu : (b1 <= 0 ? 0u : (1u << b1) - 1u);
+            } else {
+              const int row = tile * kPrTile + base, rows = p.gqa * p.max_q;
+              int q = row % p.max_q;
+              sees = 0u;
+              for (int j = 0; j < 32; ++j) {
+                if (q >= from && q < it.T && row + j < rows) sees |= 1u << j;
+                q = q + 1 == p.max_q ? 0 : q + 1;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((sees >> j) & 1u)) x[j] = 0xff800000u;
+          }
+          const ulonglong2* n2 = reinterpret_cast<const ulonglong2*>(nl + base);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const ulonglong2 v = n2[j];  // negated log-sum-exps of four rows
+            const float2 y0 = unpack2(fma2(pack2(__uint_as_float(x[4 * j]),
+                                                 __uint_as_float(x[4 * j + 1])), scale2, v.x));
+            const float2 y1 = unpack2(fma2(pack2(__uint_as_float(x[4 * j + 2]),
+                                                 __uint_as_float(x[4 * j + 3])), scale2, v.y));
+            acc[0] = add2(acc[0], pack2(fast_exp2(y0.x), fast_exp2(y0.y)));
+            acc[1] = add2(acc[1], pack2(fast_exp2(y1.x), fast_exp2(y1.y)));
+          }
+        };
+        // waits for a tile's product and starts its first half
+        auto start_tile = [&](int st) {
+          if (!mbar_wait(&tfull[st & 1], (uint32_t)((st >> 1) & 1))) {
+            aborted = true;
+            return false;
+          }
+          tc_fence_after();
+          tmem_ld32_start(tmem + lane_addr + (uint32_t)((st & 1) * 2 * kPrTile), r[0]);
+          return true;
+        };
+        // the streamed tile: its number within its head (or among all rows' tiles), counted along
+        int ti = HEADS ? it.q0 + it.first % max(it.span, 1) : it.first;
+        for (int t = 0; t < it.count; ++t, ++step, ++ti) {
+          if (HEADS && ti == it.q0 + it.span) ti = it.q0;
+          if (aborted || !start_tile(step)) continue;
+          if (!mbar_wait(&nfull[nslot], nphase)) {
             aborted = true;
             continue;
           }
-          tc_fence_after();
-          // a tile with rows that are no queries, or that do not see all of the stationary keys
-          const int x = step_tile(p, it, it.first + t);
-          int lo, hi;
-          tile_span(m2, x, kPrTile, &lo, &hi);
-          const bool mask = hi >= it.T || tile_query(m2, x, kPrTile, kPrTile - 1) < 0 ||
-                            it.L - it.T + lo < (it.tile + 1) * kPrStat - 1;
-          const uint32_t ta = tmem + lane_addr + (uint32_t)(b * 2 * kPrTile);
-          uint32_t r[2][32];
-          tmem_ld32_start(ta, r[0]);
-          tmem_ld_wait(r[0]);
-          tmem_ld32_start(ta + 32, r[1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) tmem_ld_wait(r[1]);
-            if (mask) {
-              // row j of this half is query q + j of its head (wrapping at max_q where the rows run
-              // through the heads), and sees this key from query `from` on
-              const int base = c0 + 32 * h, from = key - (it.L - it.T);
-              if (m2.per_head) {
-                const int q = (x % m2.per_head) * kPrTile + base;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (q + j < from || q + j >= it.T) r[h][j] = 0xff800000u;
-              } else {
-                const int row = x * kPrTile + base, rows = p.gqa * p.max_q;
-                int q = row % p.max_q;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  if (q < from || q >= it.T || row + j >= rows) r[h][j] = 0xff800000u;
-                  q = q + 1 == p.max_q ? 0 : q + 1;
-                }
-              }
-            }
-            const ulonglong2* n2 =
-                reinterpret_cast<const ulonglong2*>(nl_s + ns * kPrTile + c0 + 32 * h);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const ulonglong2 v = n2[j];  // negated log-sum-exps of four rows
-              const float2 y0 = unpack2(fma2(pack2(__uint_as_float(r[h][4 * j]),
-                                                   __uint_as_float(r[h][4 * j + 1])), scale2, v.x));
-              const float2 y1 = unpack2(fma2(pack2(__uint_as_float(r[h][4 * j + 2]),
-                                                   __uint_as_float(r[h][4 * j + 3])), scale2, v.y));
-              acc[0] = add2(acc[0], pack2(fast_exp2(y0.x), fast_exp2(y0.y)));
-              acc[1] = add2(acc[1], pack2(fast_exp2(y1.x), fast_exp2(y1.y)));
-            }
+          const float* nl = nl_s + nslot * kPrTile;
+          if (++nslot == kPrNlSlots) {
+            nslot = 0;
+            nphase ^= 1u;
           }
+          const int b = step & 1;
+          // a tile with rows that are no queries, or that do not see all of the stationary keys
+          const int x = ti;
+          const int last = HEADS ? ti * kPrTile + kPrTile : p.max_q;  // queries below `last`
+          const bool mask = last > it.T || (!HEADS && ti * kPrTile + kPrTile > p.gqa * p.max_q) ||
+                            it.L - it.T + (HEADS ? ti * kPrTile : 0) < (it.tile + 1) * kPrStat - 1;
+          tmem_ld_wait(r[0]);
+          tmem_ld32_start(tmem + lane_addr + (uint32_t)(b * 2 * kPrTile) + 32, r[1]);
+          chunk(r[0], x, mask, c0, nl);
+          tmem_ld_wait(r[1]);
+          chunk(r[1], x, mask, c0 + 32, nl);
           // (the log-sum-exps are read before this too: their slot is free with the accumulator)
           tc_fence_before();
           __syncwarp();
@@ -558,15 +588,16 @@ static PromptPlan prompt_plan(int n, int n_kv, int gqa, int max_q, int max_len) 
   const int sms = device_sm_count();
   p.tiles1 = row_tiles(row_map(gqa, max_q, kPrStat), kPrStat);
   p.tiles2 = (max_len + kPrStat - 1) / kPrStat;
-  auto splits = [](long long items, long long target, int steps) {
-    const long long want = target / items, most = (steps + 3) / 4;  // at least 4 steps a split
-    return (int)(want < 1 ? 1 : (want < most ? want : most));
+  auto splits = [](long long items, long long target, int most) {
+    const long long want = target / items;
+    return (int)(want < 1 ? 1 : (want < most ? want : (most < 1 ? 1 : most)));
   };
-  p.nsplit1 = splits(units * p.tiles1, sms, (max_len + kPrTile - 1) / kPrTile);
+  const int steps1 = (max_len + kPrTile - 1) / kPrTile;
   const int steps2 = row_tiles(row_map(gqa, max_q, kPrTile), kPrTile);
-  const long long items2 = units * p.tiles2;
-  p.nsplit2 = items2 < sms ? splits(items2, sms, steps2)
-                           : splits(items2, 4LL * sms, steps2 > 64 ? steps2 : 1);
+  p.nsplit1 = splits(units * p.tiles1, sms, (steps1 + 3) / 4);
+  const int fill = splits(units * p.tiles2, sms, (steps2 + 3) / 4);         // an item for every SM
+  const int even = splits(units * p.tiles2, 4LL * sms, steps2 / 32);        // of at least 32 steps
+  p.nsplit2 = fill > even ? fill : even;
   return p;
 }
 
@@ -584,16 +615,16 @@ size_t prompt_scratch_bytes(int n, int n_kv, int gqa, int max_q, int max_len) {
          (p.nsplit2 > 1 ? align_up(units * p.nsplit2 * max_len * 4, 256) : 0);
 }
 
-template <int PASS>
+template <int PASS, bool HEADS>
 static cudaError_t launch_prompt_pass(const CUtensorMap& km, const CUtensorMap& qm,
                                       const PromptParams& p, cudaStream_t s) {
-  cudaError_t e = ensure_dyn_smem((const void*)prompt_kernel<PASS>, PrSmem::total);
+  cudaError_t e = ensure_dyn_smem((const void*)prompt_kernel<PASS, HEADS>, PrSmem::total);
   if (e != cudaSuccess) return e;
   const long long items =
       (long long)p.units * (PASS == 1 ? p.tiles1 * p.nsplit1 : p.tiles2 * p.nsplit2);
   if (items > 0x3fffffffll) return cudaErrorInvalidConfiguration;
   const int sms = device_sm_count();
-  return launch_pdl_kernel(prompt_kernel<PASS>, dim3((unsigned)(items < sms ? items : sms)),
+  return launch_pdl_kernel(prompt_kernel<PASS, HEADS>, dim3((unsigned)(items < sms ? items : sms)),
                            dim3(kPrThreads), PrSmem::total, s, km, qm, p);
 }
 
@@ -623,13 +654,15 @@ cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s) {
   p.part = reinterpret_cast<float*>(w + ml_bytes(pl, p.units));
   p.weights = a.weights;
   p.status = a.status;
-  cudaError_t e = launch_prompt_pass<1>(km, qm, p, s);
+  const bool heads = row_map(a.gqa, a.max_q, kPrTile).per_head != 0;
+  cudaError_t e = heads ? launch_prompt_pass<1, true>(km, qm, p, s)
+                        : launch_prompt_pass<1, false>(km, qm, p, s);
   if (e != cudaSuccess) return e;
   if (p.nsplit1 > 1) {
     e = launch_pdl_kernel(prompt_lse_kernel, dim3(p.units, p.tiles1), dim3(256), 0, s, p);
     if (e != cudaSuccess) return e;
   }
-  e = launch_prompt_pass<2>(km, qm, p, s);
+  e = heads ? launch_prompt_pass<2, true>(km, qm, p, s) : launch_prompt_pass<2, false>(km, qm, p, s);
   if (e != cudaSuccess || p.nsplit2 == 1) return e;
   int y = (a.max_len + 255) / 256;
   return launch_pdl_kernel(prompt_sum_kernel, dim3(p.units, y < 1024 ? y : 1024), dim3(256), 0, s,
