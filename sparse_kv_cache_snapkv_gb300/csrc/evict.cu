@@ -21,6 +21,7 @@ constexpr int kEvMoveWarps = kEvMoveThreads / 32;
 // Up to this many rows a unit's keys stay in its CTA's shared memory through the select; beyond, they
 // are made again from the weights for each pass.
 constexpr int kEvSmemRows = 40960;
+constexpr int kEvHeldRows = 8192;  // up to this many, their weights and positions too (two CTAs per SM)
 constexpr int kEvBins = 2048;
 
 // free rows and kept rows past keep of one (unit, KV head); at most `most` of each
@@ -114,14 +115,15 @@ __device__ __forceinline__ bool evict_unit(const EvictArgs& a, int ukv, EvUnit* 
 }
 
 // Moved rows' weights and positions, and the reset of the rows past keep (after a barrier, with the
-// lists written).
+// lists written). weight_of, position_of: of a row as it was.
+template <typename W, typename P>
 __device__ __forceinline__ void evict_finish(const EvUnit& x, const int32_t* dst, const int32_t* src,
-                                             int moves) {
+                                             int moves, W weight_of, P position_of) {
   const int tid = threadIdx.x, nt = blockDim.x;
   for (int m = tid; m < moves; m += nt) {
     const int d = dst[m], s = src[m];
-    const int p = x.position(s);
-    const float w = x.w[s];
+    const int p = position_of(s);
+    const float w = weight_of(s);
     x.wo[d] = w;
     x.po[d] = p;
     if (x.from) x.from[d] = s;
@@ -264,8 +266,9 @@ __device__ __forceinline__ uint32_t scan_counts(uint32_t* cnt, int n, uint32_t* 
 
 // One CTA per (unit, KV head), keys in shared memory: three histogram passes of 11, 11 and 10 bits
 // (fewer when a bin is taken whole), then the kept rows as one bit each and the lists from prefix
-// sums over groups of 32 rows. FUSED: the CTA also moves its rows.
-template <bool FUSED>
+// sums over groups of 32 rows. The lists take the keys' place. FUSED: the CTA also moves its rows.
+// HELD: the weights and positions stay in shared memory too.
+template <bool FUSED, bool HELD>
 __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLists ls) {
   extern __shared__ __align__(16) uint32_t ev_dyn[];
   __shared__ uint32_t hist[kEvBins];
@@ -275,31 +278,49 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
   uint32_t* keys = ev_dyn;                      // [cap]
   uint32_t* cnt = keys + groups_cap * 32;       // [groups]
   uint32_t* kept = cnt + groups_cap;            // [groups]
+  float* held_w = reinterpret_cast<float*>(kept + groups_cap);          // HELD: [cap]
+  int32_t* held_p = reinterpret_cast<int32_t*>(held_w + groups_cap * 32);  // HELD: [cap], as they were
   const int ukv = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   EvUnit x;
   pdl_wait();
   pdl_trigger();
   int moves = 0;
-  int32_t* dst = ls.dst + (size_t)ukv * ls.most;
-  int32_t* src = ls.src + (size_t)ukv * ls.most;
+  int32_t* dst = reinterpret_cast<int32_t*>(keys);
+  int32_t* src = dst + ls.most;  // (2 most <= cap)
   if (evict_unit(a, ukv, &x)) {
     const int L = x.L, keep = x.keep, groups = (L + 31) / 32;
+    auto weight_of = [&](int i) { return HELD ? held_w[i] : x.w[i]; };
+    auto position_of = [&](int i) {
+      const int q = HELD ? held_p[i] : x.pos[i];
+      return q >= 0 ? q : x.seen - (L - i);
+    };
     for (int b = tid; b < kEvBins; b += nt) hist[b] = 0;
     __syncthreads();
     // keys, and their top 11 bits counted
-    for (int i0 = 0; i0 < L; i0 += 4 * nt) {
-      uint32_t k[4];
+    constexpr int kU = 8;  // rows in flight per thread
+    for (int i0 = 0; i0 < L; i0 += kU * nt) {
+      float w[kU];
+      int q[kU];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e * nt + tid;
-        k[e] = i < L ? x.key(i) : 0u;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kU; ++e) {
         const int i = i0 + e * nt + tid;
         if (i < L) {
-          keys[i] = k[e];
-          atomicAdd(&hist[k[e] >> 21], 1u);
+          w[e] = x.w[i];
+          q[e] = x.pos[i];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kU; ++e) {
+        const int i = i0 + e * nt + tid;
+        if (i < L) {
+          if (HELD) {
+            held_w[i] = w[e];
+            held_p[i] = q[e];
+          }
+          const int at = q[e] >= 0 ? q[e] : x.seen - (L - i);
+          const uint32_t k = (long long)at >= x.recent_from ? 0xffffffffu : weight_key(w[e]);
+          keys[i] = k;
+          atomicAdd(&hist[k >> 21], 1u);
         }
       }
     }
@@ -356,6 +377,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
     }
     __syncthreads();
     moves = (int)(scan_counts(cnt, groups, tmp) & 0xffffu);
+    // (the keys are done with: their memory takes the lists)
+#pragma unroll 4
     for (int i = tid; i < L; i += nt) {
       const int g = i >> 5, r0 = g * 32, b = i & 31;
       const uint32_t low = r0 + 32 <= keep ? 0xffffffffu : (r0 >= keep ? 0u : (1u << (keep - r0)) - 1u);
@@ -363,20 +386,24 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
       const bool k = (t >> b) & 1u;
       if (i < keep) {
         if (!k) {
-          dst[(cnt[g] & 0xffffu) + __popc(~t & low & under)] = i;
+          const int m = (int)(cnt[g] & 0xffffu) + __popc(~t & low & under);
+          dst[m] = i;
+          if (!FUSED) ls.dst[(size_t)ukv * ls.most + m] = i;
         } else {
           if (x.from) x.from[i] = i;
-          const int q = x.pos[i];
-          if (x.wo != x.w) x.wo[i] = x.w[i];
+          if (x.wo != x.w) x.wo[i] = weight_of(i);
+          const int q = HELD ? held_p[i] : x.pos[i];
           if (x.po != x.pos || q < 0) x.po[i] = q >= 0 ? q : x.seen - (L - i);
         }
       } else if (k) {
-        src[(cnt[g] >> 16) + __popc(t & ~low & under)] = i;
+        const int m = (int)(cnt[g] >> 16) + __popc(t & ~low & under);
+        src[m] = i;
+        if (!FUSED) ls.src[(size_t)ukv * ls.most + m] = i;
       }
     }
     __syncthreads();
-    if (FUSED) move_rows<4>(a, ukv, dst, src, tid >> 5, nt >> 5, moves);
-    evict_finish(x, dst, src, moves);
+    if (FUSED) move_rows<8>(a, ukv, dst, src, tid >> 5, nt >> 5, moves);
+    evict_finish(x, dst, src, moves, weight_of, position_of);
   }
   if (!FUSED && tid == 0) ls.count[ukv] = moves;
   if (FUSED) evict_lengths(a, ls.done);
@@ -466,7 +493,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
     eq_before += sm.in_bin;
     __syncthreads();
   }
-  evict_finish(x, dst, src, past_before);
+  evict_finish(x, dst, src, past_before, [&](int i) { return x.w[i]; }, [&](int i) { return x.position(i); });
   if (tid == 0) ls.count[ukv] = past_before;
 }
 
@@ -490,18 +517,19 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   // With a CTA for every SM, each moves its own rows; fewer leave that to a second kernel.
   const bool fused = a.cap <= kEvSmemRows && units >= device_sm_count();
   if (a.cap <= kEvSmemRows) {
-    const int groups = (a.cap + 31) / 32;
-    const size_t smem = (size_t)groups * (32 + 2) * 4;
-    const int threads = a.cap <= 8192 ? 512 : kEvThreads;
-    if (fused) {
-      e = ensure_dyn_smem((const void*)evict_kernel<true>, smem);
-      if (e != cudaSuccess) return e;
-      e = launch_pdl_kernel(evict_kernel<true>, dim3(units), dim3(threads), smem, s, a, ls);
-    } else {
-      e = ensure_dyn_smem((const void*)evict_kernel<false>, smem);
-      if (e != cudaSuccess) return e;
-      e = launch_pdl_kernel(evict_kernel<false>, dim3(units), dim3(threads), smem, s, a, ls);
-    }
+    const size_t groups = (a.cap + 31) / 32;
+    const bool held = a.cap <= kEvHeldRows;
+    const size_t smem = groups * (32 + 2 + (held ? 64 : 0)) * 4;
+    const int threads = held ? 512 : kEvThreads;
+    auto launch = [&](auto kern) {
+      const cudaError_t r = ensure_dyn_smem((const void*)kern, smem);
+      return r != cudaSuccess ? r
+                              : launch_pdl_kernel(kern, dim3(units), dim3(threads), smem, s, a, ls);
+    };
+    if (fused)
+      e = held ? launch(evict_kernel<true, true>) : launch(evict_kernel<true, false>);
+    else
+      e = held ? launch(evict_kernel<false, true>) : launch(evict_kernel<false, false>);
   } else {
     e = launch_pdl_kernel(evict_select_kernel, dim3(units), dim3(kEvThreads), 0, s, a, ls);
   }
