@@ -117,12 +117,13 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
 // ==========================================================================================
 // decode
 // ==========================================================================================
-// The work of a call is the sequence of all (unit, KV head)s' rounds of 128 tokens; CTA i of C
+// The work of a call is the sequence of all (unit, KV head)s' rounds of kCdRound tokens; CTA i of C
 // takes the i-th of C equal parts of it, whatever the lengths are. A part is a run of segments, each
 // within one (unit, KV head); only its first and its last can be shared with other CTAs, so two
-// slots of partial results per CTA are enough. The CTA that finishes a (unit, KV head) last (a
-// counter in the workspace, back at zero afterwards) joins the parts in their order: no second
-// launch, and no result depends on the order in which CTAs end.
+// slots of partial results per CTA are enough. A second kernel joins the parts in their order, turns
+// the logits into weights and moves the lengths on, after every reader; nothing in the workspace has
+// to hold anything before a call. (A CTA that came last at a counter could join in place: 32 units of
+// 32K with weights took 242 us so, 231 as here, and the counters had to be zero before a call.)
 constexpr int kCdThreads = 256;
 constexpr int kCdWarps = kCdThreads / 32;
 constexpr int kCdTile = 16;                   // tokens of a fragment tile
@@ -133,7 +134,8 @@ template <bool KV4>
 constexpr int kCdStep = KV4 ? 2 * kCdTile : kCdTile;
 template <bool KV4>
 constexpr int kCdRound = kCdStep<KV4>* kCdWarps;
-constexpr int kCdWeightChunk = 1024;          // tokens a CTA of the weights kernel takes
+constexpr int kCdWeightChunk = 1024;          // tokens that a CTA turns into weights at a time
+constexpr int kCdWeightCtasPerSm = 8;
 
 // CTAs of a call: one per slot of the SMs; where that leaves a part fewer than kCdMinRounds rounds,
 // the same number for each (unit, KV head), so that parts of equal lengths end with them.
@@ -148,14 +150,14 @@ static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
 }
 
 struct CacheScratch {
-  size_t counters, lse, part_ml, part_o, logits, total;
+  size_t units, lse, part_ml, part_o, logits, total;
 };
 static CacheScratch cache_scratch(int n, int n_kv, int gqa, int cap, bool with_weights) {
   const size_t units = (size_t)n * n_kv;
   const size_t slots = 2 * (size_t)cache_decode_ctas(n, n_kv, cap, false);  // (never fewer than 4 bits')
   CacheScratch c;
-  c.counters = 0;
-  c.lse = align_up((units + 1) * 4, 256);
+  c.units = 0;
+  c.lse = align_up(((size_t)n + 1) * sizeof(CdUnit), 256);
   c.part_ml = c.lse + align_up(units * gqa * 4, 256);
   c.part_o = c.part_ml + align_up(slots * gqa * 8, 256);
   c.logits = c.part_o + align_up(slots * gqa * kHeadDim * 4, 256);
@@ -170,7 +172,7 @@ size_t cache_decode_scratch_bytes(int n, int n_kv, int gqa, int cap, bool with_w
 void cache_decode_carve(CacheDecodeArgs* a, void* scratch) {
   unsigned char* p = static_cast<unsigned char*>(scratch);
   const CacheScratch c = cache_scratch(a->n, a->n_kv, a->gqa, a->cap, a->weights != nullptr);
-  a->counters = reinterpret_cast<int32_t*>(p + c.counters);
+  a->unit = reinterpret_cast<CdUnit*>(p + c.units);
   a->lse = reinterpret_cast<float*>(p + c.lse);
   a->part_ml = reinterpret_cast<float*>(p + c.part_ml);
   a->part_o = reinterpret_cast<float*>(p + c.part_o);
@@ -508,6 +510,12 @@ __device__ __forceinline__ int decode_length(const CacheDecodeArgs& a, int u, bo
   return *append ? l + 1 : max(0, min(l, a.cap));
 }
 
+__device__ __forceinline__ CdUnit unit_of(const CacheDecodeArgs& a, int u, long long at) {
+  bool append;
+  const int l = a.len[u], L = decode_length(a, u, &append);
+  return CdUnit{at, L, append ? l + 1 : l, l < 0 || l > a.cap || (a.new_k && !append), 0};
+}
+
 // -(m + log2 l), to be added to a logit (log2 domain) of the same head; no tokens: no weight
 __device__ __forceinline__ float neg_lse(float m, float l) {
   return l > 0.f ? -(m + log2f(l)) : (l == 0.f ? -INFINITY : l);
@@ -565,20 +573,13 @@ struct CdMerge {
   float l[kCdWarps][8];
   float o[kCdWarps][32 * kCdORow];
 };
-// Joining the parts; the factors of more parts than this are made again for each output.
-constexpr int kCdFactors = 512;
-struct CdJoin {
-  float4 sums[kCdThreads];
-  float total[8], top[8];  // sums and maxima of the heads
-  float factor[kCdFactors * 8];
-};
-// two steps of two tiles per warp: one read, one on its way (a third step in flight took 1 to 8 %
-// longer)
+// two steps of two tiles per warp: one read, one on its way (a third step in flight: 32 units of 32K
+// 243 us instead of 231)
 constexpr int kCdRing = 2;
-// the ring, the warps' join and the parts' join use the same memory one after the other
+// the ring and the warps' join use the same memory one after the other
 template <bool KV4>
 constexpr size_t kCdSmemBytes = KV4 ? (size_t)kCdWarps * kCdRing * 2 * sizeof(Kv4Tile) : sizeof(CdMerge);
-static_assert(kCdSmemBytes<true> >= sizeof(CdMerge) && sizeof(CdMerge) >= sizeof(CdJoin), "sizes");
+static_assert(kCdSmemBytes<true> >= sizeof(CdMerge), "the warps' join fits in the ring");
 
 // Where a CTA begins: its first round's unit, KV head and round, and how much there is in all.
 struct CdStart {
@@ -593,13 +594,16 @@ __device__ __forceinline__ int rounds_of(int L) {
   return (L + kCdRound<KV4> - 1) / kCdRound<KV4>;
 }
 
-// first round of CTA i, and the CTA that has round x
-__device__ __forceinline__ long long part_begin(const CdStart& s, int i) { return s.total * i / s.ctas; }
-__device__ __forceinline__ int part_of(const CdStart& s, long long x) {
-  return (int)(((x + 1) * s.ctas - 1) / s.total);
+// first round of CTA i of `ctas`, and the CTA that has round x
+__device__ __forceinline__ long long part_begin(long long total, int ctas, int i) {
+  return total * i / ctas;
+}
+__device__ __forceinline__ int part_of(long long total, int ctas, long long x) {
+  return (int)(((x + 1) * ctas - 1) / total);
 }
 
-// Every CTA adds up the units' rounds (each thread a run of units) and finds its own part.
+// Every CTA adds up the units' rounds (each thread a run of units) and finds its own part; the first
+// writes down what it found of every unit, for the joins.
 template <bool KV4>
 __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* out,
                                            unsigned long long* tmp) {
@@ -620,6 +624,10 @@ __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* ou
         out->begin = b;
         out->end = work ? total * (blockIdx.x + 1) / ctas : 0;
       }
+      if (blockIdx.x == 0) {
+        if (tid < a.n) a.unit[tid] = unit_of(a, tid, at);
+        if (tid == 0) a.unit[a.n] = CdUnit{total, 0, 0, 0, 0};
+      }
       if (work && b >= at && b < at + (long long)R * a.n_kv) {
         out->u = tid;
         out->g = (int)((b - at) / R);
@@ -638,6 +646,14 @@ __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* ou
   if (tid == kCdThreads - 1) out->total = (long long)(before + mine) * a.n_kv;
   __syncthreads();
   const long long total = out->total;
+  if (blockIdx.x == 0) {
+    long long at = (long long)before * a.n_kv;
+    for (int u = u0; u < u1; ++u) {
+      a.unit[u] = unit_of(a, u, at);
+      at += (long long)rounds_of<KV4>(decode_length(a, u, &ap)) * a.n_kv;
+    }
+    if (tid == 0) a.unit[a.n] = CdUnit{total, 0, 0, 0, 0};
+  }
   const int ctas = (int)min((long long)gridDim.x, total);
   if (ctas == 0 || (int)blockIdx.x >= ctas) {
     if (tid == 0) out->ctas = ctas;
@@ -669,17 +685,15 @@ __device__ __forceinline__ void find_start(const CacheDecodeArgs& a, CdStart* ou
 
 template <int G, bool KV4, bool PAGED>
 __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(CacheDecodeArgs a) {
-  extern __shared__ __align__(16) unsigned char dyn[];
+  // (the ring begins on a sector: where two lanes' 16 bytes of one sector of the cache do not make one
+  // sector here, each is fetched by itself, and the 32 units of 32K took 280 us instead of 231)
+  extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ CdStart start;
   __shared__ unsigned long long scan[33];
   __shared__ uint2 qf[KV4 ? 1 : 8 * 32];
-  __shared__ float lse[8];
-  __shared__ int flag;
   CdMerge& mg = *reinterpret_cast<CdMerge*>(dyn);
-  CdJoin& jn = *reinterpret_cast<CdJoin*>(dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int units = a.n * a.n_kv;
   bool append;
   pdl_wait();
 
@@ -882,98 +896,12 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       }
       if (tid < G) {
         if (whole)
-          lse[tid] = neg_lse(M, S);
+          a.lse[(size_t)ukv * G + tid] = neg_lse(M, S);
         else
           reinterpret_cast<float2*>(a.part_ml)[slot * G + tid] = make_float2(M, S);
       }
     }
 
-    bool done = whole;
-    if (!whole) {
-      // the CTAs that share this (unit, KV head): those of its first and its last round
-      const long long z0 = at - round, z1 = z0 + R - 1;
-      const int i0 = part_of(start, z0), i1 = part_of(start, z1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        flag = atomicAdd(a.counters + ukv, 1) == i1 - i0;
-        if (flag) a.counters[ukv] = 0;
-      }
-      __syncthreads();
-      done = flag != 0;
-      if (done) {
-        __threadfence();
-        const size_t s0 = 2 * (size_t)i0 + (part_begin(start, i0) == z0 ? 0 : 1);
-        auto slot_of = [&](int k) { return k == 0 ? s0 : 2 * (size_t)(i0 + k); };
-        const int parts = i1 - i0 + 1;
-        const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-        if (warp < G) {
-          float M = -1e30f;
-          for (int k = lane; k < parts; k += 32)
-            M = fmaxf(M, __ldcg(ml + slot_of(k) * G + warp).x);
-#pragma unroll
-          for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-          float S = 0.f;
-          for (int k = lane; k < parts; k += 32) {
-            const float2 x = __ldcg(ml + slot_of(k) * G + warp);
-            const float f = fast_exp2(x.x - M);
-            if (k < kCdFactors) jn.factor[k * G + warp] = f;
-            S = fmaf(x.y, f, S);
-          }
-#pragma unroll
-          for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
-          if (lane == 0) {
-            jn.total[warp] = S;
-            jn.top[warp] = M;
-            lse[warp] = neg_lse(M, S);
-          }
-        }
-        __syncthreads();
-        // four outputs per thread; with fewer than eight heads the threads also share the parts
-        constexpr int kQuads = G * kHeadDim / 4, kShare = kCdThreads / kQuads;
-        const int quad = tid % kQuads, share = tid / kQuads;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = share; k < parts; k += kShare) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_of(k) * G * kHeadDim) + quad);
-          float f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int h = (4 * quad + e) % G;
-            f[e] = k < kCdFactors ? jn.factor[k * G + h]
-                                  : fast_exp2(__ldcg(ml + slot_of(k) * G + h).x - jn.top[h]);
-          }
-          o.x = fmaf(x.x, f[0], o.x);
-          o.y = fmaf(x.y, f[1], o.y);
-          o.z = fmaf(x.z, f[2], o.z);
-          o.w = fmaf(x.w, f[3], o.w);
-        }
-        if (kShare > 1) {
-          jn.sums[tid] = o;
-          __syncthreads();
-          if (share == 0)
-            for (int e = 1; e < kShare; ++e) {
-              const float4 x = jn.sums[e * kQuads + quad];
-              o.x += x.x;
-              o.y += x.y;
-              o.z += x.z;
-              o.w += x.w;
-            }
-        }
-        if (share == 0) {
-          const float y[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 4 * quad + e, h = i % G;
-            const float S = jn.total[h];
-            a.out[((size_t)ukv * G + h) * kHeadDim + out_dim<KV4>(i / G)] =
-                __float2bfloat16_rn(S == 0.f ? 0.f : y[e] / S);
-          }
-        }
-      }
-    }
-    __syncthreads();  // (lse is written)
-    if (done && a.weights && tid < G) a.lse[(size_t)ukv * G + tid] = lse[tid];
     __syncthreads();  // shared memory is used again
     at += rounds;
     round = 0;
@@ -983,49 +911,116 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     }
   }
 
-  // units without tokens have no CTA of their own; bad lengths are told once
-  for (int ukv = blockIdx.x; ukv < units; ukv += gridDim.x) {
-    const int u = ukv / a.n_kv, L = decode_length(a, u, &append);
+  // (a launch that follows may take this CTA's place from here; from the start, 1021 tokens took 8.2 us
+  // instead of 7.8)
+  pdl_trigger();
+}
+
+// The joins: blockIdx.y = 0 the outputs and the length, the others kCdWeightChunk tokens' weights.
+// `ctas`: CTAs of the decode's launch.
+constexpr int kCdFactors = 512;  // the factors of more parts are made again for each output
+template <int G, bool KV4>
+__global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs a, int ctas) {
+  __shared__ float4 sums[kCdThreads];
+  __shared__ float factor[kCdFactors * G];
+  __shared__ float total_s[8], top[8], nlse[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ukv = blockIdx.x, u = ukv / a.n_kv, g = ukv - u * a.n_kv;
+  // (no early trigger: the next launch's CTAs would wait in these CTAs' places, 1021 tokens 8.4 us
+  // instead of 8.2)
+  pdl_wait();
+  const CdUnit un = a.unit[u];
+  const long long total = a.unit[a.n].at;
+  const int L = un.length, R = rounds_of<KV4>(L);
+  if (blockIdx.y == 0) {
+    if (g == 0 && tid == 0) {
+      if (un.bad) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
+      if (a.len_out) a.len_out[u] = un.next;
+    }
     if (L == 0)
       for (int i = tid; i < G * kHeadDim; i += kCdThreads)
         a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(0.f);
-    if (tid == 0 && ukv == u * a.n_kv) {
-      const int l = a.len[u];
-      if (l < 0 || l > a.cap || (a.new_k && !append)) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
+  } else if ((int)(blockIdx.y - 1) * kCdWeightChunk >= L) {
+    return;
+  }
+  if (L == 0) return;
+  // the parts that share this (unit, KV head): those of its first and its last round
+  ctas = (int)min((long long)ctas, total);
+  const long long z0 = un.at + (long long)g * R;
+  const int i0 = part_of(total, ctas, z0), parts = part_of(total, ctas, z0 + R - 1) - i0 + 1;
+  if (parts == 1) {  // (its outputs are written)
+    if (blockIdx.y == 0) return;
+    if (tid < G) nlse[tid] = a.lse[(size_t)ukv * G + tid];
+  }
+  const size_t s0 = 2 * (size_t)i0 + (part_begin(total, ctas, i0) == z0 ? 0 : 1);
+  auto slot_of = [&](int k) { return k == 0 ? s0 : 2 * (size_t)(i0 + k); };
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  if (parts > 1 && warp < G) {
+    float M = -1e30f, S = 0.f;
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, ml[slot_of(k) * G + warp].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int k = lane; k < parts; k += 32) {
+      const float2 x = ml[slot_of(k) * G + warp];
+      const float f = fast_exp2(x.x - M);
+      if (k < kCdFactors) factor[k * G + warp] = f;
+      S = fmaf(x.y, f, S);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
+    if (lane == 0) {
+      total_s[warp] = S;
+      top[warp] = M;
+      nlse[warp] = neg_lse(M, S);
     }
   }
-
-  // (a launch that follows may take this CTA's place from here; from the start, its CTAs did so unevenly
-  // and a 245 us call took 263)
-  pdl_trigger();
-  // the lengths move on when every CTA has read them (they may be their own inputs)
-  if (a.len_out) {
-    __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      flag = atomicAdd(a.counters + units, 1) == (int)gridDim.x - 1;
-      if (flag) a.counters[units] = 0;
+  __syncthreads();
+  if (blockIdx.y > 0) {
+    for (int t0 = (blockIdx.y - 1) * kCdWeightChunk; t0 < L; t0 += (gridDim.y - 1) * kCdWeightChunk)
+      add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, t0,
+                     min(L, t0 + kCdWeightChunk), nlse);
+    return;
+  }
+  // four outputs per thread; with fewer than eight heads the threads also share the parts
+  constexpr int kQuads = G * kHeadDim / 4, kShare = kCdThreads / kQuads;
+  const int quad = tid % kQuads, share = tid / kQuads;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = share; k < parts; k += kShare) {
+    const float4 x = reinterpret_cast<const float4*>(a.part_o + slot_of(k) * G * kHeadDim)[quad];
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int h = (4 * quad + e) % G;
+      f[e] = k < kCdFactors ? factor[k * G + h] : fast_exp2(ml[slot_of(k) * G + h].x - top[h]);
     }
+    o.x = fmaf(x.x, f[0], o.x);
+    o.y = fmaf(x.y, f[1], o.y);
+    o.z = fmaf(x.z, f[2], o.z);
+    o.w = fmaf(x.w, f[3], o.w);
+  }
+  if (kShare > 1) {
+    sums[tid] = o;
     __syncthreads();
-    if (flag)
-      for (int i = tid; i < a.n; i += kCdThreads) {
-        const int l = a.len[i];
-        a.len_out[i] = l >= 0 && l < a.cap ? l + 1 : l;
+    if (share == 0)
+      for (int e = 1; e < kShare; ++e) {
+        const float4 x = sums[e * kQuads + quad];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
       }
   }
-}
-
-// Weights from the logits and the joined sums, kCdWeightChunk tokens per CTA. A kernel of its own: done
-// by the CTA that finishes a (unit, KV head), the 32 units of 32K took 251 us instead of 238, the ragged
-// bf16 batch 259 instead of 241.
-template <int G>
-__global__ void __launch_bounds__(kCdThreads) cache_weights_kernel(CacheDecodeArgs a) {
-  pdl_wait();
-  const int ukv = blockIdx.x, u = ukv / a.n_kv;
-  const int L = max(0, min((a.len_out ? a.len_out : a.len)[u], a.cap));
-  for (int t0 = blockIdx.y * kCdWeightChunk; t0 < L; t0 += gridDim.y * kCdWeightChunk)
-    add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, t0,
-                   min(L, t0 + kCdWeightChunk), a.lse + (size_t)ukv * G);
+  if (share == 0) {
+    const float y[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 4 * quad + e, h = i % G;
+      const float S = total_s[h];
+      a.out[((size_t)ukv * G + h) * kHeadDim + out_dim<KV4>(i / G)] =
+          __float2bfloat16_rn(S == 0.f ? 0.f : y[e] / S);
+    }
+  }
 }
 
 template <int G, bool KV4, bool PAGED>
@@ -1035,10 +1030,13 @@ static cudaError_t launch_group(const CacheDecodeArgs& a, cudaStream_t s) {
   cudaError_t e = ensure_dyn_smem((const void*)cache_decode_kernel<G, KV4, PAGED>, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl_kernel(cache_decode_kernel<G, KV4, PAGED>, dim3(ctas), dim3(kCdThreads), smem, s, a);
-  if (e != cudaSuccess || !a.weights) return e;
-  const int chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;
-  return launch_pdl_kernel(cache_weights_kernel<G>, dim3(a.n * a.n_kv, chunks < 4096 ? chunks : 4096),
-                           dim3(kCdThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  // weights: CTAs for eight per SM, since each has the sums to find first (32 units of 32K: four per SM
+  // 237 us, eight 231, sixteen 232, a CTA per chunk 237)
+  const int units = a.n * a.n_kv, chunks = (a.cap + kCdWeightChunk - 1) / kCdWeightChunk;
+  const int fill = (kCdWeightCtasPerSm * device_sm_count() + units - 1) / units;
+  const int y = a.weights ? (chunks < fill ? chunks : fill) : 0;
+  return launch_pdl_kernel(cache_join_kernel<G, KV4>, dim3(units, 1 + y), dim3(kCdThreads), 0, s, a, ctas);
 }
 
 template <int G>

@@ -31,7 +31,6 @@ static inline int most_moves(int cap, int keep) {
 }
 
 struct EvictLists {
-  int32_t* done;   // CTAs that are through (zero between calls)
   int32_t* count;  // [n*n_kv]
   int32_t* dst;    // [n*n_kv][most]
   int32_t* src;    // [n*n_kv][most]
@@ -42,8 +41,7 @@ static EvictLists lists_of(const EvictArgs& a) {
   EvictLists l;
   const size_t units = (size_t)a.n * a.n_kv;
   l.most = most_moves(a.cap, a.keep);
-  l.done = static_cast<int32_t*>(a.scratch);
-  l.count = l.done + 64;
+  l.count = static_cast<int32_t*>(a.scratch);
   l.dst = l.count + align_up(units * 4, 256) / 4;
   l.src = l.dst + align_up(units * l.most * 4, 256) / 4;
   return l;
@@ -51,7 +49,7 @@ static EvictLists lists_of(const EvictArgs& a) {
 
 size_t evict_scratch_bytes(int n, int n_kv, int cap, int keep) {
   const size_t units = (size_t)n * n_kv;
-  return 256 + align_up(units * 4, 256) + 2 * align_up(units * most_moves(cap, keep) * 4, 256);
+  return align_up(units * 4, 256) + 2 * align_up(units * most_moves(cap, keep) * 4, 256);
 }
 
 struct EvSmem {
@@ -190,21 +188,17 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int ukv, const int
   }
 }
 
-// Lengths move on when every CTA has read them (they may be their own inputs).
-__device__ __forceinline__ void evict_lengths(const EvictArgs& a, int32_t* done) {
-  __shared__ int last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(done, 1) == (int)gridDim.x - 1;
-    if (last) *done = 0;
-  }
-  __syncthreads();
-  if (last)
-    for (int u = threadIdx.x; u < a.n; u += blockDim.x) {
-      const int L = a.len[u];
-      a.len_out[u] = (L >= 0 && L <= a.cap) ? min(L, a.keep) : L;
-    }
+__device__ __forceinline__ void evict_length(const EvictArgs& a, int u) {
+  const int L = a.len[u];
+  a.len_out[u] = (L >= 0 && L <= a.cap) ? min(L, a.keep) : L;
+}
+
+// Lengths that are their own inputs move on after every reader.
+__global__ void evict_length_kernel(EvictArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int u = blockIdx.x * blockDim.x + threadIdx.x;
+  if (u < a.n) evict_length(a, u);
 }
 
 struct EvDigit {
@@ -406,7 +400,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
     evict_finish(x, dst, src, moves, weight_of, position_of);
   }
   if (!FUSED && tid == 0) ls.count[ukv] = moves;
-  if (FUSED) evict_lengths(a, ls.done);
+  if (FUSED && a.len_out != a.len && tid == 0 && ukv % a.n_kv == 0) evict_length(a, ukv / a.n_kv);
 }
 
 // The same for units of more rows than shared memory holds: 8 bits at a time, the keys made again for
@@ -501,10 +495,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
 __global__ void __launch_bounds__(kEvMoveThreads) evict_move_kernel(EvictArgs a, EvictLists ls) {
   pdl_wait();
   const int ukv = blockIdx.x, u = ukv / a.n_kv;
-  if (blockIdx.y == 0 && ukv == u * a.n_kv && threadIdx.x == 0) {
-    const int L = a.len[u];
-    a.len_out[u] = (L >= 0 && L <= a.cap) ? min(L, a.keep) : L;
-  }
+  if (blockIdx.y == 0 && ukv == u * a.n_kv && threadIdx.x == 0) evict_length(a, u);
   move_rows<4>(a, ukv, ls.dst + (size_t)ukv * ls.most, ls.src + (size_t)ukv * ls.most,
                blockIdx.y * kEvMoveWarps + (threadIdx.x >> 5), gridDim.y * kEvMoveWarps,
                ls.count[ukv]);
@@ -533,7 +524,9 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   } else {
     e = launch_pdl_kernel(evict_select_kernel, dim3(units), dim3(kEvThreads), 0, s, a, ls);
   }
-  if (e != cudaSuccess || fused) return e;
+  if (e != cudaSuccess || (fused && a.len_out != a.len)) return e;
+  if (fused)
+    return launch_pdl_kernel(evict_length_kernel, dim3((a.n + 255) / 256), dim3(256), 0, s, a);
   const int rows = 4 * kEvMoveWarps * (a.row_bytes[2] ? 3 : 1);  // of a CTA at a time
   int y = (ls.most + rows - 1) / rows;
   y = y < 1 ? 1 : (y > 1024 ? 1024 : y);

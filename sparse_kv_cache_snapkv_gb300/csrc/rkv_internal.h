@@ -215,6 +215,14 @@ struct Kv4AppendArgs {
 };
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
 
+// A unit as a decode's kernels see it: rounds of tokens before it (its KV heads' in all), the tokens
+// it attends to, its length after the call, whether its length was out of range or it was full.
+// Behind the last: all rounds.
+struct CdUnit {
+  long long at;
+  int length, next, bad, pad;
+};
+
 // Decode over a whole cache in bf16 (k, v) or 4 bits (codes and scales), with the optional
 // append (4 bits only) and the optional accumulation of the tokens' weights.
 struct CacheDecodeArgs {
@@ -232,9 +240,9 @@ struct CacheDecodeArgs {
   float scale_log2;
   bf16* out;
   float* weights;      // nullptr: not asked for
-  int32_t* counters;   // workspace [n*n_kv + 1], zero between calls
+  CdUnit* unit;        // workspace [n + 1]: what the first kernel found, for the second
   float* lse;          // workspace [n*n_kv][gqa]: negated log-sum-exps (log2 domain)
-  float* part_ml;      // workspace [2 per CTA][gqa][2]
+  float* part_ml;      // workspace [2 per CTA][gqa][2]: maxima and sums of a part
   float* part_o;       // workspace [2 per CTA][gqa][128]
   float* logits;       // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
   uint32_t* status;

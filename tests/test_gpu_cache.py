@@ -710,3 +710,37 @@ def test_prompt_and_evict_in_a_graph(rkv):
         res.append((kk, vv, w, lo, wo, po))
     for a, b in zip(*res):
         assert torch.equal(a, b)
+
+
+def test_workspace_contents_do_not_matter(rkv):
+    """One workspace for every call and shape, full of bytes but for its status word."""
+    ws = torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    for n, n_kv, gqa, cap in ((2, 2, 4, 300), (40, 2, 2, 700), (1, 1, 8, 20000)):
+        lens = [cap - 1 - 3 * u for u in range(n)]
+        cache = _kv4_case(rkv, n, n_kv, cap, lens, 170)
+        q = _normal(171, 1, n, n_kv * gqa, D)[0]
+        nk = _normal(172, n, n_kv, 1, D)[:, :, 0].contiguous()
+        k, v = _normal(173, n, n_kv, cap, D), _normal(174, n, n_kv, cap, D)
+        qp = _normal(175, n, n_kv * gqa, 50, D)
+        pos = torch.full((n, n_kv, cap), -1, dtype=I32, device="cuda")
+        res = []
+        for shared in (False, True):
+            w = ws if shared else None
+            c = [x.clone() for x in cache]
+            kk, vv = k.clone(), v.clone()
+            out, wt, ln = torch.empty_like(q), torch.zeros(n, n_kv, cap, device="cuda"), _ints(lens)
+            p, seen = pos.clone(), _ints(lens)
+            o2, w2 = torch.empty_like(q), torch.zeros_like(wt)
+            for call in (
+                lambda: rkv.rkv_kv4_decode(q, *c, ln, SCALE, out, new_k=nk, new_v=nk, length_out=ln,
+                                           weights=wt, ws=w),
+                lambda: rkv.rkv_dense_decode_weights(q, kk, vv, seen, SCALE, o2, w2, ws=w),
+                lambda: rkv.rkv_prompt_weights(qp, _ints([50] * n), kk, seen, SCALE, w2, ws=w),
+                lambda: rkv.rkv_evict(kk, vv, seen, w2, p, seen, 100, 9, seen, w2, p, ws=w),
+                lambda: rkv.rkv_evict_kv4(*c, ln, wt, pos, ln, 200, 9, ln, wt, p, ws=w),
+            ):
+                rkv.rkv_check_status(call())
+            res.append((out, wt, ln, *c, o2, w2, kk, vv, seen, p))
+        for a, b in zip(*res):
+            assert torch.equal(a, b)
