@@ -410,12 +410,14 @@ rkv_status rkv_dense_decode_noalloc(const void* q, const void* k, const void* v,
  *   new_k, new_v [n][n_kv][max_new][128] bf16: rows 0 .. new_len[u]-1 are taken
  *   new_len  [n] int32 (device) or NULL (max_new rows of every unit)
  *   len      [n] int32: rows in the cache before the call
- *   len_out  [n] int32: len[u] + new_len[u]; may be the same array as len. A unit with new_len[u]
+ *   len_out  [n] int32: len[u] + new_len[u]; may be the same array as len or new_len. A unit with new_len[u]
  *            outside [0, max_new], len[u] < 0 or len[u] + new_len[u] > cap sets
  *            RKV_DEV_LEN_OVER_CAP and is left as it was (len_out[u] = len[u]).
  *   k_values, v_values NULL or [n][n_kv][max_new][128] bf16: the values the rows now stand for
  *            (for a prompt whose own attention is to see what the decode will see); rows past
  *            new_len[u] are left as they were. Both or neither.
+ * Paged: a row whose table entry is outside [0, num_blocks) sets RKV_DEV_BAD_INDEX and is not
+ * stored (as the decode's new row; block 0 is only read in a block's place).
  * Workspace rkv_kv4_append_workspace_bytes. */
 size_t rkv_kv4_append_workspace_bytes(int n);
 rkv_status rkv_kv4_append(const void* new_k, const void* new_v, const int32_t* new_len, int n,
@@ -499,7 +501,7 @@ rkv_status rkv_prompt_weights(const void* q, const int32_t* q_len, const void* k
  * are in no particular order of position (attention does not depend on it; page summaries have
  * to be rebuilt). A unit of at most `keep` rows is left as it is.
  *   k, v     [n][n_kv][cap][128] bf16, or the 4-bit arrays: moved in place
- *   len      [n] int32; len_out [n] int32: min(len[u], keep); may be the same array
+ *   len      [n] int32; len_out [n] int32: min(len[u], keep); may be the same array, or seen
  *   weights  [n][n_kv][cap] fp32, pos [n][n_kv][cap] int32: a row's position in its sequence, or -1
  *            for a row appended since the last eviction (its position is then
  *            seen[u] - (len[u] - row)); all -1 at first

@@ -55,6 +55,15 @@ __device__ __forceinline__ int append_count(const Kv4AppendArgs& a, int u, int* 
   return t;
 }
 
+// The block that a new token goes to, -1 where the table's entry is none: block 0, read in its place
+// elsewhere, may be another sequence's.
+__device__ __forceinline__ int append_block(const PagedMap& m, int u, int t, uint32_t* status) {
+  const int b = m.table[(size_t)u * m.max_blocks + t / m.block];
+  if (b >= 0 && b < m.num_blocks) return b;
+  set_status(status, RKV_DEV_BAD_INDEX);
+  return -1;
+}
+
 // One thread = one block of 16 values (32 bytes in, 8 + 1 out); blockIdx.y: K or V. Bound by the
 // copy: 8 neighbouring threads make one row of codes and one of scales.
 __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArgs a) {
@@ -72,22 +81,28 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendArg
   const bool v = blockIdx.y != 0;
   if (g == 0 && i == 0 && blk == 0 && !v) {
     if (t < 0) set_status(a.status, RKV_DEV_LEN_OVER_CAP);
-    // (len_out that is len itself is written by kv4_length_kernel, after every reader)
-    if (a.len_out != a.len) a.len_out[u] = have + max(t, 0);
+    // (len_out that is also an input is written by kv4_length_kernel, after every reader)
+    if (a.len_out != a.len && a.len_out != a.new_len) a.len_out[u] = have + max(t, 0);
   }
   if (i >= t) return;
   const int at = have + i;
   size_t dst;
-  if (a.pm.table)
-    dst = paged_row(a.pm, paged_block(a.pm, u, at, a.status), a.n_kv, g, at);
-  else
+  bool there = true;
+  if (a.pm.table) {
+    const int b = append_block(a.pm, u, at, a.status);
+    there = b >= 0;
+    dst = paged_row(a.pm, b, a.n_kv, g, at);
+  } else {
     dst = (size_t)ukv * a.cap + at;
+  }
   const size_t src = (size_t)row * kHeadDim + blk * kScaleGroup;
   uint32_t w[8], sb;
   load32((v ? a.new_v : a.new_k) + src, w);
   const uint2 c = quantise16(w, &sb);
-  *reinterpret_cast<uint2*>((v ? a.v_codes : a.k_codes) + dst * kCodeBytes + blk * 8) = c;
-  (v ? a.v_scales : a.k_scales)[dst * kRowScales + blk] = (uint8_t)sb;
+  if (there) {
+    *reinterpret_cast<uint2*>((v ? a.v_codes : a.k_codes) + dst * kCodeBytes + blk * 8) = c;
+    (v ? a.v_scales : a.k_scales)[dst * kRowScales + blk] = (uint8_t)sb;
+  }
   if (a.k_values) {
     values16(c, sb, w);
     store32((v ? a.v_values : a.k_values) + src, w);
@@ -110,7 +125,7 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
   if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   const cudaError_t e = launch_pdl_kernel(kv4_append_kernel, dim3((unsigned)ctas, 2),
                                           dim3(kAppendThreads), 0, s, a);
-  if (e != cudaSuccess || a.len_out != a.len) return e;
+  if (e != cudaSuccess || (a.len_out != a.len && a.len_out != a.new_len)) return e;
   return launch_pdl_kernel(kv4_length_kernel, dim3((a.n + 255) / 256), dim3(256), 0, s, a);
 }
 
@@ -521,26 +536,23 @@ __device__ __forceinline__ float neg_lse(float m, float l) {
   return l > 0.f ? -(m + log2f(l)) : (l == 0.f ? -INFINITY : l);
 }
 
-// weights of tokens [t0, t1) from their logits (L2, written by other SMs) and the heads' neg_lse
+// kCdWeightChunk tokens' weights from their logits and the heads' neg_lse; the loads can be on their
+// way before those are known.
 template <int G>
-__device__ __forceinline__ void add_weights(const float* logits, float* weights, int t0, int t1,
-                                            const float* nlse) {
-  float nl[G];
-#pragma unroll
-  for (int h = 0; h < G; ++h) nl[h] = nlse[h];
-  constexpr int kU = 4;  // tokens in flight per thread
-  for (int b = t0 + (int)threadIdx.x; b < t1; b += kU * kCdThreads) {
-    float x[kU][G], w[kU];
+struct CdWeights {
+  static constexpr int kU = kCdWeightChunk / kCdThreads;  // tokens of a thread
+  float x[kU][G], w[kU];
+  __device__ __forceinline__ void load(const float* logits, const float* weights, int t0, int L) {
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int t = b + k * kCdThreads;
-      if (t < t1) {
+      const int t = t0 + k * kCdThreads + (int)threadIdx.x;
+      if (t < L) {
         const float* src = logits + (size_t)t * G;
         w[k] = weights[t];
         if (G % 4 == 0) {
 #pragma unroll
           for (int h = 0; h < G; h += 4) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + h));
+            const float4 y = *reinterpret_cast<const float4*>(src + h);
             x[k][h] = y.x;
             x[k][h + 1] = y.y;
             x[k][h + 2] = y.z;
@@ -548,14 +560,19 @@ __device__ __forceinline__ void add_weights(const float* logits, float* weights,
           }
         } else {
 #pragma unroll
-          for (int h = 0; h < G; ++h) x[k][h] = __ldcg(src + h);
+          for (int h = 0; h < G; ++h) x[k][h] = src[h];
         }
       }
     }
+  }
+  __device__ __forceinline__ void add(const float* nlse, float* weights, int t0, int L) const {
+    float nl[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) nl[h] = nlse[h];
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int t = b + k * kCdThreads;
-      if (t < t1) {
+      const int t = t0 + k * kCdThreads + (int)threadIdx.x;
+      if (t < L) {
         float s = 0.f;
 #pragma unroll
         for (int h = 0; h < G; ++h) s += fast_exp2(x[k][h] + nl[h]);
@@ -563,7 +580,7 @@ __device__ __forceinline__ void add_weights(const float* logits, float* weights,
       }
     }
   }
-}
+};
 
 // Joining the warps: their O^T fragments as they are (row (j, e), lane), padded so that neither the
 // lanes' stores nor the reads meet in a bank more than twice.
@@ -720,15 +737,16 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       if (tid < 16) {
         const bool v = tid >= 8;
         const int blk = tid & 7, row = L - 1;
-        const size_t dst = PAGED
-                               ? paged_row(a.pm, paged_block(a.pm, u, row, a.status), a.n_kv, g, row)
-                               : (size_t)ukv * a.cap + row;
+        const int b = PAGED ? append_block(a.pm, u, row, a.status) : 0;
+        const size_t dst = PAGED ? paged_row(a.pm, b, a.n_kv, g, row) : (size_t)ukv * a.cap + row;
         uint32_t w[8], sb;
         load32((v ? a.new_v : a.new_k) + (size_t)ukv * kHeadDim + blk * kScaleGroup, w);
         const uint2 cd = quantise16(w, &sb);
         uint8_t* codes = static_cast<uint8_t*>(const_cast<void*>(v ? a.v : a.k));
-        *reinterpret_cast<uint2*>(codes + dst * kCodeBytes + blk * 8) = cd;
-        const_cast<uint8_t*>(v ? a.v_scales : a.k_scales)[dst * kRowScales + blk] = (uint8_t)sb;
+        if (b >= 0) {
+          *reinterpret_cast<uint2*>(codes + dst * kCodeBytes + blk * 8) = cd;
+          const_cast<uint8_t*>(v ? a.v_scales : a.k_scales)[dst * kRowScales + blk] = (uint8_t)sb;
+        }
         __threadfence();
       }
       __syncthreads();
@@ -940,10 +958,13 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
     if (L == 0)
       for (int i = tid; i < G * kHeadDim; i += kCdThreads)
         a.out[(size_t)ukv * G * kHeadDim + i] = __float2bfloat16_rn(0.f);
-  } else if ((int)(blockIdx.y - 1) * kCdWeightChunk >= L) {
-    return;
   }
-  if (L == 0) return;
+  int t0 = ((int)blockIdx.y - 1) * kCdWeightChunk;
+  if (t0 >= L || L == 0) return;
+  const float* logits = a.logits + (size_t)ukv * a.cap * G;
+  float* weights = a.weights + (size_t)ukv * a.cap;
+  CdWeights<G> cw;
+  if (blockIdx.y > 0) cw.load(logits, weights, t0, L);
   // the parts that share this (unit, KV head): those of its first and its last round
   ctas = (int)min((long long)ctas, total);
   const long long z0 = un.at + (long long)g * R;
@@ -956,12 +977,13 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
   auto slot_of = [&](int k) { return k == 0 ? s0 : 2 * (size_t)(i0 + k); };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
   if (parts > 1 && warp < G) {
-    float M = -1e30f, S = 0.f;
-    for (int k = lane; k < parts; k += 32) M = fmaxf(M, ml[slot_of(k) * G + warp].x);
+    const float2 mine = lane < parts ? ml[slot_of(lane) * G + warp] : make_float2(-1e30f, 0.f);
+    float M = mine.x, S = 0.f;
+    for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, ml[slot_of(k) * G + warp].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     for (int k = lane; k < parts; k += 32) {
-      const float2 x = ml[slot_of(k) * G + warp];
+      const float2 x = k == lane ? mine : ml[slot_of(k) * G + warp];
       const float f = fast_exp2(x.x - M);
       if (k < kCdFactors) factor[k * G + warp] = f;
       S = fmaf(x.y, f, S);
@@ -976,9 +998,12 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
   }
   __syncthreads();
   if (blockIdx.y > 0) {
-    for (int t0 = (blockIdx.y - 1) * kCdWeightChunk; t0 < L; t0 += (gridDim.y - 1) * kCdWeightChunk)
-      add_weights<G>(a.logits + (size_t)ukv * a.cap * G, a.weights + (size_t)ukv * a.cap, t0,
-                     min(L, t0 + kCdWeightChunk), nlse);
+    cw.add(nlse, weights, t0, L);
+    const int step = ((int)gridDim.y - 1) * kCdWeightChunk;
+    for (t0 += step; t0 < L; t0 += step) {
+      cw.load(logits, weights, t0, L);
+      cw.add(nlse, weights, t0, L);
+    }
     return;
   }
   // four outputs per thread; with fewer than eight heads the threads also share the parts

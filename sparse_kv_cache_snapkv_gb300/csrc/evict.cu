@@ -193,7 +193,12 @@ __device__ __forceinline__ void evict_length(const EvictArgs& a, int u) {
   a.len_out[u] = (L >= 0 && L <= a.cap) ? min(L, a.keep) : L;
 }
 
-// Lengths that are their own inputs move on after every reader.
+// Whether no input is the lengths' output.
+__host__ __device__ __forceinline__ bool lengths_apart(const EvictArgs& a) {
+  return a.len_out != a.len && a.len_out != a.seen;
+}
+
+// Lengths that are inputs too move on after every reader.
 __global__ void evict_length_kernel(EvictArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
     evict_finish(x, dst, src, moves, weight_of, position_of);
   }
   if (!FUSED && tid == 0) ls.count[ukv] = moves;
-  if (FUSED && a.len_out != a.len && tid == 0 && ukv % a.n_kv == 0) evict_length(a, ukv / a.n_kv);
+  if (FUSED && lengths_apart(a) && tid == 0 && ukv % a.n_kv == 0) evict_length(a, ukv / a.n_kv);
 }
 
 // The same for units of more rows than shared memory holds: 8 bits at a time, the keys made again for
@@ -524,7 +529,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   } else {
     e = launch_pdl_kernel(evict_select_kernel, dim3(units), dim3(kEvThreads), 0, s, a, ls);
   }
-  if (e != cudaSuccess || (fused && a.len_out != a.len)) return e;
+  if (e != cudaSuccess || (fused && lengths_apart(a))) return e;
   if (fused)
     return launch_pdl_kernel(evict_length_kernel, dim3((a.n + 255) / 256), dim3(256), 0, s, a);
   const int rows = 4 * kEvMoveWarps * (a.row_bytes[2] ? 3 : 1);  // of a CTA at a time

@@ -744,3 +744,52 @@ def test_workspace_contents_do_not_matter(rkv):
             res.append((out, wt, ln, *c, o2, w2, kk, vv, seen, p))
         for a, b in zip(*res):
             assert torch.equal(a, b)
+
+
+def test_rows_without_a_block_are_not_stored(rkv):
+    n, n_kv, block, gqa = 2, 2, 16, 4
+    pools = [torch.full((5, n_kv, block, w), 0x11, dtype=torch.uint8, device="cuda") for w in (64, 8, 64, 8)]
+    table = _ints([[1, 2], [3, 9]])  # the second unit's second block is none
+    lens = _ints([20, 15])
+    q, out = _normal(180, 1, n, n_kv * gqa, D)[0], torch.empty(n, n_kv * gqa, D, dtype=BF, device="cuda")
+    new, ln = _normal(181, n, n_kv, 3, D), torch.zeros_like(lens)
+    first = [x[0].clone() for x in pools]
+    ws = rkv.rkv_kv4_append_paged(new, new, *pools, table, lens, ln)
+    with pytest.raises(rkv.RkvError) as e:
+        rkv.rkv_check_status(ws)
+    assert e.value.bits == 0x10 and ln.tolist() == [23, 18]
+    row = new[:, :, 0].contiguous()
+    ws = rkv.rkv_kv4_decode_paged(q, *pools, table, ln, SCALE, out, new_k=row, new_v=row, length_out=ln)
+    with pytest.raises(rkv.RkvError) as e:
+        rkv.rkv_check_status(ws)
+    assert e.value.bits == 0x10 and ln.tolist() == [24, 19]
+    for x, was in zip(pools, first):
+        assert torch.equal(x[0], was) and (x[4] == 0x11).all()
+        assert (x[3, :, :15] == 0x11).all()
+    assert (pools[0][2, :, 4:8] != 0x11).any(-1).all() and (pools[0][3, :, 15] != 0x11).any()
+
+
+def test_lengths_out_may_be_any_input(rkv):
+    n, n_kv, cap, keep = 160, 3, 40, 8
+    lens = [(7 * u) % (cap - 4) for u in range(n)]
+    news = [u % 4 for u in range(n)]
+    new = _normal(190, n, n_kv, 4, D)
+    a, b = (rkv.kv4_cache(n, n_kv, cap) for _ in range(2))
+    out, same = _ints([0] * n), _ints(news)
+    rkv.rkv_check_status(rkv.rkv_kv4_append(new, new, *a, _ints(lens), out, new_len=_ints(news)))
+    rkv.rkv_check_status(rkv.rkv_kv4_append(new, new, *b, _ints(lens), same, new_len=same))
+    assert torch.equal(out, same) and out.tolist() == [x + y for x, y in zip(lens, news)]
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+    w = torch.rand(n, n_kv, cap, device="cuda")
+    pos = torch.full((n, n_kv, cap), -1, dtype=I32, device="cuda")
+    res = []
+    for alias in (False, True):
+        k, v = _normal(191, n, n_kv, cap, D), _normal(192, n, n_kv, cap, D)
+        seen, wo, po = _ints([x + 3 for x in lens]), w.clone(), pos.clone()
+        lo = seen if alias else torch.zeros_like(seen)
+        rkv.rkv_check_status(rkv.rkv_evict(k, v, _ints(lens), w, pos, seen, keep, 3, lo, wo, po))
+        res.append((k, v, wo, po, lo))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+    assert res[0][4].tolist() == [min(x, keep) for x in lens]
