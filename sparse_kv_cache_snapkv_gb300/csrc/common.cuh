@@ -161,6 +161,26 @@ __device__ __forceinline__ void cp_async_wait_all() {
 }
 
 // ------------------------------------------------------------------------------------------
+// thread-block clusters
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// 32-bit word at `local` (a shared address of this CTA) in the shared memory of CTA `rank`.
+__device__ __forceinline__ uint32_t ld_peer_u32(const void* local, uint32_t rank) {
+  uint32_t addr, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------------------------------------
 // programmatic dependent launch: a kernel launched with programmatic stream serialisation may
 // start while the previous kernel in the stream drains; pdl_wait() blocks until that kernel has
 // completed and its writes are visible (a no-op for an ordinary launch). pdl_trigger() lets the

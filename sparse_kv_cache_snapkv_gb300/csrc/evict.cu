@@ -6,6 +6,11 @@
 // MSB-first radix select; then the free rows below keep and the kept rows at or past keep, equally
 // many, are listed in ascending order and paired. Sources lie at or past keep and destinations
 // below it, so all moves are independent.
+//
+// What it has to move is little (8 bytes a row read, up to 8 written, 2 rows per move: 256 units of 4352
+// rows 12 us, 32 of up to 32K in 4 bits 5 us at the copy rate); what bounds it is the chain of barriers of
+// the select, so the select makes few passes, all of them over shared memory, by as many CTAs as there are
+// SMs: 26 us and 32 us.
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -18,10 +23,16 @@ namespace rkv {
 constexpr int kEvThreads = 1024;
 constexpr int kEvMoveThreads = 256;
 constexpr int kEvMoveWarps = kEvMoveThreads / 32;
-// Up to this many rows a unit's keys stay in its CTA's shared memory through the select; beyond, they
-// are made again from the weights for each pass.
+// Up to this many rows' keys stay in a CTA's shared memory through the select; a unit that needs more
+// than kEvMaxCluster CTAs for them has them made again from the weights for each pass.
 constexpr int kEvSmemRows = 40960;
-constexpr int kEvHeldRows = 8192;  // up to this many, their weights and positions too (two CTAs per SM)
+constexpr int kEvMaxCluster = 8;
+constexpr int kEvClusterMost = 32736;  // rows of a cluster's CTA: two counts of them are one 32-bit sum
+// A cluster grows while its CTAs have this many rows each (8 units of 8192 rows: 2048 16.9 us, 1024
+// 19.0, 4096 17.5; 16 of 4352: 15.2, 15.6, 16.0, and 28.2 with 512).
+constexpr int kEvClusterRows = 2048;
+// up to this many rows, their weights and positions too (256 units of 4352 rows: 26 us, not held 32)
+constexpr int kEvHeldRows = 8192;
 constexpr int kEvBins = 2048;
 
 // free rows and kept rows past keep of one (unit, KV head); at most `most` of each
@@ -83,9 +94,10 @@ struct EvUnit {
   }
 };
 
-// The unit's arrays; false when there is nothing to evict (then everything has been done).
-__device__ __forceinline__ bool evict_unit(const EvictArgs& a, int ukv, EvUnit* x) {
-  const int u = ukv / a.n_kv, tid = threadIdx.x, nt = blockDim.x;
+// The unit's arrays; false when there is nothing to evict (then everything has been done, by the
+// unit's `nt` threads, of which this is the tid-th).
+__device__ __forceinline__ bool evict_unit(const EvictArgs& a, int ukv, EvUnit* x, int tid, int nt) {
+  const int u = ukv / a.n_kv;
   const size_t row0 = (size_t)ukv * a.cap;
   x->L = a.len[u];
   x->keep = a.keep;
@@ -265,10 +277,10 @@ __device__ __forceinline__ uint32_t scan_counts(uint32_t* cnt, int n, uint32_t* 
 
 // One CTA per (unit, KV head), keys in shared memory: three histogram passes of 11, 11 and 10 bits
 // (fewer when a bin is taken whole), then the kept rows as one bit each and the lists from prefix
-// sums over groups of 32 rows. The lists take the keys' place. FUSED: the CTA also moves its rows.
+// sums over groups of 32 rows. The lists take the keys' place; the CTA moves its rows itself.
 // HELD: the weights and positions stay in shared memory too.
-template <bool FUSED, bool HELD>
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLists ls) {
+template <bool HELD>
+__global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, int most) {
   extern __shared__ __align__(16) uint32_t ev_dyn[];
   __shared__ uint32_t hist[kEvBins];
   __shared__ EvDigit dg;
@@ -283,10 +295,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
   EvUnit x;
   pdl_wait();
   pdl_trigger();
-  int moves = 0;
   int32_t* dst = reinterpret_cast<int32_t*>(keys);
-  int32_t* src = dst + ls.most;  // (2 most <= cap)
-  if (evict_unit(a, ukv, &x)) {
+  int32_t* src = dst + most;  // (2 most <= cap)
+  if (evict_unit(a, ukv, &x, tid, nt)) {
     const int L = x.L, keep = x.keep, groups = (L + 31) / 32;
     auto weight_of = [&](int i) { return HELD ? held_w[i] : x.w[i]; };
     auto position_of = [&](int i) {
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
       cnt[g] = __popc(~t & low) | (__popc(t & ~low) << 16);  // (at most kEvSmemRows / 2 of each)
     }
     __syncthreads();
-    moves = (int)(scan_counts(cnt, groups, tmp) & 0xffffu);
+    const int moves = (int)(scan_counts(cnt, groups, tmp) & 0xffffu);
     // (the keys are done with: their memory takes the lists)
 #pragma unroll 4
     for (int i = tid; i < L; i += nt) {
@@ -387,7 +398,6 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
         if (!k) {
           const int m = (int)(cnt[g] & 0xffffu) + __popc(~t & low & under);
           dst[m] = i;
-          if (!FUSED) ls.dst[(size_t)ukv * ls.most + m] = i;
         } else {
           if (x.from) x.from[i] = i;
           if (x.wo != x.w) x.wo[i] = weight_of(i);
@@ -397,18 +407,171 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a, EvictLis
       } else if (k) {
         const int m = (int)(cnt[g] >> 16) + __popc(t & ~low & under);
         src[m] = i;
-        if (!FUSED) ls.src[(size_t)ukv * ls.most + m] = i;
       }
     }
     __syncthreads();
-    if (FUSED) move_rows<8>(a, ukv, dst, src, tid >> 5, nt >> 5, moves);
+    move_rows<8>(a, ukv, dst, src, tid >> 5, nt >> 5, moves);
     evict_finish(x, dst, src, moves, weight_of, position_of);
   }
-  if (!FUSED && tid == 0) ls.count[ukv] = moves;
-  if (FUSED && lengths_apart(a) && tid == 0 && ukv % a.n_kv == 0) evict_length(a, ukv / a.n_kv);
+  if (lengths_apart(a) && tid == 0 && ukv % a.n_kv == 0) evict_length(a, ukv / a.n_kv);
 }
 
-// The same for units of more rows than shared memory holds: 8 bits at a time, the keys made again for
+// The same by a cluster of C CTAs per (unit, KV head), each with its part of the rows: histograms and
+// counts are read from one another's shared memory and every CTA finds the same digits. The lists go
+// to global memory; a kept row past keep leaves its weight and position in the out arrays at its own
+// place, for the kernel that moves it.
+__global__ void __launch_bounds__(kEvThreads) evict_cluster_kernel(EvictArgs a, EvictLists ls, int C) {
+  extern __shared__ __align__(16) uint32_t ev_dyn[];
+  __shared__ uint32_t hist[2][kEvBins], sum[kEvBins];
+  __shared__ EvDigit dg;
+  __shared__ uint32_t tmp[32], equal, free_rows, past_rows;
+  const int part_groups = ((a.cap + 31) / 32 + C - 1) / C;
+  uint32_t* keys = ev_dyn;                       // [32 part_groups]
+  uint32_t* cnt = keys + part_groups * 32;       // [part_groups]
+  uint32_t* kept = cnt + part_groups;            // [part_groups]
+  const int rank = (int)cluster_rank(), ukv = blockIdx.x / C;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+  EvUnit x;
+  pdl_wait();
+  pdl_trigger();
+  if (!evict_unit(a, ukv, &x, rank * nt + tid, C * nt)) {  // (the same for the whole cluster)
+    if (rank == 0 && tid == 0) ls.count[ukv] = 0;
+    return;
+  }
+  // this CTA's rows [r0, r0 + rows)
+  const int keep = x.keep, per = ((x.L + 31) / 32 + C - 1) / C;
+  const int r0 = min(x.L, rank * per * 32), rows = min(x.L, r0 + per * 32) - r0;
+  const int groups = (rows + 31) / 32, span = (rows + nt - 1) / nt * nt;
+  for (int b = tid; b < kEvBins; b += nt) hist[0][b] = hist[1][b] = 0;
+  __syncthreads();
+  constexpr int kU = 8;  // rows in flight per thread
+  for (int j0 = 0; j0 < rows; j0 += kU * nt) {
+    float w[kU];
+    int q[kU];
+#pragma unroll
+    for (int e = 0; e < kU; ++e) {
+      const int j = j0 + e * nt + tid;
+      if (j < rows) {
+        w[e] = x.w[r0 + j];
+        q[e] = x.pos[r0 + j];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kU; ++e) {
+      const int j = j0 + e * nt + tid;
+      if (j < rows) {
+        const int at = q[e] >= 0 ? q[e] : x.seen - (x.L - (r0 + j));
+        const uint32_t k = (long long)at >= x.recent_from ? 0xffffffffu : weight_key(w[e]);
+        keys[j] = k;
+        atomicAdd(&hist[0][k >> 21], 1u);
+      }
+    }
+  }
+  // the digit that the cluster's histograms together give (a barrier before and after its reads)
+  auto digit = [&](const uint32_t* h, int remaining) {
+    cluster_sync_all();
+    for (int b = tid; b < kEvBins; b += nt) {
+      uint32_t s = 0;
+      for (int c = 0; c < C; ++c) s += ld_peer_u32(h + b, c);
+      sum[b] = s;
+    }
+    __syncthreads();
+    find_digit(sum, remaining, dg);
+  };
+  digit(hist[0], keep);
+  uint32_t prefix = (uint32_t)dg.digit << 21;
+  int remaining = keep - dg.above;
+  bool all = dg.in_bin == remaining;  // every key of the bin is kept
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    if (all) break;
+    const int shift = pass == 0 ? 10 : 0;
+    const uint32_t high = pass == 0 ? 0xffe00000u : 0xfffffc00u;
+    const uint32_t bins = pass == 0 ? 2047u : 1023u;
+    uint32_t* h = hist[pass == 0 ? 1 : 0];
+    if (pass == 1) {  // (every CTA has read the first one: each was at a cluster barrier since)
+      for (int b = tid; b < kEvBins; b += nt) h[b] = 0;
+      __syncthreads();
+    }
+    for (int j = tid; j < rows; j += nt) {
+      const uint32_t k = keys[j];
+      if ((k & high) == prefix) atomicAdd(&h[(k >> shift) & bins], 1u);
+    }
+    digit(h, remaining);
+    prefix |= (uint32_t)dg.digit << shift;
+    remaining -= dg.above;
+    all = dg.in_bin == remaining;
+  }
+  // kept: key above prefix, and of those equal the first `remaining` (all: every key from prefix on)
+  if (!all) {
+    for (int j = tid; j < span; j += nt) {
+      const uint32_t m = __ballot_sync(0xffffffffu, j < rows && keys[j] == prefix);
+      if (lane == 0 && j < groups * 32) cnt[j >> 5] = __popc(m);
+    }
+    __syncthreads();
+    const uint32_t mine = scan_counts(cnt, groups, tmp);
+    if (tid == 0) equal = mine;
+    cluster_sync_all();
+    for (int c = 0; c < rank; ++c) remaining -= (int)ld_peer_u32(&equal, c);
+  }
+  for (int j = tid; j < span; j += nt) {
+    const uint32_t k = j < rows ? keys[j] : 0u;
+    bool take = j < rows && (all ? k >= prefix : k > prefix);
+    if (!all) {
+      const uint32_t m = __ballot_sync(0xffffffffu, j < rows && k == prefix);
+      if (j < rows && k == prefix)
+        take = (int)(cnt[j >> 5] + __popc(m & ((1u << lane) - 1u))) < remaining;
+    }
+    const uint32_t t = __ballot_sync(0xffffffffu, take);
+    if (lane == 0 && j < groups * 32) kept[j >> 5] = t;
+  }
+  __syncthreads();
+  // of group g: its rows below keep
+  auto low_rows = [&](int g) {
+    const int left = keep - (r0 + g * 32);
+    return left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
+  };
+  for (int g = tid; g < groups; g += nt) {
+    const uint32_t low = low_rows(g), t = kept[g];
+    cnt[g] = __popc(~t & low) | (__popc(t & ~low) << 16);  // (at most kEvClusterMost of both together)
+  }
+  __syncthreads();
+  const uint32_t mine = scan_counts(cnt, groups, tmp);
+  if (tid == 0) {
+    free_rows = mine & 0xffffu;
+    past_rows = mine >> 16;
+  }
+  cluster_sync_all();
+  int free_at = 0, past_at = 0;
+  for (int c = 0; c < rank; ++c) {
+    free_at += (int)ld_peer_u32(&free_rows, c);
+    past_at += (int)ld_peer_u32(&past_rows, c);
+  }
+  if (rank == C - 1 && tid == 0) ls.count[ukv] = free_at + (int)free_rows;
+  int32_t* dst = ls.dst + (size_t)ukv * ls.most + free_at;
+  int32_t* src = ls.src + (size_t)ukv * ls.most + past_at;
+#pragma unroll 4
+  for (int j = tid; j < rows; j += nt) {
+    const int g = j >> 5, b = j & 31, i = r0 + j;
+    const uint32_t low = low_rows(g), t = kept[g], under = (1u << b) - 1u;
+    const bool k = (t >> b) & 1u;
+    if (k) {
+      if (i < keep && x.from) x.from[i] = i;
+      if (i >= keep) src[(cnt[g] >> 16) + __popc(t & ~low & under)] = i;
+      if (x.wo != x.w) x.wo[i] = x.w[i];
+      const int q = x.pos[i];
+      if (x.po != x.pos || q < 0) x.po[i] = q >= 0 ? q : x.seen - (x.L - i);
+    } else if (i < keep) {
+      dst[(cnt[g] & 0xffffu) + __popc(~t & low & under)] = i;
+    } else {
+      x.wo[i] = 0.f;
+      x.po[i] = -1;
+    }
+  }
+  cluster_sync_all();  // (no CTA ends before its shared memory has been read)
+}
+
+// The same for units of more rows than that holds: 8 bits at a time, the keys made again for
 // each pass, the lists 1024 rows at a time.
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, EvictLists ls) {
   __shared__ EvSmem sm;
@@ -417,7 +580,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
   EvUnit x;
   pdl_wait();
   pdl_trigger();
-  if (!evict_unit(a, ukv, &x)) {
+  if (!evict_unit(a, ukv, &x, tid, kEvThreads)) {
     if (tid == 0) ls.count[ukv] = 0;
     return;
   }
@@ -480,11 +643,14 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
       sm.base[1] = (int)(y >> 32) + (mover ? 1 : 0);
       sm.in_bin = (int)e + (eq ? 1 : 0);
     }
-    if (kept && i < keep) {
-      if (x.from) x.from[i] = i;
+    if (kept) {
+      if (i < keep && x.from) x.from[i] = i;
       const int p = x.position(i);
       x.wo[i] = x.w[i];
       x.po[i] = p;
+    } else if (i >= keep && i < L) {
+      x.wo[i] = 0.f;
+      x.po[i] = -1;
     }
     __syncthreads();
     free_before += sm.base[0];
@@ -492,7 +658,6 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(EvictArgs a, E
     eq_before += sm.in_bin;
     __syncthreads();
   }
-  evict_finish(x, dst, src, past_before, [&](int i) { return x.w[i]; }, [&](int i) { return x.position(i); });
   if (tid == 0) ls.count[ukv] = past_before;
 }
 
@@ -504,34 +669,73 @@ __global__ void __launch_bounds__(kEvMoveThreads) evict_move_kernel(EvictArgs a,
   move_rows<4>(a, ukv, ls.dst + (size_t)ukv * ls.most, ls.src + (size_t)ukv * ls.most,
                blockIdx.y * kEvMoveWarps + (threadIdx.x >> 5), gridDim.y * kEvMoveWarps,
                ls.count[ukv]);
+  // their weights and positions, which the select left in the out arrays
+  const size_t row0 = (size_t)ukv * a.cap, list = (size_t)ukv * ls.most;
+  for (int m = blockIdx.y * kEvMoveThreads + threadIdx.x; m < ls.count[ukv]; m += gridDim.y * kEvMoveThreads) {
+    const int d = ls.dst[list + m], s = ls.src[list + m];
+    const float w = a.weights_out[row0 + s];
+    const int p = a.pos_out[row0 + s];
+    a.weights_out[row0 + d] = w;
+    a.pos_out[row0 + d] = p;
+    a.weights_out[row0 + s] = 0.f;
+    a.pos_out[row0 + s] = -1;
+    if (a.src_rows) a.src_rows[(size_t)ukv * a.keep + d] = s;
+  }
+}
+
+// CTAs of a cluster: more while the GPU has SMs for them and each has rows to work on (32 units of up
+// to 32K rows: one CTA each 44.6 us, two 37.8, four 31.7, eight, more than there are SMs, 58.5), and as
+// many as shared memory asks for (8 units of 131072 rows: clusters 41 us, evict_select_kernel 402);
+// 0: more than kEvMaxCluster.
+static int evict_cluster(int units, int cap) {
+  int c = 1;
+  while (c < kEvMaxCluster && (long long)units * 2 * c <= device_sm_count() && cap / (2 * c) >= kEvClusterRows)
+    c *= 2;
+  while (c <= kEvMaxCluster && (cap + c - 1) / c > kEvClusterMost) c *= 2;
+  return c <= kEvMaxCluster ? c : 0;
+}
+
+static cudaError_t launch_cluster(const EvictArgs& a, const EvictLists& ls, int c, cudaStream_t s) {
+  const size_t groups = ((a.cap + 31) / 32 + c - 1) / c, smem = groups * (32 + 2) * 4;
+  const cudaError_t e = ensure_dyn_smem((const void*)evict_cluster_kernel, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.n * a.n_kv) * c);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_cluster_kernel, a, ls, c);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const EvictLists ls = lists_of(a);
   const int units = a.n * a.n_kv;
-  cudaError_t e;
-  // With a CTA for every SM, each moves its own rows; fewer leave that to a second kernel.
-  const bool fused = a.cap <= kEvSmemRows && units >= device_sm_count();
-  if (a.cap <= kEvSmemRows) {
+  // With a unit for every SM, one CTA does all of it (256 units of 4352 rows: 26 us, as clusters and moves
+  // apart 42); fewer are spread over clusters, and their rows moved by a second kernel.
+  if (a.cap <= kEvSmemRows && units >= device_sm_count()) {
     const size_t groups = (a.cap + 31) / 32;
     const bool held = a.cap <= kEvHeldRows;
     const size_t smem = groups * (32 + 2 + (held ? 64 : 0)) * 4;
-    const int threads = held ? 512 : kEvThreads;
-    auto launch = [&](auto kern) {
-      const cudaError_t r = ensure_dyn_smem((const void*)kern, smem);
-      return r != cudaSuccess ? r
-                              : launch_pdl_kernel(kern, dim3(units), dim3(threads), smem, s, a, ls);
-    };
-    if (fused)
-      e = held ? launch(evict_kernel<true, true>) : launch(evict_kernel<true, false>);
-    else
-      e = held ? launch(evict_kernel<false, true>) : launch(evict_kernel<false, false>);
-  } else {
-    e = launch_pdl_kernel(evict_select_kernel, dim3(units), dim3(kEvThreads), 0, s, a, ls);
-  }
-  if (e != cudaSuccess || (fused && lengths_apart(a))) return e;
-  if (fused)
+    const auto kern = held ? evict_kernel<true> : evict_kernel<false>;
+    cudaError_t e = ensure_dyn_smem((const void*)kern, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl_kernel(kern, dim3(units), dim3(held ? 512 : kEvThreads), smem, s, a, ls.most);
+    if (e != cudaSuccess || lengths_apart(a)) return e;
     return launch_pdl_kernel(evict_length_kernel, dim3((a.n + 255) / 256), dim3(256), 0, s, a);
+  }
+  const int c = evict_cluster(units, a.cap);
+  const cudaError_t e =
+      c ? launch_cluster(a, ls, c, s)
+        : launch_pdl_kernel(evict_select_kernel, dim3(units), dim3(kEvThreads), 0, s, a, ls);
+  if (e != cudaSuccess) return e;
   const int rows = 4 * kEvMoveWarps * (a.row_bytes[2] ? 3 : 1);  // of a CTA at a time
   int y = (ls.most + rows - 1) / rows;
   y = y < 1 ? 1 : (y > 1024 ? 1024 : y);

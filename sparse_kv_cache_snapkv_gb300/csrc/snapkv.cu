@@ -498,23 +498,6 @@ constexpr int kSelCBins = 2048;
 constexpr int kSelCMaxSpan = 20480;   // positions per CTA (beyond: the one-CTA select)
 constexpr int kSelCMaxRadius = 255;   // pooling radius (beyond: the one-CTA select)
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-// 32-bit word at `local` (a shared address of this CTA) in the shared memory of CTA `rank`.
-__device__ __forceinline__ uint32_t ld_peer_u32(const void* local, uint32_t rank) {
-  uint32_t addr, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 struct SelCSmem {  // after the dynamic key / score arrays
   uint32_t hist[kSelCBins];
   unsigned long long tmp[33];

@@ -524,6 +524,40 @@ def test_evict_many_and_long(rkv, n, n_kv, cap, lens, keep, recent, kv4):
                 assert torch.equal(now[u, g, m:].view(torch.uint8), was[u, g, m:].view(torch.uint8))
 
 
+@pytest.mark.parametrize("n,n_kv,cap,lens,keep", [
+    (1, 1, 2047, [2047], 1000), (1, 1, 2048, [2048], 1), (3, 1, 4100, [4100, 33, 3000], 2999),
+    (2, 1, 40000, [40000, 70], 60),                       # a unit that leaves most of its CTAs none
+    (1, 3, 70001, [70001], 70000), (20, 1, 8191, [8191 - 31 * u for u in range(20)], 5000),
+    (1, 1, 261888, [261888], 130000), (1, 1, 261889, [261889], 130000),  # the most rows of a cluster
+    (160, 1, 41000, [41000 if u == 7 else u for u in range(160)], 500),
+])
+@pytest.mark.parametrize("equal", [False, True])
+def test_evict_over_clusters(rkv, n, n_kv, cap, lens, keep, equal):
+    w, pos = _evict_case(n, n_kv, cap, lens, keep, 135)
+    if equal:
+        w[:, :, 1::2] = w[:, :, :1]
+    seen = [t + 50 for t in lens]
+    k = torch.arange(n * n_kv * cap, device="cuda").view(n, n_kv, cap, 1).expand(-1, -1, -1, 8)
+    rows = [torch.zeros(n, n_kv, cap, x, dtype=torch.uint8, device="cuda") for x in (64, 8, 64, 8)]
+    rows[1].copy_((k >> torch.arange(0, 64, 8, device="cuda")) & 0xff)  # each row its own number
+    was = rows[1].clone()
+    length, win, pin = _ints(lens), w.clone(), pos.clone()
+    recent = min(16, keep)
+    rkv.rkv_check_status(rkv.rkv_evict_kv4(*rows, length, win, pin, _ints(seen), keep, recent, length, win,
+                                           pin))
+    assert length.tolist() == [min(t, keep) for t in lens]
+    for u, t in enumerate(lens):
+        m = min(t, keep)
+        for g in range(n_kv):
+            want, at = C.evict(_f64(w[u, g, :t]), _np(pos[u, g, :t]), seen[u], keep, recent)
+            ix = torch.tensor(want, device="cuda", dtype=torch.long)
+            assert torch.equal(win[u, g, :m], w[u, g, ix]) and np.array_equal(_np(pin[u, g, :m]), at)
+            assert (win[u, g, m:t] == 0).all() and (pin[u, g, m:t] == -1).all()
+            assert torch.equal(win[u, g, t:], w[u, g, t:]) and torch.equal(pin[u, g, t:], pos[u, g, t:])
+            assert torch.equal(rows[1][u, g, :m], was[u, g, ix])
+            assert torch.equal(rows[1][u, g, m:], was[u, g, m:])
+
+
 def test_evict_special_weights(rkv):
     """Zeros of either sign tie, infinities and NaN are largest, the newest rows come first."""
     w = torch.tensor([0.0, -0.0, float("nan"), 1.0, float("inf"), 2.0, 0.0, 0.0], device="cuda").view(1, 1, 8)
