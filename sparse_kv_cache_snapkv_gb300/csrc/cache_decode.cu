@@ -165,15 +165,16 @@ static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
 }
 
 struct CacheScratch {
-  size_t units, lse, part_ml, part_o, logits, total;
+  size_t units, ml, cs, part_ml, part_o, logits, total;
 };
 static CacheScratch cache_scratch(int n, int n_kv, int gqa, int cap, bool with_weights) {
   const size_t units = (size_t)n * n_kv;
   const size_t slots = 2 * (size_t)cache_decode_ctas(n, n_kv, cap, false);  // (never fewer than 4 bits')
   CacheScratch c;
   c.units = 0;
-  c.lse = align_up(((size_t)n + 1) * sizeof(CdUnit), 256);
-  c.part_ml = c.lse + align_up(units * gqa * 4, 256);
+  c.ml = align_up(((size_t)n + 1) * sizeof(CdUnit), 256);
+  c.cs = c.ml + align_up(units * gqa * 8, 256);
+  c.part_ml = c.cs + align_up(units * gqa * 4, 256);
   c.part_o = c.part_ml + align_up(slots * gqa * 8, 256);
   c.logits = c.part_o + align_up(slots * gqa * kHeadDim * 4, 256);
   c.total = c.logits + (with_weights ? align_up(units * cap * gqa * 4, 256) : 0);
@@ -188,7 +189,8 @@ void cache_decode_carve(CacheDecodeArgs* a, void* scratch) {
   unsigned char* p = static_cast<unsigned char*>(scratch);
   const CacheScratch c = cache_scratch(a->n, a->n_kv, a->gqa, a->cap, a->weights != nullptr);
   a->unit = reinterpret_cast<CdUnit*>(p + c.units);
-  a->lse = reinterpret_cast<float*>(p + c.lse);
+  a->ml = reinterpret_cast<float*>(p + c.ml);
+  a->cs = reinterpret_cast<float*>(p + c.cs);
   a->part_ml = reinterpret_cast<float*>(p + c.part_ml);
   a->part_o = reinterpret_cast<float*>(p + c.part_o);
   a->logits = reinterpret_cast<float*>(p + c.logits);
@@ -434,6 +436,8 @@ __device__ __forceinline__ int out_dim(int x) {
 constexpr float kCdLazy = 8.0f;
 template <bool KV4>
 constexpr float kCdShift = KV4 ? 7.0f : 0.0f;
+template <bool KV4>
+constexpr float kCdUnshift = KV4 ? 0x1p-7f : 1.0f;  // (a part's O and sum carry the shift)
 
 // A warp's softmax state: maxima and sums of heads 2 c and 2 c + 1 (the sums per lane), O^T.
 struct CdState {
@@ -446,19 +450,14 @@ struct CdState {
   }
 };
 
-// NT tiles' products -> their probabilities, after the maximum has followed. Logits (log2 domain,
-// rows past the end -inf) are kept for the weights at `logits`, which is the step's first row.
+// NT tiles' products -> their probabilities, after the maximum has followed. The products (their
+// factors cs make logits in the log2 domain of them; rows past the end -inf) are kept for the weights
+// at `logits`, which is the step's first row. cs meets them only in a multiply-add with the maximum:
+// a product rounded by itself would be off by 2^-24 of a logit, not of a difference of two.
 template <int G, bool KV4, int NT>
 __device__ __forceinline__ void softmax_step(CdState& st, float (&s)[NT][4], const float (&cs)[2],
                                              int left, int r, int c, float* logits) {
   const int ta = frag_token(r);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    s[n][0] *= cs[0];
-    s[n][1] *= cs[1];
-    s[n][2] *= cs[0];
-    s[n][3] *= cs[1];
-  }
   if (left < NT * kCdTile) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -485,6 +484,8 @@ __device__ __forceinline__ void softmax_step(CdState& st, float (&s)[NT][4], con
     m0 = fmaxf(m0, fmaxf(s[n][0], s[n][2]));
     m1 = fmaxf(m1, fmaxf(s[n][1], s[n][3]));
   }
+  m0 *= cs[0];
+  m1 *= cs[1];
   if (__any_sync(0xffffffffu, m0 > st.m[0] + kCdLazy || m1 > st.m[1] + kCdLazy)) {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
@@ -509,10 +510,10 @@ __device__ __forceinline__ void softmax_step(CdState& st, float (&s)[NT][4], con
   const float b0 = kCdShift<KV4> - st.m[0], b1 = kCdShift<KV4> - st.m[1];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    s[n][0] = fast_exp2(s[n][0] + b0);
-    s[n][1] = fast_exp2(s[n][1] + b1);
-    s[n][2] = fast_exp2(s[n][2] + b0);
-    s[n][3] = fast_exp2(s[n][3] + b1);
+    s[n][0] = fast_exp2(fmaf(s[n][0], cs[0], b0));
+    s[n][1] = fast_exp2(fmaf(s[n][1], cs[1], b1));
+    s[n][2] = fast_exp2(fmaf(s[n][2], cs[0], b0));
+    s[n][3] = fast_exp2(fmaf(s[n][3], cs[1], b1));
     st.l[0] += s[n][0] + s[n][2];
     st.l[1] += s[n][1] + s[n][3];
   }
@@ -531,13 +532,14 @@ __device__ __forceinline__ CdUnit unit_of(const CacheDecodeArgs& a, int u, long 
   return CdUnit{at, L, append ? l + 1 : l, l < 0 || l > a.cap || (a.new_k && !append), 0};
 }
 
-// -(m + log2 l), to be added to a logit (log2 domain) of the same head; no tokens: no weight
-__device__ __forceinline__ float neg_lse(float m, float l) {
-  return l > 0.f ? -(m + log2f(l)) : (l == 0.f ? -INFINITY : l);
-}
+// What a head's probabilities are divided by: 1 / l, no weight where there are no tokens.
+__device__ __forceinline__ float over(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
 
-// kCdWeightChunk tokens' weights from their logits and the heads' neg_lse; the loads can be on their
-// way before those are known.
+// kCdWeightChunk tokens' weights 2^(cs x - m) / l from their products x and what is known of the heads;
+// the loads can be on their way before that is.
+struct CdHead {
+  float cs, m, over;
+};
 template <int G>
 struct CdWeights {
   static constexpr int kU = kCdWeightChunk / kCdThreads;  // tokens of a thread
@@ -565,17 +567,17 @@ struct CdWeights {
       }
     }
   }
-  __device__ __forceinline__ void add(const float* nlse, float* weights, int t0, int L) const {
-    float nl[G];
+  __device__ __forceinline__ void add(const CdHead* head, float* weights, int t0, int L) const {
+    CdHead hd[G];
 #pragma unroll
-    for (int h = 0; h < G; ++h) nl[h] = nlse[h];
+    for (int h = 0; h < G; ++h) hd[h] = head[h];
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
       const int t = t0 + k * kCdThreads + (int)threadIdx.x;
       if (t < L) {
         float s = 0.f;
 #pragma unroll
-        for (int h = 0; h < G; ++h) s += fast_exp2(x[k][h] + nl[h]);
+        for (int h = 0; h < G; ++h) s = fmaf(fast_exp2(fmaf(x[k][h], hd[h].cs, -hd[h].m)), hd[h].over, s);
         weights[t] = w[k] + s;
       }
     }
@@ -828,6 +830,15 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       __syncthreads();
     }
 
+    // (a factor of zero would make NaN of a masked product; below this every logit is zero)
+    cs[0] = fmaxf(cs[0], 0x1p-126f);
+    cs[1] = fmaxf(cs[1], 0x1p-126f);
+    if (a.weights && round == 0 && warp == 0 && r == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * c + e < G) a.cs[(size_t)ukv * G + 2 * c + e] = cs[e];
+    }
+
     CdState st;
     st.clear();
     float* logits = a.weights ? a.logits + ((size_t)ukv * a.cap + t0) * G : nullptr;
@@ -897,7 +908,6 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
         f[w] = fast_exp2(mg.m[w][h] - M);
         S = fmaf(mg.l[w][h], f[w], S);
       }
-      M -= kCdShift<KV4>;  // p was 2^(s - m + shift)
       const float inv = S == 0.f ? 0.f : 1.f / S;
 #pragma unroll
       for (int i0 = 0; i0 < G * kHeadDim; i0 += kCdThreads) {
@@ -914,7 +924,7 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
       }
       if (tid < G) {
         if (whole)
-          a.lse[(size_t)ukv * G + tid] = neg_lse(M, S);
+          reinterpret_cast<float2*>(a.ml)[(size_t)ukv * G + tid] = make_float2(M, S * kCdUnshift<KV4>);
         else
           reinterpret_cast<float2*>(a.part_ml)[slot * G + tid] = make_float2(M, S);
       }
@@ -941,7 +951,8 @@ template <int G, bool KV4>
 __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs a, int ctas) {
   __shared__ float4 sums[kCdThreads];
   __shared__ float factor[kCdFactors * G];
-  __shared__ float total_s[8], top[8], nlse[8];
+  __shared__ float total_s[8], top[8];
+  __shared__ CdHead head[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ukv = blockIdx.x, u = ukv / a.n_kv, g = ukv - u * a.n_kv;
   // (no early trigger: the next launch's CTAs would wait in these CTAs' places, 1021 tokens 8.4 us
@@ -971,7 +982,10 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
   const int i0 = part_of(total, ctas, z0), parts = part_of(total, ctas, z0 + R - 1) - i0 + 1;
   if (parts == 1) {  // (its outputs are written)
     if (blockIdx.y == 0) return;
-    if (tid < G) nlse[tid] = a.lse[(size_t)ukv * G + tid];
+    if (tid < G) {
+      const float2 x = reinterpret_cast<const float2*>(a.ml)[(size_t)ukv * G + tid];
+      head[tid] = CdHead{a.cs[(size_t)ukv * G + tid], x.x, over(x.y)};
+    }
   }
   const size_t s0 = 2 * (size_t)i0 + (part_begin(total, ctas, i0) == z0 ? 0 : 1);
   auto slot_of = [&](int k) { return k == 0 ? s0 : 2 * (size_t)(i0 + k); };
@@ -993,16 +1007,16 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
     if (lane == 0) {
       total_s[warp] = S;
       top[warp] = M;
-      nlse[warp] = neg_lse(M, S);
+      if (blockIdx.y > 0) head[warp] = CdHead{a.cs[(size_t)ukv * G + warp], M, over(S * kCdUnshift<KV4>)};
     }
   }
   __syncthreads();
   if (blockIdx.y > 0) {
-    cw.add(nlse, weights, t0, L);
+    cw.add(head, weights, t0, L);
     const int step = ((int)gridDim.y - 1) * kCdWeightChunk;
     for (t0 += step; t0 < L; t0 += step) {
       cw.load(logits, weights, t0, L);
-      cw.add(nlse, weights, t0, L);
+      cw.add(head, weights, t0, L);
     }
     return;
   }

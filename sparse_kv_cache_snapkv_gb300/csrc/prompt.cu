@@ -15,7 +15,7 @@
 // tensor cores. Stationary tiles of 256 rows halve the streamed bytes per product against 128.
 //
 // A CTA is persistent over work items (a stationary tile, or one split of its stream), largest
-// first. One thread loads (TMA), one issues the products, eight warps read the accumulators: two
+// first. One thread loads (TMA), one issues the products, sixteen warps read the accumulators: two
 // of 128 rows, each double-buffered in TMEM (512 columns), so that the exponentials of one tile run
 // under the products of the next.
 #include <cuda.h>
@@ -445,7 +445,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         named_bar_sync(1, kPrEpi);  // xch is rewritten by the next item
       } else {
         const int key = it.tile * kPrStat + srow;
-        uint64_t acc[2] = {0ull, 0ull};
+        // A key's sum over many tiles is a compensated one (sum - lost): an early key of a long prompt
+        // has tens of thousands of weights added, each of which a plain sum would round at its size.
+        const uint64_t minus = pack2(-1.f, -1.f);
+        uint64_t acc[2], sum = 0ull, lost = 0ull;
         uint32_t r[2][32];
         auto chunk = [&](uint32_t (&x)[32], int tile, bool mask, int base, const float* nl) {
           if (mask) {
@@ -507,6 +510,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             nphase ^= 1u;
           }
           const int b = step & 1;
+          acc[0] = acc[1] = 0ull;
           // a tile with rows that are no queries, or that do not see all of the stationary keys
           const int x = ti;
           const int last = HEADS ? ti * kPrTile + kPrTile : p.max_q;  // queries below `last`
@@ -517,12 +521,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           chunk(r[0], x, mask, c0, nl);
           tmem_ld_wait(r[1]);
           chunk(r[1], x, mask, c0 + 32, nl);
+          const uint64_t y = fma2(lost, minus, add2(acc[0], acc[1])), now = add2(sum, y);
+          lost = fma2(y, minus, fma2(sum, minus, now));
+          sum = now;
           // (the log-sum-exps are read before this too: their slot is free with the accumulator)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[b]);
         }
-        const float2 s = unpack2(add2(acc[0], acc[1]));
+        const float2 s = unpack2(sum);
         // the two threads of a key add to it one after the other (shared memory is full)
         const bool one = p.nsplit2 == 1;
         const int split = (i % (p.units * p.nsplit2)) % p.nsplit2;

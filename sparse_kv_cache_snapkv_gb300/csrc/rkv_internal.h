@@ -241,7 +241,8 @@ struct CacheDecodeArgs {
   bf16* out;
   float* weights;      // nullptr: not asked for
   CdUnit* unit;        // workspace [n + 1]: what the first kernel found, for the second
-  float* lse;          // workspace [n*n_kv][gqa]: negated log-sum-exps (log2 domain)
+  float* ml;           // workspace [n*n_kv][gqa][2]: maximum (log2 domain) and sum, where one CTA has all
+  float* cs;           // workspace [n*n_kv][gqa]: what makes a logit of a kept product
   float* part_ml;      // workspace [2 per CTA][gqa][2]: maxima and sums of a part
   float* part_o;       // workspace [2 per CTA][gqa][128]
   float* logits;       // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
