@@ -6,8 +6,12 @@
 //   weights_j += sum_h p_hj / l_h
 // in one pass over K and V: each warp takes 16 tokens at a time with a running maximum and sum;
 // the warps of a CTA, then the CTAs of a split sequence, are joined. The weights need the final
-// sums, so the logits (4 G bytes per token against 144 or 512 of K and V) are kept in the
+// sums, so the products (4 G bytes per token against 144 or 512 of K and V) are kept in the
 // workspace and turned into weights once those are known.
+//
+// Measured against the bytes at the copy rate: 32 units of 32K in 4 bits, 8 heads, G = 4, with weights
+// 231 us of 188; one unit of 131071 tokens 39 of 23.5; 16 ragged paged units of up to 20K, 4 heads,
+// G = 8, 37 of 18; 16 ragged bf16 units of up to 32K with weights 229 of 208.
 //
 // Both products run on mma.sync m16n8k16 with the tokens (S^T = K Q^T) or the dimensions
 // (O^T = V^T P^T) as the 16 rows and the query heads as the 8 columns: no row of the tile is
@@ -136,7 +140,7 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
 // takes the i-th of C equal parts of it, whatever the lengths are. A part is a run of segments, each
 // within one (unit, KV head); only its first and its last can be shared with other CTAs, so two
 // slots of partial results per CTA are enough. A second kernel joins the parts in their order, turns
-// the logits into weights and moves the lengths on, after every reader; nothing in the workspace has
+// the kept products into weights and moves the lengths on, after every reader; nothing in the workspace has
 // to hold anything before a call. (A CTA that came last at a counter could join in place: 32 units of
 // 32K with weights took 242 us so, 231 as here, and the counters had to be zero before a call.)
 constexpr int kCdThreads = 256;

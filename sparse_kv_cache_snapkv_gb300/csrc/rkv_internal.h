@@ -245,7 +245,7 @@ struct CacheDecodeArgs {
   float* cs;           // workspace [n*n_kv][gqa]: what makes a logit of a kept product
   float* part_ml;      // workspace [2 per CTA][gqa][2]: maxima and sums of a part
   float* part_o;       // workspace [2 per CTA][gqa][128]
-  float* logits;       // workspace [n*n_kv][cap][gqa], log2 domain (with weights)
+  float* logits;       // workspace [n*n_kv][cap][gqa]: the kept products (with weights)
   uint32_t* status;
   bool kv4;
 };
