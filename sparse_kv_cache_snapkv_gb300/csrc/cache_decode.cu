@@ -10,8 +10,8 @@
 // workspace and turned into weights once those are known.
 //
 // Measured against the bytes at the copy rate: 32 units of 32K in 4 bits, 8 heads, G = 4, with weights
-// 231 us of 188; one unit of 131071 tokens 39 of 23.5; 16 ragged paged units of up to 20K, 4 heads,
-// G = 8, 37 of 18; 16 ragged bf16 units of up to 32K with weights 229 of 208.
+// 233 us of 188; one unit of 131071 tokens 39.6 of 23.5; 16 ragged paged units of up to 20K, 4 heads,
+// G = 8, 39 of 18; 16 ragged bf16 units of up to 32K with weights 229 of 208.
 //
 // Both products run on mma.sync m16n8k16 with the tokens (S^T = K Q^T) or the dimensions
 // (O^T = V^T P^T) as the 16 rows and the query heads as the 8 columns: no row of the tile is
@@ -332,13 +332,34 @@ __device__ __forceinline__ void scores_kv4(const Kv4Tile* t, const uint2 (&q)[8]
   }
 }
 
-// O^T += V^T P^T; p are the probabilities of this lane's S^T entries. P in fp16 (11 significant
-// bits, at most 2^15: see kCdShift), V exact in fp16.
+// With at most four heads, columns 4 to 7 of the fragments hold the heads of columns 0 to 3 once more.
+template <int G>
+constexpr bool kCdTwice = G <= 4;
+
+// O^T += V^T P^T; p are the probabilities of this lane's S^T entries (at most 2^15: see kCdShift).
+// V is exact in fp16; P is the sum of two fp16 numbers (22 significant bits), as the bf16 form's is of
+// two bf16: the first alone left the outputs off by up to 2^-11 of sum_j p_j |v_j|, which shows where
+// they cancel. The second numbers are in columns 4 to 7 where those repeat the heads (32 units of 32K,
+// G = 4: 233.1 us; P in one fp16 232.7, a second product 245.1), else in a product of their own (16 ragged
+// paged units, G = 8: 39.1 us, P in one fp16 36.6).
+template <int G>
 __device__ __forceinline__ void accumulate_kv4(const Kv4Tile* t, const float (&p)[4], int r, int c,
                                                float (&o)[8][4]) {
-  const __half2 p0 = __floats2half2_rn(p[0], p[1]), p1 = __floats2half2_rn(p[2], p[3]);
+  __half2 p0 = __floats2half2_rn(p[0], p[1]), p1 = __floats2half2_rn(p[2], p[3]);
+  const float2 f0 = __half22float2(p0), f1 = __half22float2(p1);
+  const __half2 l0 = __floats2half2_rn(p[0] - f0.x, p[1] - f0.y);
+  const __half2 l1 = __floats2half2_rn(p[2] - f1.x, p[3] - f1.y);
+  if (kCdTwice<G> && c >= 2) {
+    p0 = l0;
+    p1 = l1;
+  }
   const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
   const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+  uint32_t c0 = 0u, c1 = 0u;
+  if (!kCdTwice<G>) {
+    c0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&l0));
+    c1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&l1));
+  }
   const int t0 = frag_token(2 * c), t1 = frag_token(2 * c + 1);
   const uint8_t* v0 = t->v + t0 * kCodeBytes + 16 * ((r >> 1) ^ ((t0 >> 1) & 2)) + 8 * (r & 1);
   const uint8_t* v1 = t->v + t1 * kCodeBytes + 16 * ((r >> 1) ^ ((t1 >> 1) & 2)) + 8 * (r & 1);
@@ -358,9 +379,12 @@ __device__ __forceinline__ void accumulate_kv4(const Kv4Tile* t, const float (&p
     codes_to_half2((w2 & m) | ((w3 << 4) & ~m), e23);
     codes_to_half2(((w2 >> 4) & m) | (w3 & ~m), d23);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      mma16816<true>(o[4 * w + e], hmul2(e01[e], s01), hmul2(d01[e], s01), hmul2(e23[e], s23),
-                     hmul2(d23[e], s23), b0, b1);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t a0 = hmul2(e01[e], s01), a1 = hmul2(d01[e], s01);
+      const uint32_t a2 = hmul2(e23[e], s23), a3 = hmul2(d23[e], s23);
+      mma16816<true>(o[4 * w + e], a0, a1, a2, a3, b0, b1);
+      if (!kCdTwice<G>) mma16816<true>(o[4 * w + e], a0, a1, a2, a3, c0, c1);
+    }
   }
 }
 
@@ -794,17 +818,18 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
     };
     if (KV4) fetch(t0, 0);
 
-    // Q fragments: lane (r, c) holds head r. 4 bits: fp16, each head scaled by a power of two that
-    // puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it is exact, and
-    // what is lost below is far under the fp32 rounding of the sum.
+    // Q fragments: lane (r, c) holds head r (kCdTwice: r % 4). 4 bits: fp16, each head scaled by a
+    // power of two that puts its largest value in [2^8, 2^9): then every bf16 value down to 2^-25 of it
+    // is exact, and what is lost below is far under the fp32 rounding of the sum.
     uint2 q[KV4 ? 8 : 1];
     float cs[2] = {a.scale_log2, a.scale_log2};  // logit scale of heads 2 c, 2 c + 1
-    const bf16* qr = a.q + ((size_t)ukv * G + r) * kHeadDim;
+    const int hr = KV4 && kCdTwice<G> ? r & 3 : r;
+    const bf16* qr = a.q + ((size_t)ukv * G + hr) * kHeadDim;
     if (KV4) {
       float amax = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        q[j] = r < G ? *reinterpret_cast<const uint2*>(qr + 32 * c + 4 * j) : make_uint2(0u, 0u);
+        q[j] = hr < G ? *reinterpret_cast<const uint2*>(qr + 32 * c + 4 * j) : make_uint2(0u, 0u);
         amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j].x)), fabsf(bf16_hi(q[j].x))));
         amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j].y)), fabsf(bf16_hi(q[j].y))));
       }
@@ -858,8 +883,8 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
         scores_kv4(t + 1, reinterpret_cast<const uint2(&)[8]>(q), r, c, s[1]);
         softmax_step<G, true, 2>(st, s, cs, te - t0, r, c, logits);
         if (logits) logits += kRound * G;
-        accumulate_kv4(t, s[0], r, c, st.o);
-        accumulate_kv4(t + 1, s[1], r, c, st.o);
+        accumulate_kv4<G>(t, s[0], r, c, st.o);
+        accumulate_kv4<G>(t + 1, s[1], r, c, st.o);
       }
     } else {
       BfTile t;
@@ -920,7 +945,8 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
         const int at = (2 * jh + (h & 1)) * kCdORow + 4 * row + (h >> 1);  // 4 j + e, e = 2 hi + h % 2
         float O = 0.f;
 #pragma unroll
-        for (int w = 0; w < kCdWarps; ++w) O = fmaf(mg.o[w][at], f[w], O);
+        for (int w = 0; w < kCdWarps; ++w)
+          O = fmaf(KV4 && kCdTwice<G> ? mg.o[w][at] + mg.o[w][at + 2] : mg.o[w][at], f[w], O);
         if (whole)
           a.out[((size_t)ukv * G + h) * kHeadDim + out_dim<KV4>(x)] = __float2bfloat16_rn(O * inv);
         else
