@@ -4,8 +4,8 @@
  * The kernels never spin without a bound: every wait on an mbarrier gives up after a time limit,
  * records RKV_DEV_WAIT_TIMEOUT in the workspace's status word, lets the copies it already issued
  * land, frees its tensor memory and returns, so that the CUDA context stays usable and the host
- * learns of the failure through rkv_check_status. This hook makes such a wait run out on purpose,
- * without any GPU fault, so that a test can check that path.
+ * learns of the failure through rkv_check_status. The two wait hooks make such a wait run out on
+ * purpose, without any GPU fault, so that a test can check that path.
  */
 #ifndef RKV_TESTING_H_
 #define RKV_TESTING_H_
@@ -31,6 +31,23 @@ rkv_status rkv_testing_scores_wait_timeout(const void* k, const int32_t* seq_len
                                            int head_dim, int max_len, int window, float scale,
                                            float* scores_out, uint64_t wait_limit_ns, void* ws,
                                            size_t ws_bytes, void* stream);
+
+/* rkv_prompt_weights with every mbarrier wait bounded by wait_limit_ns (in [1000, 1e9], instead of
+ * 1 s) and with one load of thread block 0 never requested, by `what`:
+ *   RKV_TESTING_PROMPT_KEYS     the first pass's first tile of keys
+ *   RKV_TESTING_PROMPT_QUERIES  the second pass's first tile of queries
+ *   RKV_TESTING_PROMPT_SUMS     that tile's log-sum-exps
+ * The waits on it (and those on what would follow) run out, block 0 records RKV_DEV_WAIT_TIMEOUT and
+ * returns, every other block completes normally. Arguments and errors as rkv_prompt_weights; the
+ * weights of the units that block 0 serves are not meaningful after such a call. */
+#define RKV_TESTING_PROMPT_KEYS 1
+#define RKV_TESTING_PROMPT_QUERIES 2
+#define RKV_TESTING_PROMPT_SUMS 3
+rkv_status rkv_testing_prompt_wait_timeout(const void* q, const int32_t* q_len, const void* k,
+                                           const int32_t* len, int n, int n_kv, int gqa,
+                                           int head_dim, int max_q, int max_len, float scale,
+                                           float* weights, int what, uint64_t wait_limit_ns,
+                                           void* ws, size_t ws_bytes, void* stream);
 
 /* Shared-memory layout of every later rkv_hybrid_decode call in this process, so that a test
  * can run each on the same inputs (the results do not depend on it; one CTA per (unit, KV head)

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "../../include/rkv.h"
+#include "../../include/rkv_testing.h"
 #include "api_util.h"
 #include "rkv_internal.h"
 
@@ -144,6 +145,41 @@ rkv_status evict_impl(EvictArgs a, int head_dim, void* ws, size_t ws_bytes, void
   return from_cuda(launch_evict(a, as_stream(stream)));
 }
 
+rkv_status prompt_impl(const void* q, const int32_t* q_len, const void* k, const int32_t* len, int n,
+                       int n_kv, int gqa, int head_dim, int max_q, int max_len, float scale,
+                       float* weights, uint64_t wait_limit_ns, int test_skip, void* ws,
+                       size_t ws_bytes, void* stream) {
+  if (head_dim != kHeadDim || gqa > kMaxPromptGqa) return RKV_ERR_UNSUPPORTED;
+  if (!q || !q_len || !k || !len || !weights || !aligned16(q) || !aligned16(k))
+    return RKV_ERR_INVALID_ARG;
+  if (!counts_ok(n, n_kv, gqa) || max_q <= 0 || max_len < max_q || !scale_ok(scale))
+    return RKV_ERR_INVALID_ARG;
+  // a row's index is a 32-bit coordinate of the tensor maps
+  if ((long long)n * n_kv * gqa * max_q > INT_MAX - 512 ||
+      (long long)n * n_kv * max_len > INT_MAX - 512)
+    return RKV_ERR_TOO_LARGE;
+  const rkv_status w =
+      ws_check(ws, ws_bytes, rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len));
+  if (w != RKV_OK) return w;
+  PromptArgs a{};
+  a.q = static_cast<const bf16*>(q);
+  a.q_len = q_len;
+  a.k = static_cast<const bf16*>(k);
+  a.len = len;
+  a.n = n;
+  a.n_kv = n_kv;
+  a.gqa = gqa;
+  a.max_q = max_q;
+  a.max_len = max_len;
+  a.scale_log2 = scale * kLog2e;
+  a.weights = weights;
+  a.scratch = after_status(ws);
+  a.status = status_ptr(ws);
+  a.wait_limit_ns = wait_limit_ns;
+  a.test_skip = test_skip;
+  return from_cuda(launch_prompt_weights(a, as_stream(stream)));
+}
+
 EvictArgs evict_args(const int32_t* len, int32_t* len_out, const float* weights,
                      float* weights_out, const int32_t* pos, int32_t* pos_out,
                      const int32_t* seen, int n, int n_kv, int cap, int keep, int recent,
@@ -261,33 +297,21 @@ rkv_status rkv_prompt_weights(const void* q, const int32_t* q_len, const void* k
                               int max_q, int max_len, float scale, float* weights, void* ws,
                               size_t ws_bytes, void* stream) {
   RKV_TRACE();
-  if (head_dim != kHeadDim || gqa > kMaxPromptGqa) return RKV_ERR_UNSUPPORTED;
-  if (!q || !q_len || !k || !len || !weights || !aligned16(q) || !aligned16(k))
+  return prompt_impl(q, q_len, k, len, n, n_kv, gqa, head_dim, max_q, max_len, scale, weights, 0, 0,
+                     ws, ws_bytes, stream);
+}
+
+rkv_status rkv_testing_prompt_wait_timeout(const void* q, const int32_t* q_len, const void* k,
+                                           const int32_t* len, int n, int n_kv, int gqa,
+                                           int head_dim, int max_q, int max_len, float scale,
+                                           float* weights, int what, uint64_t wait_limit_ns,
+                                           void* ws, size_t ws_bytes, void* stream) {
+  RKV_TRACE();
+  if (what < RKV_TESTING_PROMPT_KEYS || what > RKV_TESTING_PROMPT_SUMS ||
+      wait_limit_ns < 1000ull || wait_limit_ns > 1000000000ull)
     return RKV_ERR_INVALID_ARG;
-  if (!counts_ok(n, n_kv, gqa) || max_q <= 0 || max_len < max_q || !scale_ok(scale))
-    return RKV_ERR_INVALID_ARG;
-  // a row's index is a 32-bit coordinate of the tensor maps
-  if ((long long)n * n_kv * gqa * max_q > INT_MAX - 512 ||
-      (long long)n * n_kv * max_len > INT_MAX - 512)
-    return RKV_ERR_TOO_LARGE;
-  const rkv_status w =
-      ws_check(ws, ws_bytes, rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len));
-  if (w != RKV_OK) return w;
-  PromptArgs a{};
-  a.q = static_cast<const bf16*>(q);
-  a.q_len = q_len;
-  a.k = static_cast<const bf16*>(k);
-  a.len = len;
-  a.n = n;
-  a.n_kv = n_kv;
-  a.gqa = gqa;
-  a.max_q = max_q;
-  a.max_len = max_len;
-  a.scale_log2 = scale * kLog2e;
-  a.weights = weights;
-  a.scratch = after_status(ws);
-  a.status = status_ptr(ws);
-  return from_cuda(launch_prompt_weights(a, as_stream(stream)));
+  return prompt_impl(q, q_len, k, len, n, n_kv, gqa, head_dim, max_q, max_len, scale, weights,
+                     wait_limit_ns, what, ws, ws_bytes, stream);
 }
 
 // ------------------------------------------------------------------------------- eviction

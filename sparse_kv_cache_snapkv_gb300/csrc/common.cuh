@@ -136,6 +136,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The same for a whole, converged warp, with one answer for all of its lanes: each lane has its own
+// reading of the clock, so lanes that decided for themselves could part at the limit, and the warp's
+// collective operations behind the wait would then be left by some of them.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint32_t a = smem_addr(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > limit_ns)) return false;
+  }
+}
+
 // 16-byte asynchronous global -> shared copies (LDGSTS). A thread waits for its own copies with
 // cp_async_wait_all(); a barrier then publishes them to the other threads.
 __device__ __forceinline__ void cp_async16(void* dst_smem, const void* src_gmem) {

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "../../include/rkv_testing.h"
 #include "common.cuh"
 #include "rkv_internal.h"
 #include "tensor_core.cuh"
@@ -90,6 +91,8 @@ struct PromptParams {
   float* part;           // [nsplit2][units][max_len] when nsplit2 > 1
   float* weights;        // [units][max_len]
   uint32_t* status;
+  uint64_t wait_limit_ns;  // bound of every mbarrier wait
+  int test_skip;           // testing only: what CTA 0 never requests (RKV_TESTING_PROMPT_*; 0: nothing)
 };
 
 struct PrSmem {
@@ -232,6 +235,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   pdl_wait();
   pdl_trigger();
   bool aborted = false;
+  const uint64_t limit = p.wait_limit_ns;
+  const int skip = blockIdx.x == 0 ? p.test_skip : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const PromptItem it = prompt_item<PASS>(p, i);
         if (it.count == 0) continue;
         const int sb = ic & 1;
-        if (ic >= 2 && !mbar_wait(&sempty[sb], (uint32_t)(((ic >> 1) - 1) & 1))) {
+        if (ic >= 2 && !mbar_wait(&sempty[sb], (uint32_t)(((ic >> 1) - 1) & 1), limit)) {
           aborted = true;
           break;
         }
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (int t = 0; t < it.count; ++t, ++step) {
           const int s = step % kPrStages;
           if (step >= kPrStages &&
-              !mbar_wait(&empty[s], (uint32_t)(((step / kPrStages) - 1) & 1))) {
+              !mbar_wait(&empty[s], (uint32_t)(((step / kPrStages) - 1) & 1), limit)) {
             aborted = true;
             break;
           }
@@ -274,10 +279,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                                               (x % m2.per_head) * kPrTile
                                         : x * kPrTile;
             const int ns = step % kPrNlSlots;
-            mbar_arrive_expect_tx(&nfull[ns], kPrTile * 4);
-            bulk_load(nl_s + ns * kPrTile, p.nl + (size_t)it.ukv * p.tiles1 * kPrStat + row,
-                      kPrTile * 4, &nfull[ns]);
+            if (skip != RKV_TESTING_PROMPT_SUMS || step > 0) {
+              mbar_arrive_expect_tx(&nfull[ns], kPrTile * 4);
+              bulk_load(nl_s + ns * kPrTile, p.nl + (size_t)it.ukv * p.tiles1 * kPrStat + row,
+                        kPrTile * 4, &nfull[ns]);
+            }
           }
+          if (skip == (PASS == 1 ? RKV_TESTING_PROMPT_KEYS : RKV_TESTING_PROMPT_QUERIES) && step == 0)
+            continue;
           uint8_t* dst = tiles + (size_t)s * kPrTileBytes;
           mbar_arrive_expect_tx(&full[s], (uint32_t)kPrTileBytes);
           tma_load_2d(dst, PASS == 1 ? &kmap : &qmap, 0, y, &full[s]);
@@ -285,14 +294,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         ++ic;
       }
-      if (aborted) {
-        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
-        for (int j = max(0, step - kPrStages); j < step; ++j)  // let issued loads land
-          mbar_wait(&full[j % kPrStages], (uint32_t)((j / kPrStages) & 1));
-        for (int j = max(0, step - kPrNlSlots); PASS == 2 && j < step; ++j)
-          mbar_wait(&nfull[j % kPrNlSlots], (uint32_t)((j / kPrNlSlots) & 1));
-        for (int j = max(0, ic - 2); j < sent; ++j) mbar_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1));
-      }
+      if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+      // every issued load lands before the CTA ends, whoever gave up (else they have, and this is no wait)
+      for (int j = max(0, step - kPrStages); j < step; ++j)
+        mbar_wait(&full[j % kPrStages], (uint32_t)((j / kPrStages) & 1), limit);
+      for (int j = max(0, step - kPrNlSlots); PASS == 2 && j < step; ++j)
+        mbar_wait(&nfull[j % kPrNlSlots], (uint32_t)((j / kPrNlSlots) & 1), limit);
+      for (int j = max(0, ic - 2); j < sent; ++j)
+        mbar_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1), limit);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
@@ -304,15 +313,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const PromptItem it = prompt_item<PASS>(p, i);
         if (it.count == 0) continue;
         const int sb = ic & 1;
-        if (!mbar_wait(&sfull[sb], (uint32_t)((ic >> 1) & 1))) {
+        if (!mbar_wait(&sfull[sb], (uint32_t)((ic >> 1) & 1), limit)) {
           aborted = true;
           break;
         }
         const uint32_t sbase = smem_addr(stat + (size_t)sb * kPrStatBytes);
         for (int t = 0; t < it.count; ++t, ++step) {
           const int s = step % kPrStages, b = step & 1;
-          if (!mbar_wait(&full[s], (uint32_t)((step / kPrStages) & 1)) ||
-              (step >= 2 && !mbar_wait(&tempty[b], (uint32_t)(((step >> 1) - 1) & 1)))) {
+          if (!mbar_wait(&full[s], (uint32_t)((step / kPrStages) & 1), limit) ||
+              (step >= 2 && !mbar_wait(&tempty[b], (uint32_t)(((step >> 1) - 1) & 1), limit))) {
             aborted = true;
             break;
           }
@@ -336,7 +345,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         umma_commit(&sempty[sb]);
         ++ic;
       }
-      if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+      if (aborted) {
+        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+        for (int j = max(0, step - 2); j < step; ++j)  // let issued products end
+          mbar_wait(&tfull[j & 1], (uint32_t)((j >> 1) & 1), limit);
+      }
     }
   } else {
     // ------------------------------------------------------------------ accumulators
@@ -403,10 +416,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           l += sum;
         };
-        // waits for a tile's product and starts its first half (started under the half before it,
-        // instead of after that, the loads made the 8K prompt take 513 us instead of 447)
+        // waits for a tile's product (the whole warp goes on or none of it: `aborted` is the same in all
+        // lanes) and starts its first half (started under the half before it, instead of after that, the
+        // loads made the 8K prompt take 513 us instead of 447)
         auto start_tile = [&](int st) {
-          if (!mbar_wait(&tfull[st & 1], (uint32_t)((st >> 1) & 1))) {
+          if (!mbar_wait_warp(&tfull[st & 1], (uint32_t)((st >> 1) & 1), limit)) {
             aborted = true;
             return false;
           }
@@ -485,25 +499,23 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             acc[1] = add2(acc[1], pack2(fast_exp2(y1.x), fast_exp2(y1.y)));
           }
         };
-        // waits for a tile's product and starts its first half
-        auto start_tile = [&](int st) {
-          if (!mbar_wait(&tfull[st & 1], (uint32_t)((st >> 1) & 1))) {
-            aborted = true;
-            return false;
-          }
-          tc_fence_after();
-          tmem_ld32_start(tmem + lane_addr + (uint32_t)((st & 1) * 2 * kPrTile), r[0]);
-          return true;
-        };
         // the streamed tile: its number within its head (or among all rows' tiles), counted along
         int ti = HEADS ? it.q0 + it.first % max(it.span, 1) : it.first;
         for (int t = 0; t < it.count; ++t, ++step, ++ti) {
           if (HEADS && ti == it.q0 + it.span) ti = it.q0;
-          if (aborted || !start_tile(step)) continue;
-          if (!mbar_wait(&nfull[nslot], nphase)) {
+          if (aborted) continue;
+          // the tile's product and its log-sum-exps, both before the first load is started: that would
+          // have to be waited for. One vote where both are there (8K prompt: 1.0 % over lanes that
+          // decide for themselves, with a vote for each 1.5 %).
+          const uint32_t tphase = (uint32_t)((step >> 1) & 1);
+          if (!__all_sync(0xffffffffu, mbar_try_wait(smem_addr(&tfull[step & 1]), tphase) &&
+                                           mbar_try_wait(smem_addr(&nfull[nslot]), nphase)) &&
+              !(mbar_wait_warp(&tfull[step & 1], tphase, limit) && mbar_wait_warp(&nfull[nslot], nphase, limit))) {
             aborted = true;
             continue;
           }
+          tc_fence_after();
+          tmem_ld32_start(tmem + lane_addr + (uint32_t)((step & 1) * 2 * kPrTile), r[0]);
           const float* nl = nl_s + nslot * kPrTile;
           if (++nslot == kPrNlSlots) {
             nslot = 0;
@@ -661,6 +673,8 @@ cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s) {
   p.part = reinterpret_cast<float*>(w + ml_bytes(pl, p.units));
   p.weights = a.weights;
   p.status = a.status;
+  p.wait_limit_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
+  p.test_skip = a.test_skip;
   const bool heads = row_map(a.gqa, a.max_q, kPrTile).per_head != 0;
   cudaError_t e = heads ? launch_prompt_pass<1, true>(km, qm, p, s)
                         : launch_prompt_pass<1, false>(km, qm, p, s);

@@ -267,6 +267,8 @@ struct PromptArgs {
   float* weights;
   void* scratch;  // workspace after the status word
   uint32_t* status;
+  uint64_t wait_limit_ns;  // 0: the default bound of every mbarrier wait (1 s)
+  int test_skip;           // testing only (rkv_testing_prompt_wait_timeout)
 };
 size_t prompt_scratch_bytes(int n, int n_kv, int gqa, int max_q, int max_len);
 cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s);

@@ -38,7 +38,7 @@ SYMBOLS = [
     "rkv_kv4_decode_workspace_bytes", "rkv_kv4_decode", "rkv_kv4_decode_paged",
     "rkv_dense_decode_weights_workspace_bytes", "rkv_dense_decode_weights",
     "rkv_prompt_weights_workspace_bytes", "rkv_prompt_weights", "rkv_evict_workspace_bytes",
-    "rkv_evict", "rkv_evict_kv4",
+    "rkv_evict", "rkv_evict_kv4", "rkv_testing_prompt_wait_timeout",
 ]
 
 
@@ -132,6 +132,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "rkv_prompt_weights_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
         "rkv_prompt_weights": ([vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz,
                                 vp], i32),
+        "rkv_testing_prompt_wait_timeout": ([vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp,
+                                             i32, ctypes.c_uint64, vp, sz, vp], i32),
         "rkv_evict_workspace_bytes": ([i32, i32, i32, i32], sz),
         "rkv_evict": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp,
                        sz, vp], i32),
@@ -733,18 +735,30 @@ def rkv_prompt_weights_workspace_bytes(n: int, n_kv: int, gqa: int, max_q: int,
     return int(load().rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len))
 
 
-def rkv_prompt_weights(q, q_len, k, length, scale: float, weights, ws=None, stream=None):
-    """Adds the softmax weight that every key gets from the last q_len[u] positions' queries
-    (q [n][Hq][max_q][128]) to weights [n][n_kv][max_len] fp32; see include/rkv.h."""
+def _prompt(fn, hook, q, q_len, k, length, scale, weights, ws, stream):
     n, n_kv, max_len, d = shape = _dims(k, "k", 4)
     _, hq, max_q, _ = _dims(q, "q", 4)
     gqa, dev = _group(hq, n_kv), q.get_device()
     args = (_at(q, "q", _BF16, (n, hq, max_q, d), dev), _at(q_len, "q_len", _I32, (n,), dev),
             _at(k, "k", _BF16, shape, dev), _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d,
-            max_q, max_len, scale, _at(weights, "weights", _F32, (n, n_kv, max_len), dev))
-    return _call("rkv_prompt_weights", args, ws,
+            max_q, max_len, scale, _at(weights, "weights", _F32, (n, n_kv, max_len), dev), *hook)
+    return _call(fn, args, ws,
                  lambda: rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len), dev,
                  stream)
+
+
+def rkv_prompt_weights(q, q_len, k, length, scale: float, weights, ws=None, stream=None):
+    """Adds the softmax weight that every key gets from the last q_len[u] positions' queries
+    (q [n][Hq][max_q][128]) to weights [n][n_kv][max_len] fp32; see include/rkv.h."""
+    return _prompt("rkv_prompt_weights", (), q, q_len, k, length, scale, weights, ws, stream)
+
+
+def rkv_testing_prompt_wait_timeout(q, q_len, k, length, scale: float, weights, what: int,
+                                    wait_limit_ns: int, ws=None, stream=None):
+    """Test hook (include/rkv_testing.h): rkv_prompt_weights with one load of block 0 never
+    requested, so that its bounded waits run out after wait_limit_ns."""
+    return _prompt("rkv_testing_prompt_wait_timeout", (int(what), int(wait_limit_ns)), q, q_len, k,
+                   length, scale, weights, ws, stream)
 
 
 def rkv_evict_workspace_bytes(n: int, n_kv: int, cap: int, keep: int) -> int:
