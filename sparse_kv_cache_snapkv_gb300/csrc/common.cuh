@@ -121,31 +121,34 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
   return ok != 0;
 }
 
-// Wait for phase `parity` of `bar` to complete. Gives up after kWaitLimitNs of wall time and
-// returns false (the caller records RKV_DEV_WAIT_TIMEOUT and abandons its unit).
-constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
+// Bound of a wait in wall time. A type of its own, so that no other number is taken for one.
+struct WaitLimit {
+  uint64_t ns;
+};
+constexpr WaitLimit kWaitLimit{1000ull * 1000ull * 1000ull};  // 1 s
 
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
-                                          uint64_t limit_ns = kWaitLimitNs) {
+// Wait for phase `parity` of `bar` to complete. Gives up after `limit` and returns false (the caller
+// records RKV_DEV_WAIT_TIMEOUT and abandons its unit).
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, WaitLimit limit) {
   const uint32_t a = smem_addr(bar);
   if (mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (mbar_try_wait(a, parity)) return true;
-    if (global_timer_ns() - t0 > limit_ns) return false;
+    if (global_timer_ns() - t0 > limit.ns) return false;
   }
 }
 
 // The same for a whole, converged warp, with one answer for all of its lanes: each lane has its own
 // reading of the clock, so lanes that decided for themselves could part at the limit, and the warp's
 // collective operations behind the wait would then be left by some of them.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, WaitLimit limit) {
   const uint32_t a = smem_addr(bar);
   if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
-    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > limit_ns)) return false;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > limit.ns)) return false;
   }
 }
 

@@ -91,7 +91,7 @@ struct PromptParams {
   float* part;           // [nsplit2][units][max_len] when nsplit2 > 1
   float* weights;        // [units][max_len]
   uint32_t* status;
-  uint64_t wait_limit_ns;  // bound of every mbarrier wait
+  WaitLimit wait_limit;    // bound of every mbarrier wait
   int test_skip;           // testing only: what CTA 0 never requests (RKV_TESTING_PROMPT_*; 0: nothing)
 };
 
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   pdl_wait();
   pdl_trigger();
   bool aborted = false;
-  const uint64_t limit = p.wait_limit_ns;
+  const WaitLimit limit = p.wait_limit;
   const int skip = blockIdx.x == 0 ? p.test_skip : 0;
 
   if (warp == 0) {
@@ -673,7 +673,7 @@ cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s) {
   p.part = reinterpret_cast<float*>(w + ml_bytes(pl, p.units));
   p.weights = a.weights;
   p.status = a.status;
-  p.wait_limit_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
+  p.wait_limit = a.wait_limit_ns ? WaitLimit{a.wait_limit_ns} : kWaitLimit;
   p.test_skip = a.test_skip;
   const bool heads = row_map(a.gqa, a.max_q, kPrTile).per_head != 0;
   cudaError_t e = heads ? launch_prompt_pass<1, true>(km, qm, p, s)

@@ -62,7 +62,7 @@ struct ScoreParams {
   const float* nlse;  // [units][RP]: merged, negated log2-sum-exp of every row (pass 2)
   float* scores;   // [units][max_len - window]
   uint32_t* status;
-  uint64_t wait_limit_ns;  // bound of every mbarrier wait
+  WaitLimit wait_limit;    // bound of every mbarrier wait
   int test_skip_tile;      // testing only: CTA 0 never loads its first K tile of pass 1
 };
 
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int W = p.window;
   const int R = p.gqa * W;
   const int items = p.units * p.nsplit;
-  const uint64_t lim = p.wait_limit_ns;
+  const WaitLimit limit = p.wait_limit;
 
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -161,12 +161,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int it = 0, ic = 0;
+      int it = 0, ic = 0, sent = 0;  // sent: Q tiles requested
       for (int i = blockIdx.x; i < items && !aborted; i += gridDim.x) {
         const ItemInfo itm = score_item<PASS>(p, i);
         if (itm.ntiles == 0) continue;
         const int qb = QB == 2 ? (ic & 1) : 0;
-        if (ic >= QB && !mbar_wait(&qempty[qb], (uint32_t)(((ic / QB) - 1) & 1), lim)) {
+        if (ic >= QB && !mbar_wait(&qempty[qb], (uint32_t)(((ic / QB) - 1) & 1), limit)) {
           aborted = true;
           break;
         }
@@ -177,10 +177,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           for (int rb = 0; rb < RB; ++rb)
             tma_load_2d(qdst + (size_t)h * RP * 128 + (size_t)rb * 128 * 128, &qmap, 64 * h,
                         qrow0 + rb * 128, &qfull[qb]);
+        sent = ic + 1;
         const int krow0 = (itm.ukv / p.kv_div) * p.max_len;
         for (int t = 0; t < itm.ntiles; ++t, ++it) {
           const int s = it % kKStages;
-          if (it >= kKStages && !mbar_wait(&empty[s], (uint32_t)(((it / kKStages) - 1) & 1), lim)) {
+          if (it >= kKStages && !mbar_wait(&empty[s], (uint32_t)(((it / kKStages) - 1) & 1), limit)) {
             aborted = true;
             break;
           }
@@ -194,11 +195,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         }
         ++ic;
       }
-      if (aborted) {
-        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
-        for (int j = max(0, it - kKStages); j < it; ++j)  // let issued loads land
-          mbar_wait(&full[j % kKStages], (uint32_t)((j / kKStages) & 1), lim);
-      }
+      if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+      // every issued load lands before the CTA ends, whoever gave up (else they have, and this is no wait)
+      for (int j = max(0, it - kKStages); j < it; ++j)
+        mbar_wait(&full[j % kKStages], (uint32_t)((j / kKStages) & 1), limit);
+      for (int j = max(0, ic - QB); j < sent; ++j)
+        mbar_wait(&qfull[QB == 2 ? (j & 1) : 0], (uint32_t)((j / QB) & 1), limit);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -208,18 +210,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         const ItemInfo itm = score_item<PASS>(p, i);
         if (itm.ntiles == 0) continue;
         const int qb = QB == 2 ? (ic & 1) : 0;
-        if (!mbar_wait(&qfull[qb], (uint32_t)((ic / QB) & 1), lim)) {
+        if (!mbar_wait(&qfull[qb], (uint32_t)((ic / QB) & 1), limit)) {
           aborted = true;
           break;
         }
         const uint32_t qbase = smem_addr(qs + (size_t)qb * SM::q_bytes);
         for (int t = 0; t < itm.ntiles; ++t, ++it) {
           const int s = it % kKStages, b = it & 1;
-          if (!mbar_wait(&full[s], (uint32_t)((it / kKStages) & 1), lim)) {
+          if (!mbar_wait(&full[s], (uint32_t)((it / kKStages) & 1), limit)) {
             aborted = true;
             break;
           }
-          if (it >= 2 && !mbar_wait(&tempty[b], (uint32_t)(((it >> 1) - 1) & 1), lim)) {
+          if (it >= 2 && !mbar_wait(&tempty[b], (uint32_t)(((it >> 1) - 1) & 1), limit)) {
             aborted = true;
             break;
           }
@@ -255,7 +257,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         umma_commit(&qempty[qb]);  // arrives once this item's MMAs are done with its Q tile
         ++ic;
       }
-      if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+      if (aborted) {
+        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+        for (int j = max(0, it - 2); j < it; ++j)  // let issued MMAs end
+          mbar_wait(&tfull[j & 1], (uint32_t)((j >> 1) & 1), limit);
+      }
     }
   } else {
     // ------------------------------------------------------------------ epilogue
@@ -275,14 +281,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         const int rb = (RB == 2) ? hf : 0;
         const int rg = rb * 128 + lrow;
         const bool row_ok = rg < R;
-        const int lim = itm.L - W + (row_ok ? rg % W : 0);  // last visible key position
+        const int last = itm.L - W + (row_ok ? rg % W : 0);  // last visible key position
         const int c0 = (RB == 2) ? 0 : hf * 64;
         const int ncol = (RB == 2) ? 128 : 64;
         float m = -1e30f, l = 0.f;
         for (int t = 0; t < itm.ntiles; ++t, ++it) {
           const int b = it & 1;
           if (aborted) continue;
-          if (!mbar_wait(&tfull[b], (uint32_t)((it >> 1) & 1), lim)) {
+          if (!mbar_wait_warp(&tfull[b], (uint32_t)((it >> 1) & 1), limit)) {
             aborted = true;
             continue;
           }
@@ -295,13 +301,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             // max on the raw logits (the scale is positive); only chunks that reach the causal
             // part of the window need the visibility mask
             float mt = -INFINITY;
-            if (tb + 31 <= lim) {
+            if (tb + 31 <= last) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) mt = fmaxf(mt, __uint_as_float(r[j]));
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
-                const float x = (tb + j <= lim) ? __uint_as_float(r[j]) : -INFINITY;
+                const float x = (tb + j <= last) ? __uint_as_float(r[j]) : -INFINITY;
                 r[j] = __float_as_uint(x);
                 mt = fmaxf(mt, x);
               }
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         // so that a timeout in one warp can never leave the others waiting at the barrier.
         for (int t = 0; t < itm.ntiles; ++t, ++it) {
           const int b = it & 1;
-          if (!aborted && !mbar_wait(&tfull[b], (uint32_t)((it >> 1) & 1), lim)) aborted = true;
+          if (!aborted && !mbar_wait_warp(&tfull[b], (uint32_t)((it >> 1) & 1), limit)) aborted = true;
           float acc = 0.f;
           if (!aborted) {
             tc_fence_after();
@@ -1198,7 +1204,7 @@ cudaError_t launch_snapkv(const SnapArgs& a, cudaStream_t s) {
   sp.nlse = a.nlse;
   sp.scores = a.scores;
   sp.status = a.status;
-  sp.wait_limit_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
+  sp.wait_limit = a.wait_limit_ns ? WaitLimit{a.wait_limit_ns} : kWaitLimit;
   sp.test_skip_tile = a.test_skip_tile;
   cudaError_t e;
   sp.reverse = 0;
