@@ -404,7 +404,10 @@ rkv_status rkv_dense_decode_noalloc(const void* q, const void* k, const void* v,
  *
  * Layouts: k_codes, v_codes [n][n_kv][cap][64], k_scales, v_scales [n][n_kv][cap][8] bytes; paged:
  * pools [num_blocks][n_kv][block][64] and [..][8] with a block table as for the paged calls above,
- * block at least 16. All 16-byte aligned. Rows at and past a unit's length are never read. */
+ * block at least 16. All 16-byte aligned. Rows at and past a unit's length are never read.
+ *
+ * Workspaces of this part's calls and of the next one's: no *_workspace_bytes falls when one of its
+ * arguments grows, so a workspace made for the largest shape serves every smaller one. */
 
 /* Quantise the new_len[u] new rows of every KV head of unit u behind its len[u] cached ones.
  *   new_k, new_v [n][n_kv][max_new][128] bf16: rows 0 .. new_len[u]-1 are taken

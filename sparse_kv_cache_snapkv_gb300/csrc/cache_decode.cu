@@ -168,12 +168,20 @@ static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
   return (int)(units * (each < rounds ? each : rounds));
 }
 
+// Room for the parts of every call of no larger sizes: a workspace for the largest shape serves all (the
+// number of CTAs itself falls where more units, or more rows, make a part for each of them longer).
+static size_t most_ctas(int n, int n_kv, int cap) {
+  const long long units = (long long)n * n_kv, rounds = (cap + kCdRound<false> - 1) / kCdRound<false>;
+  const long long slots = (long long)kCdPerSm * device_sm_count();
+  return (size_t)(units * rounds < slots ? units * rounds : slots);
+}
+
 struct CacheScratch {
   size_t units, ml, cs, part_ml, part_o, logits, total;
 };
 static CacheScratch cache_scratch(int n, int n_kv, int gqa, int cap, bool with_weights) {
   const size_t units = (size_t)n * n_kv;
-  const size_t slots = 2 * (size_t)cache_decode_ctas(n, n_kv, cap, false);  // (never fewer than 4 bits')
+  const size_t slots = 2 * most_ctas(n, n_kv, cap);
   CacheScratch c;
   c.units = 0;
   c.ml = align_up(((size_t)n + 1) * sizeof(CdUnit), 256);

@@ -58,9 +58,11 @@ static EvictLists lists_of(const EvictArgs& a) {
   return l;
 }
 
+// Room for every call of no larger sizes, so that a workspace for the largest shape serves all: there
+// are most moves where half of the rows are kept.
 size_t evict_scratch_bytes(int n, int n_kv, int cap, int keep) {
-  const size_t units = (size_t)n * n_kv;
-  return align_up(units * 4, 256) + 2 * align_up(units * most_moves(cap, keep) * 4, 256);
+  const size_t units = (size_t)n * n_kv, most = cap / 2 < keep ? cap / 2 : keep;
+  return align_up(units * 4, 256) + 2 * align_up(units * most * 4, 256);
 }
 
 struct EvSmem {

@@ -627,11 +627,19 @@ static size_t ml_bytes(const PromptPlan& p, size_t units) {
   return p.nsplit1 > 1 ? align_up(units * p.nsplit1 * p.tiles1 * kPrStat * 8, 256) : 0;
 }
 
+// Room for every call of no larger sizes, so that a workspace for the largest shape serves all: splits
+// are made until there are `sms` items in pass 1 and 4 sms in pass 2, so their partial results are at
+// most that many tiles' (and a split fewer than four steps of the stream is not made), whichever sizes
+// bring that about.
 size_t prompt_scratch_bytes(int n, int n_kv, int gqa, int max_q, int max_len) {
   const PromptPlan p = prompt_plan(n, n_kv, gqa, max_q, max_len);
-  const size_t units = (size_t)n * n_kv;
-  return nl_bytes(p, units) + ml_bytes(p, units) +
-         (p.nsplit2 > 1 ? align_up(units * p.nsplit2 * max_len * 4, 256) : 0);
+  const size_t units = (size_t)n * n_kv, sms = device_sm_count();
+  const size_t most1 = (size_t)((max_len + kPrTile - 1) / kPrTile + 3) / 4;
+  const size_t most2 = (size_t)(row_tiles(row_map(gqa, max_q, kPrTile), kPrTile) + 3) / 4;
+  const size_t items1 = units * p.tiles1 * most1, rows2 = units * most2 * max_len;
+  const size_t ml = (items1 < sms ? items1 : sms) * kPrStat * 8;
+  const size_t part = (rows2 < 4 * sms * kPrStat ? rows2 : 4 * sms * kPrStat) * 4;
+  return nl_bytes(p, units) + align_up(ml, 256) + align_up(part, 256);
 }
 
 template <int PASS, bool HEADS>

@@ -1,5 +1,6 @@
 """What the cache calls promise before any launch: hooks' refusals and workspace sizes. No GPU needed."""
 import ctypes
+import random
 
 import pytest
 
@@ -21,3 +22,41 @@ def test_prompt_timeout_hook_refusals(lib):
     for change, code in ((dict(what=0), 1), (dict(what=4), 1), (dict(limit=999), 1), (dict(limit=10**9 + 1), 1),
                          (dict(head_dim=64), 2), (dict(weights=None), 1), (dict(ws_bytes=300), 3)):
         assert lib.rkv_testing_prompt_wait_timeout(*{**ok, **change}.values()) == code, change
+
+
+# the arguments of each *_workspace_bytes: (smallest, largest) or the choices
+SIZES = {
+    "rkv_kv4_append_workspace_bytes": [(1, 4096)],
+    "rkv_kv4_decode_workspace_bytes": [(1, 64), (1, 16), [1, 2, 4, 8], (1, 1 << 20), [0, 1]],
+    "rkv_dense_decode_weights_workspace_bytes": [(1, 64), (1, 16), [1, 2, 4, 8], (1, 1 << 20)],
+    "rkv_prompt_weights_workspace_bytes": [(1, 64), (1, 16), (1, 64), (1, 1 << 15), (1 << 15, 1 << 18)],
+    "rkv_evict_workspace_bytes": [(1, 600), (1, 16), (1, 1 << 20), (1, 1 << 20)],
+}
+
+
+def _pick(rng, span, at_least=None):
+    if isinstance(span, list):
+        return rng.choice([x for x in span if at_least is None or x >= at_least])
+    low = span[0] if at_least is None else at_least
+    if rng.random() < 0.3:  # next door
+        return min(span[1], low + rng.randint(0, 2))
+    return int(round(low * (span[1] / low) ** rng.random()))
+
+
+@pytest.mark.parametrize("name", sorted(SIZES))
+def test_workspaces_do_not_shrink(lib, name):
+    rng, size = random.Random(name), getattr(lib, name)
+    for _ in range(4000):
+        a = [_pick(rng, s) for s in SIZES[name]]
+        b = [_pick(rng, s, x) if rng.random() < 0.5 else x for s, x in zip(SIZES[name], a)]
+        assert 256 <= size(*a) <= size(*b), (a, b)
+
+
+@pytest.mark.parametrize("name,small,large", [
+    ("rkv_prompt_weights_workspace_bytes", (1, 8, 4, 8192, 8192), (1, 8, 4, 8192, 32768)),
+    ("rkv_kv4_decode_workspace_bytes", (19, 8, 4, 256, 0), (20, 8, 4, 256, 0)),
+    ("rkv_evict_workspace_bytes", (1, 8, 8192, 4096), (1, 8, 8192, 8000)),
+])
+def test_workspace_of_the_larger_shape_serves(lib, name, small, large):
+    size = getattr(lib, name)
+    assert size(*small) <= size(*large)
