@@ -490,7 +490,9 @@ rkv_status rkv_dense_decode_weights(const void* q, const void* k, const void* v,
  *   k       [n][n_kv][max_len][128] bf16, the chunk's own keys included; rows len[u] and up unused
  *   len     [n] int32, at most max_len (else RKV_DEV_LEN_OVER_CAP, unit skipped)
  *   gqa     1 .. 64
- *   weights [n][n_kv][max_len] fp32 */
+ *   weights [n][n_kv][max_len] fp32
+ *   1 <= max_q <= max_len; n * n_kv * gqa * max_q and n * n_kv * max_len at most 2^31 - 513
+ *   (RKV_ERR_TOO_LARGE; rkv_prompt_weights_workspace_bytes is 0 for what the call refuses) */
 size_t rkv_prompt_weights_workspace_bytes(int n, int n_kv, int gqa, int max_q, int max_len);
 rkv_status rkv_prompt_weights(const void* q, const int32_t* q_len, const void* k,
                               const int32_t* len, int n, int n_kv, int gqa, int head_dim,

@@ -29,6 +29,12 @@ bool kv4_ok(const void* a, const void* b, const void* c, const void* d) {
   return a && b && c && d && aligned16(a) && aligned16(b) && aligned16(c) && aligned16(d);
 }
 
+// a row's index is a 32-bit coordinate of the tensor maps
+bool prompt_rows_ok(int n, int n_kv, int gqa, int max_q, int max_len) {
+  return (long long)n * n_kv * gqa * max_q <= INT_MAX - 512 &&
+         (long long)n * n_kv * max_len <= INT_MAX - 512;
+}
+
 rkv_status ws_check(const void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return RKV_ERR_INVALID_ARG;
   return ws && aligned16(ws) && ws_bytes >= need ? RKV_OK : RKV_ERR_WORKSPACE;
@@ -154,10 +160,7 @@ rkv_status prompt_impl(const void* q, const int32_t* q_len, const void* k, const
     return RKV_ERR_INVALID_ARG;
   if (!counts_ok(n, n_kv, gqa) || max_q <= 0 || max_len < max_q || !scale_ok(scale))
     return RKV_ERR_INVALID_ARG;
-  // a row's index is a 32-bit coordinate of the tensor maps
-  if ((long long)n * n_kv * gqa * max_q > INT_MAX - 512 ||
-      (long long)n * n_kv * max_len > INT_MAX - 512)
-    return RKV_ERR_TOO_LARGE;
+  if (!prompt_rows_ok(n, n_kv, gqa, max_q, max_len)) return RKV_ERR_TOO_LARGE;
   const rkv_status w =
       ws_check(ws, ws_bytes, rkv_prompt_weights_workspace_bytes(n, n_kv, gqa, max_q, max_len));
   if (w != RKV_OK) return w;
@@ -288,7 +291,9 @@ rkv_status rkv_dense_decode_weights(const void* q, const void* k, const void* v,
 }
 
 size_t rkv_prompt_weights_workspace_bytes(int n, int n_kv, int gqa, int max_q, int max_len) {
-  if (!counts_ok(n, n_kv, gqa) || gqa > kMaxPromptGqa || max_q <= 0 || max_len < max_q) return 0;
+  if (!counts_ok(n, n_kv, gqa) || gqa > kMaxPromptGqa || max_q <= 0 || max_len < max_q ||
+      !prompt_rows_ok(n, n_kv, gqa, max_q, max_len))
+    return 0;
   return kStatusBytes + prompt_scratch_bytes(n, n_kv, gqa, max_q, max_len);
 }
 

@@ -60,3 +60,13 @@ def test_workspaces_do_not_shrink(lib, name):
 def test_workspace_of_the_larger_shape_serves(lib, name, small, large):
     size = getattr(lib, name)
     assert size(*small) <= size(*large)
+
+
+def test_prompt_workspace_of_what_is_refused_is_none(lib):
+    size, top = lib.rkv_prompt_weights_workspace_bytes, 2**31 - 1
+    for a in ((1, 1, 1, 1, top), (1, 1, 64, top // 64, top), (2, 1, 1, 1, 2**30), (1, 8, 64, 2**22, 2**22),
+              (1, 1, 65, 1, 1), (1, 1, 1, 2, 1), (0, 1, 1, 1, 1)):
+        assert size(*a) == 0, a
+    # the largest that are taken
+    assert 256 < size(1, 1, 1, 1, top - 512) < 2**20  # (one query: a tile's sums, splits of at most the SMs' number)
+    assert size(1, 1, 1, top - 512, top - 512) >= 4 * (top - 512)
