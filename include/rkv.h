@@ -442,9 +442,10 @@ rkv_status rkv_kv4_append_paged(const void* new_k, const void* new_v, const int3
  * appends nothing and attends to its cap tokens. A unit without tokens gets zeros.
  *   q, out [n][n_kv*gqa][128] bf16; gqa 1, 2, 4 or 8
  *   new_k, new_v NULL or [n][n_kv][128] bf16; len_out [n] int32 (may be len), NULL without them
- *   weights NULL or [n][n_kv][cap] fp32 (paged: cap = max_blocks * block): the softmax weight of
- *           every token, summed over the group's query heads, is added to its entry (rows at and
- *           past the length are left as they are, so entries of rows to come should hold zero)
+ *   weights NULL or [n][n_kv][cap] fp32, 16-byte aligned (paged: cap = max_blocks * block): the
+ *           softmax weight of every token, summed over the group's query heads, is added to its
+ *           entry (rows at and past the length are left as they are, so entries of rows to come
+ *           should hold zero)
  * Workspace rkv_kv4_decode_workspace_bytes (cap as above; with_weights: whether weights are asked
  * for, which takes 4 * gqa bytes per cached row). Results do not depend on what the workspace
  * holds, status word apart. */
@@ -474,7 +475,8 @@ rkv_status rkv_kv4_decode_paged(const void* q, const void* new_k, const void* ne
  * softmax(scale * q[u][h] . K[u][g]^T)[j] to weights[u][g][j], j < len[u].
  *   q, k, v, len, out as rkv_dense_decode (0 <= len[u]: a unit without tokens gets zeros; a longer
  *   one than max_len sets RKV_DEV_LEN_OVER_CAP and counts as max_len)
- *   weights [n][n_kv][max_len] fp32, rows past len[u] left as they are */
+ *   weights [n][n_kv][max_len] fp32, 16-byte aligned; rows past len[u] left as they are
+ *   (In the prompt call and the evictions 4 bytes are enough for weights and pos.) */
 size_t rkv_dense_decode_weights_workspace_bytes(int n, int n_kv, int gqa, int max_len);
 rkv_status rkv_dense_decode_weights(const void* q, const void* k, const void* v,
                                     const int32_t* len, int n, int n_kv, int gqa, int head_dim,

@@ -571,6 +571,16 @@ def _at(t, name, dtype, shape, dev):
     _refuse(t, name, dtype, shape, dev)
 
 
+def _weights16(t, shape, dev, given=True):
+    """Address of a decode's weights, which begin on 16 bytes: a slice of a larger array need not.
+    given: they have to be (else None: not asked for)."""
+    p = (_at if given else _at_or_none)(t, "weights", _F32, shape, dev)
+    if p is not None and p % 16:
+        raise ValueError("weights must begin on a 16-byte boundary: a slice of units does where "
+                         "n_kv * cap is a multiple of 4")
+    return p
+
+
 def _at_or_none(t, name, dtype, shape, dev):
     return None if t is None else _at(t, name, dtype, shape, dev)
 
@@ -681,7 +691,7 @@ def rkv_kv4_decode(q, k_codes, k_scales, v_codes, v_scales, length, scale: float
             _at(length, "len", _I32, (n,), dev),
             _at_or_none(length_out, "len_out", _I32, (n,), dev), n, n_kv, gqa, d, cap, scale,
             _at(out, "out", _BF16, shape, dev),
-            _at_or_none(weights, "weights", _F32, (n, n_kv, cap), dev))
+            _weights16(weights, (n, n_kv, cap), dev, given=False))
     return _call("rkv_kv4_decode", args, ws,
                  lambda: rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None),
                  dev, stream)
@@ -704,7 +714,7 @@ def rkv_kv4_decode_paged(q, k_codes, k_scales, v_codes, v_scales, block_table, l
             _at(length, "len", _I32, (n,), dev),
             _at_or_none(length_out, "len_out", _I32, (n,), dev), n, n_kv, gqa, d, num_blocks,
             block, max_blocks, scale, _at(out, "out", _BF16, shape, dev),
-            _at_or_none(weights, "weights", _F32, (n, n_kv, cap), dev))
+            _weights16(weights, (n, n_kv, cap), dev, given=False))
     return _call("rkv_kv4_decode_paged", args, ws,
                  lambda: rkv_kv4_decode_workspace_bytes(n, n_kv, gqa, cap, weights is not None),
                  dev, stream)
@@ -724,7 +734,7 @@ def rkv_dense_decode_weights(q, k, v, length, scale: float, out, weights, ws=Non
     args = (_at(q, "q", _BF16, (n, hq, d), dev), _at(k, "k", _BF16, shape, dev),
             _at(v, "v", _BF16, shape, dev), _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d,
             max_len, scale, _at(out, "out", _BF16, (n, hq, d), dev),
-            _at(weights, "weights", _F32, (n, n_kv, max_len), dev))
+            _weights16(weights, (n, n_kv, max_len), dev))
     return _call("rkv_dense_decode_weights", args, ws,
                  lambda: rkv_dense_decode_weights_workspace_bytes(n, n_kv, gqa, max_len), dev,
                  stream)

@@ -70,3 +70,24 @@ def test_prompt_workspace_of_what_is_refused_is_none(lib):
     # the largest that are taken
     assert 256 < size(1, 1, 1, 1, top - 512) < 2**20  # (one query: a tile's sums, splits of at most the SMs' number)
     assert size(1, 1, 1, top - 512, top - 512) >= 4 * (top - 512)
+
+
+ODD = ctypes.c_void_p((1 << 20) + 8)
+
+
+def test_decode_weights_begin_on_16_bytes(lib):
+    """As include/rkv.h says of every decode that takes them."""
+    v = FAKE
+    dense = dict(q=v, k=v, v=v, len=v, n=1, n_kv=2, gqa=4, head_dim=128, max_len=64, scale=0.1, out=v, weights=ODD,
+                 ws=v, ws_bytes=BIG, stream=None)
+    assert lib.rkv_dense_decode_weights(*dense.values()) == 1
+    paged = dict(q=v, new_k=None, new_v=None, kc=v, ks=v, vc=v, vs=v, table=v, len=v, len_out=None, n=1, n_kv=2,
+                 gqa=4, head_dim=128, num_blocks=4, block=16, max_blocks=2, scale=0.1, out=v, weights=ODD, ws=v,
+                 ws_bytes=BIG, stream=None)
+    assert lib.rkv_kv4_decode_paged(*paged.values()) == 1
+    import os
+    with open(os.path.join(os.path.dirname(__file__), "..", "include", "rkv.h")) as f:
+        header = f.read()
+    for call in ("weights NULL or [n][n_kv][cap] fp32, 16-byte aligned",
+                 "weights [n][n_kv][max_len] fp32, 16-byte aligned"):
+        assert call in header
