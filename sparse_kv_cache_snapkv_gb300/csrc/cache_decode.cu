@@ -159,10 +159,15 @@ constexpr int kCdWeightCtasPerSm = 8;
 // CTAs of a call: one per slot of the SMs; where that leaves a part fewer than kCdMinRounds rounds,
 // the same number for each (unit, KV head), so that parts of equal lengths end with them.
 constexpr int kCdMinRounds = 2;
+constexpr int kCdMostCtas = 512;  // the joins have room for the factors of as many parts
+static long long cache_decode_slots() {
+  const int s = kCdPerSm * device_sm_count();
+  return s < kCdMostCtas ? s : kCdMostCtas;
+}
 static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
   const int round = kv4 ? kCdRound<true> : kCdRound<false>;
   const long long units = (long long)n * n_kv, rounds = (cap + round - 1) / round;
-  const long long slots = (long long)kCdPerSm * device_sm_count();
+  const long long slots = cache_decode_slots();
   if (units * rounds >= slots * kCdMinRounds || units >= slots) return (int)slots;
   const long long each = slots / units;
   return (int)(units * (each < rounds ? each : rounds));
@@ -172,7 +177,7 @@ static int cache_decode_ctas(int n, int n_kv, int cap, bool kv4) {
 // number of CTAs itself falls where more units, or more rows, make a part for each of them longer).
 static size_t most_ctas(int n, int n_kv, int cap) {
   const long long units = (long long)n * n_kv, rounds = (cap + kCdRound<false> - 1) / kCdRound<false>;
-  const long long slots = (long long)kCdPerSm * device_sm_count();
+  const long long slots = cache_decode_slots();
   return (size_t)(units * rounds < slots ? units * rounds : slots);
 }
 
@@ -984,12 +989,11 @@ __global__ void __launch_bounds__(kCdThreads, kCdPerSm) cache_decode_kernel(Cach
 
 // The joins: blockIdx.y = 0 the outputs and the length, the others kCdWeightChunk tokens' weights.
 // `ctas`: CTAs of the decode's launch.
-constexpr int kCdFactors = 512;  // the factors of more parts are made again for each output
 template <int G, bool KV4>
 __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs a, int ctas) {
   __shared__ float4 sums[kCdThreads];
-  __shared__ float factor[kCdFactors * G];
-  __shared__ float total_s[8], top[8];
+  __shared__ float factor[kCdMostCtas * G];
+  __shared__ float total_s[8];
   __shared__ CdHead head[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ukv = blockIdx.x, u = ukv / a.n_kv, g = ukv - u * a.n_kv;
@@ -1037,14 +1041,13 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
     for (int k = lane; k < parts; k += 32) {
       const float2 x = k == lane ? mine : ml[slot_of(k) * G + warp];
       const float f = fast_exp2(x.x - M);
-      if (k < kCdFactors) factor[k * G + warp] = f;
+      factor[k * G + warp] = f;
       S = fmaf(x.y, f, S);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) S += __shfl_xor_sync(0xffffffffu, S, d);
     if (lane == 0) {
       total_s[warp] = S;
-      top[warp] = M;
       if (blockIdx.y > 0) head[warp] = CdHead{a.cs[(size_t)ukv * G + warp], M, over(S * kCdUnshift<KV4>)};
     }
   }
@@ -1067,10 +1070,7 @@ __global__ void __launch_bounds__(kCdThreads) cache_join_kernel(CacheDecodeArgs 
     const float4 x = reinterpret_cast<const float4*>(a.part_o + slot_of(k) * G * kHeadDim)[quad];
     float f[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int h = (4 * quad + e) % G;
-      f[e] = k < kCdFactors ? factor[k * G + h] : fast_exp2(ml[slot_of(k) * G + h].x - top[h]);
-    }
+    for (int e = 0; e < 4; ++e) f[e] = factor[k * G + (4 * quad + e) % G];
     o.x = fmaf(x.x, f[0], o.x);
     o.y = fmaf(x.y, f[1], o.y);
     o.z = fmaf(x.z, f[2], o.z);
