@@ -72,3 +72,60 @@ def test_kv4_probabilities_keep_their_bits(rkv, gqa, T):
         for g in range(n_kv):
             H.check_decode(got[u, g], w[u, g].double().cpu().numpy(), q[u, g].double().numpy(), held[0][u, g],
                            held[1][u, g], SCALE, True, 64 + T // 64, f"unit {u} head {g}", most=1e-4)
+
+
+def _decode_both(rkv, q, k, v, gqa, kv4):
+    """q [n, gqa, D], k, v [n, 1, T, D]: outputs and weights, and the numbers that the cache holds."""
+    n, _, T, _ = k.shape
+    q, k, v = q.to(BF).cuda(), k.to(BF).cuda(), v.to(BF).cuda()
+    out, w, length = torch.empty_like(q), torch.zeros(n, 1, T, device="cuda"), _ints([0] * n)
+    if kv4:
+        cache = rkv.kv4_cache(n, 1, T)
+        rkv.rkv_check_status(rkv.rkv_kv4_append(k, v, *cache, length, length))
+        rkv.rkv_check_status(rkv.rkv_kv4_decode(q, *cache, length, SCALE, out, weights=w))
+        held = [C.kv4_values(cache[i].cpu().numpy(), cache[i + 1].cpu().numpy()) for i in (0, 2)]
+    else:
+        rkv.rkv_check_status(rkv.rkv_dense_decode_weights(q, k, v, _ints([T] * n), SCALE, out, w))
+        held = [x.double().cpu().numpy() for x in (k, v)]
+    for u in range(n):
+        H.check_decode(out[u].double().cpu().numpy(), w[u, 0].double().cpu().numpy(), q[u].double().cpu().numpy(),
+                       held[0][u, 0], held[1][u, 0], SCALE, kv4, 64 + T // 64, f"unit {u}")
+
+
+@pytest.mark.parametrize("kv4", [True, False])
+@pytest.mark.parametrize("gqa", [2, 4, 8])
+@pytest.mark.parametrize("T", [33, 1500])
+def test_heads_of_very_different_size(rkv, gqa, T, kv4):
+    """Keys with scales near the top of the 4-bit format and query heads from 2^-40 to some 100 of logit:
+    each head has its own power of two on the way into the product, and its own tolerance here."""
+    g = torch.Generator().manual_seed(T + gqa)
+    n = 3
+    q = torch.randn(n, gqa, D, generator=g)
+    k = torch.randn(n, 1, T, D, generator=g) * torch.tensor([3000.0, 3000.0, 2.0 ** -6]).view(n, 1, 1, 1)
+    for h in range(gqa):
+        q[0, h] *= 2.0 ** (-9 - [0, 3, 31, 12, 1, 5, 20, 8][h])
+        q[1, h] *= 2.0 ** (-9 - [12, 0, 8, 2, 40, 1, 3, 2][h])
+        q[2, h] *= 2.0 ** (10 - [0, 30, 3, 6, 1, 50, 2, 9][h])
+    q[0, 0, ::2] *= 2.0 ** -16   # a head whose values reach over more bits than fp16 has
+    q[2, 1, 1::3] = 0.0
+    v = torch.randn(n, 1, T, D, generator=g) * torch.tensor([1.0, 5000.0, 2.0 ** -8]).view(n, 1, 1, 1)
+    _decode_both(rkv, q, k, v, gqa, kv4)
+
+
+@pytest.mark.parametrize("kv4", [True, False])
+@pytest.mark.parametrize("T", [400, 5000])
+def test_maximum_that_moves(rkv, T, kv4):
+    """Logits that rise or fall along the sequence, in steps of less and of more than the lag that the running
+    maximum is allowed, and one token far above the rest; each for another head."""
+    g = torch.Generator().manual_seed(T)
+    n, gqa = 4, 4
+    q = torch.randn(n, gqa, D, generator=g)
+    unit = q / q.norm(dim=-1, keepdim=True)
+    ramp = torch.linspace(-1, 1, T).view(T, 1)
+    k = torch.randn(n, 1, T, D, generator=g) * 0.1
+    k[0, 0] += ramp * unit[0, 0] * 40
+    k[1, 0] -= ramp * unit[1, 1] * 120
+    k[2, 0, T // 3] += unit[2, 2] * 60
+    k[3, 0] += ramp.abs() * unit[3, 3] * 100 - ramp * unit[3, 0] * 9
+    v = torch.randn(n, 1, T, D, generator=g)
+    _decode_both(rkv, q, k, v, gqa, kv4)
