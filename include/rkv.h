@@ -474,7 +474,9 @@ rkv_status rkv_kv4_decode_paged(const void* q, const void* new_k, const void* ne
  * rkv_dense_decode with the weights: adds sum over the group's heads h of
  * softmax(scale * q[u][h] . K[u][g]^T)[j] to weights[u][g][j], j < len[u].
  *   q, k, v, len, out as rkv_dense_decode (0 <= len[u]: a unit without tokens gets zeros; a longer
- *   one than max_len sets RKV_DEV_LEN_OVER_CAP and counts as max_len)
+ *   one than max_len sets RKV_DEV_LEN_OVER_CAP and counts as max_len). v finite and below 2^100 in
+ *   magnitude in the unit's rows: sums of v come before the division by the softmax's sum, and an
+ *   infinite value makes NaN of its outputs. Rows past len[u] may hold anything.
  *   weights [n][n_kv][max_len] fp32, 16-byte aligned; rows past len[u] left as they are
  *   (In the prompt call and the evictions 4 bytes are enough for weights and pos.) */
 size_t rkv_dense_decode_weights_workspace_bytes(int n, int n_kv, int gqa, int max_len);
