@@ -126,6 +126,11 @@ struct WaitLimit {
   uint64_t ns;
 };
 constexpr WaitLimit kWaitLimit{1000ull * 1000ull * 1000ull};  // 1 s
+// Bound of a wait for what this CTA has in flight itself, before it frees its memory: far above what
+// a copy or a product takes, also where the waits' own limit is a test's microsecond.
+__device__ __forceinline__ WaitLimit drain_limit(WaitLimit limit) {
+  return WaitLimit{max((unsigned long long)limit.ns, 10ull * 1000ull * 1000ull)};
+}
 
 // Wait for phase `parity` of `bar` to complete. Gives up after `limit` and returns false (the caller
 // records RKV_DEV_WAIT_TIMEOUT and abandons its unit).

@@ -297,11 +297,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
       // every issued load lands before the CTA ends, whoever gave up (else they have, and this is no wait)
       for (int j = max(0, step - kPrStages); j < step; ++j)
-        mbar_wait(&full[j % kPrStages], (uint32_t)((j / kPrStages) & 1), limit);
+        mbar_wait(&full[j % kPrStages], (uint32_t)((j / kPrStages) & 1), drain_limit(limit));
       for (int j = max(0, step - kPrNlSlots); PASS == 2 && j < step; ++j)
-        mbar_wait(&nfull[j % kPrNlSlots], (uint32_t)((j / kPrNlSlots) & 1), limit);
+        mbar_wait(&nfull[j % kPrNlSlots], (uint32_t)((j / kPrNlSlots) & 1), drain_limit(limit));
       for (int j = max(0, ic - 2); j < sent; ++j)
-        mbar_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1), limit);
+        mbar_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1), drain_limit(limit));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (aborted) {
         set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
         for (int j = max(0, step - 2); j < step; ++j)  // let issued products end
-          mbar_wait(&tfull[j & 1], (uint32_t)((j >> 1) & 1), limit);
+          mbar_wait(&tfull[j & 1], (uint32_t)((j >> 1) & 1), drain_limit(limit));
       }
     }
   } else {

@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (aborted) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
       // every issued load lands before the CTA ends, whoever gave up (else they have, and this is no wait)
       for (int j = max(0, it - kKStages); j < it; ++j)
-        mbar_wait(&full[j % kKStages], (uint32_t)((j / kKStages) & 1), limit);
+        mbar_wait(&full[j % kKStages], (uint32_t)((j / kKStages) & 1), drain_limit(limit));
       for (int j = max(0, ic - QB); j < sent; ++j)
-        mbar_wait(&qfull[QB == 2 ? (j & 1) : 0], (uint32_t)((j / QB) & 1), limit);
+        mbar_wait(&qfull[QB == 2 ? (j & 1) : 0], (uint32_t)((j / QB) & 1), drain_limit(limit));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (aborted) {
         set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
         for (int j = max(0, it - 2); j < it; ++j)  // let issued MMAs end
-          mbar_wait(&tfull[j & 1], (uint32_t)((j >> 1) & 1), limit);
+          mbar_wait(&tfull[j & 1], (uint32_t)((j >> 1) & 1), drain_limit(limit));
       }
     }
   } else {

@@ -56,3 +56,25 @@ def test_prompt_wait_runs_out_and_context_survives(n, n_kv, gqa, max_q, lens, ne
     w.zero_()
     rkv.rkv_check_status(rkv.rkv_prompt_weights(q, ql, k, ln, SCALE, w, ws=ws))
     _check(w, q, k, lens, news, gqa, range(min(n, 3)))
+
+
+@pytest.mark.parametrize("max_q,cap", [(600, 900), (90, 900)])
+def test_the_shortest_limit(max_q, cap):
+    """A microsecond, which no wait for memory meets: every block gives up with copies and products on their
+    way, lets those land, and the next call is right."""
+    from sparse_kv_cache_snapkv_gb300 import rkv
+    rkv.load()
+    n, n_kv, gqa = 12, 2, 4
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k = torch.randn(n, n_kv, cap, D, generator=g, device="cuda").bfloat16()
+    q = torch.randn(n, n_kv * gqa, max_q, D, generator=g, device="cuda").bfloat16()
+    ql, ln = (torch.full((n,), x, dtype=torch.int32, device="cuda") for x in (max_q, cap))
+    w = torch.zeros(n, n_kv, cap, device="cuda")
+    for what in (KEYS, QUERIES, SUMS):
+        ws = rkv.rkv_testing_prompt_wait_timeout(q, ql, k, ln, SCALE, w, what, 1000)
+        with pytest.raises(rkv.RkvError) as e:
+            rkv.rkv_check_status(ws)
+        assert e.value.bits == 0x4
+    w.zero_()
+    rkv.rkv_check_status(rkv.rkv_prompt_weights(q, ql, k, ln, SCALE, w, ws=ws))
+    _check(w, q, k, [cap] * n, [max_q] * n, gqa, (0, n - 1))

@@ -40,3 +40,27 @@ def test_score_waits_run_out(n, n_kv, gqa, window, lens):
                                   q[u, h * gqa:(h + 1) * gqa].double().cpu().numpy(), scale)
             got = scores[u, h, :lens[u] - window].double().cpu().numpy()
             assert (np.abs(got - ref) <= 1e-4 * np.abs(ref) + 1e-30).all(), (u, h)
+
+
+@pytest.mark.parametrize("gqa", [4, 8])
+def test_the_shortest_limit(gqa):
+    """A microsecond, which no wait for memory meets: every block gives up with copies and products on their
+    way, lets those land, and the next call is right."""
+    from sparse_kv_cache_snapkv_gb300 import rkv
+    rkv.load()
+    n, window, L = 200, 32, 1500
+    g = torch.Generator(device="cuda").manual_seed(8)
+    k = torch.randn(n, 1, L, D, generator=g, device="cuda").bfloat16()
+    q = torch.randn(n, gqa, window, D, generator=g, device="cuda").bfloat16()
+    ln = torch.full((n,), L, dtype=torch.int32, device="cuda")
+    scale = 1.0 / math.sqrt(D)
+    scores = torch.zeros(n, 1, L - window, device="cuda")
+    ws = rkv.rkv_testing_scores_wait_timeout(k, ln, q, scale, scores, wait_limit_ns=1000)
+    with pytest.raises(rkv.RkvError) as e:
+        rkv.rkv_check_status(ws)
+    assert e.value.bits == 0x4
+    rkv.rkv_check_status(rkv.rkv_snapkv_scores(k, ln, q, scale, scores))
+    for u in (0, n - 1):
+        ref = O.window_scores(k[u, 0].double().cpu().numpy(), q[u].double().cpu().numpy(), scale)
+        got = scores[u, 0].double().cpu().numpy()
+        assert (np.abs(got - ref) <= 1e-4 * np.abs(ref) + 1e-30).all(), u
