@@ -62,6 +62,7 @@ typedef enum {
 #define RKV_DEV_WAIT_TIMEOUT   0x4u  /* a bounded mbarrier wait ran out (unit abandoned)      */
 #define RKV_DEV_SELECT_FAILED  0x8u  /* a top-k selection produced the wrong count            */
 #define RKV_DEV_BAD_INDEX      0x10u /* a kept index outside the valid rows (row 0 read)      */
+#define RKV_DEV_NO_BLOCKS      0x20u /* fewer free blocks than a unit needs (unit not served) */
 
 /* Human-readable name of a status code (static string). */
 const char* rkv_status_string(rkv_status s);
@@ -532,6 +533,154 @@ rkv_status rkv_evict_kv4(void* k_codes, void* k_scales, void* v_codes, void* v_s
                          float* weights_out, const int32_t* pos, int32_t* pos_out,
                          const int32_t* seen, int n, int n_kv, int head_dim, int cap, int keep,
                          int recent, int32_t* src_rows, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* A serving step around the cache: places, rotary positions, attention of packed tokens        */
+/* ------------------------------------------------------------------------------------------ */
+/* What fills the caches that the calls above compress and read, and the steps that have more than
+ * one query per request. A step's new tokens of all units lie packed, token-major: unit u has the
+ * tokens q_start[u] .. q_start[u+1]-1 of arrays [tokens][heads][128] (q_start [n+1] int32). q, k
+ * and v may be slices of one projection's output: their tokens are `*_stride` elements apart (a
+ * multiple of 8, at least heads * 128), the heads of one token contiguous.
+ * A slot names a row of every KV head: slot = b * block + r is row r of block b of pools
+ * [num_blocks][n_kv][block][128]; a contiguous cache [n][n_kv][cap][128] is the pool of n blocks of
+ * cap rows (any block size >= 1 is taken here). A negative slot is no place. No *_workspace_bytes
+ * of this part falls when one of its arguments grows.
+ *
+ * Block tables and slots on the device. The free blocks are a stack: free_blocks [num_blocks]
+ * int32, entries 0 .. free_count[0]-1, the top last.
+ *
+ * rkv_reserve_slots: a place for new_len[u] more tokens of every unit behind its len[u] ones.
+ *   new_len, len, held [n] int32: held[u] blocks of block_table [n][max_blocks] are the unit's
+ *            already, ceil(len / block) at least (blocks kept after a sequence was cut are used
+ *            first); entries from held[u] on are not read
+ *   block    tokens of a block, >= 1; num_blocks * block and max_blocks * block at most 2^30
+ *   block_table  entries held[u] .. of a unit that needs more blocks are written: they come off the
+ *            top of the stack in the order of the units. free_blocks itself is only read.
+ *   q_start  [n+1] int32: prefix sums of new_len (a negative one counts as 0)
+ *   slots, positions [max_tokens] int32: slot and position (len[u] + i) of every new token; -1 and
+ *            0 for tokens of units not served, and behind the last token (so a batch padded to
+ *            max_tokens stores nothing there)
+ *   len_out, held_out, free_count_out: the values after the call (may be the input arrays)
+ * A unit is served or left as it was. Not served: len, new_len or held out of range, or len + new_len
+ * above max_blocks * block, or tokens that do not fit in max_tokens (RKV_DEV_LEN_OVER_CAP); fewer
+ * blocks held than its tokens need, or a block outside [0, num_blocks) among those that its new
+ * tokens go to (RKV_DEV_BAD_INDEX; in the latter case those tokens alone have no place); blocks
+ * needed, and more needed by it and the units before it, served or not, than are free
+ * (RKV_DEV_NO_BLOCKS). free_count outside [0, num_blocks]: RKV_DEV_BAD_INDEX, none is free. */
+size_t rkv_reserve_slots_workspace_bytes(int n);
+rkv_status rkv_reserve_slots(const int32_t* new_len, const int32_t* len, const int32_t* held,
+                             int32_t* block_table, const int32_t* free_blocks,
+                             const int32_t* free_count, int n, int num_blocks, int block,
+                             int max_blocks, int max_tokens, int32_t* q_start, int32_t* slots,
+                             int32_t* positions, int32_t* len_out, int32_t* held_out,
+                             int32_t* free_count_out, void* ws, size_t ws_bytes, void* stream);
+
+/* The way back: every unit keeps the ceil(len[u] / block) blocks that its tokens need (none with
+ * len[u] = 0), the others of its held[u] go to the stack, in the order of units and of the table.
+ * held_out, free_count_out may be the input arrays; block_table is only read. A unit with len < 0 or
+ * held outside [0, max_blocks] sets RKV_DEV_LEN_OVER_CAP and keeps all. If more would come back than
+ * the pool can lack (num_blocks - free_count), RKV_DEV_BAD_INDEX is set and nothing is released; a
+ * table entry outside [0, num_blocks) sets it too and goes to the stack as it is. */
+size_t rkv_release_blocks_workspace_bytes(int n);
+rkv_status rkv_release_blocks(const int32_t* len, const int32_t* held, const int32_t* block_table,
+                              int32_t* free_blocks, const int32_t* free_count, int n,
+                              int num_blocks, int block, int max_blocks, int32_t* held_out,
+                              int32_t* free_count_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Rotary positions. rkv_rope_frequencies (host): inv_freq[i] of the rot_dim / 2 pairs, and mscale.
+ *   RKV_ROPE_PLAIN    base^(-2 i / rot_dim)
+ *   RKV_ROPE_LINEAR   divided by factor (positions as if interpolated)
+ *   RKV_ROPE_BASE     plain with base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is slower
+ *                     by factor, the fastest unchanged (rot_dim >= 4)
+ *   RKV_ROPE_BY_PARTS pairs that turn more than `fast` times within the original context `ctx` keep
+ *                     their frequency, those that turn fewer than `slow` times are divided by
+ *                     factor, linear in the pair's number between the (real) numbers of these two;
+ *                     mscale = 0.1 ln(factor) + 1 (factor > 1)
+ *   RKV_ROPE_SMOOTH   the same with a ramp linear in the number of turns; mscale 1
+ * factor >= 1; ctx > 0, fast > slow > 0 for the last two (ignored by the others). rot_dim even,
+ * 2 .. 128; base > 1. Errors: RKV_ERR_INVALID_ARG. */
+#define RKV_ROPE_PLAIN 0
+#define RKV_ROPE_LINEAR 1
+#define RKV_ROPE_BASE 2
+#define RKV_ROPE_BY_PARTS 3
+#define RKV_ROPE_SMOOTH 4
+rkv_status rkv_rope_frequencies(int kind, int rot_dim, double base, double factor, int ctx,
+                                double fast, double slow, float* inv_freq, float* mscale);
+
+/* Turn the queries and keys of the new tokens to their positions and store the keys and values.
+ * For every token t with slots[t] >= 0, pair i < rot_dim / 2 of each head of q and k,
+ *   (a, b) -> mscale (a cos w - b sin w, b cos w + a sin w),   w = positions[t] * inv_freq[i],
+ * (a, b) being dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved; dimensions from
+ * rot_dim on stay as they are. fp32 arithmetic, rounded once; w is reduced exactly, however far
+ * the position (any int32).
+ *   q [tokens][hq][128], k, v [tokens][n_kv][128] bf16 with strides as above; inv_freq
+ *   [rot_dim / 2] fp32; positions, slots [tokens] int32
+ *   q_out    [tokens][hq][128] bf16, contiguous; may be q (then q_stride = hq * 128)
+ *   k_pool, v_pool [num_blocks][n_kv][block][128] bf16: row slots[t] of every KV head
+ *   rot_dim  a multiple of 16, 16 .. 128; hq >= 1 (hq need not be a multiple of n_kv)
+ * A token with a negative slot is left out: none of its rows is written. A slot at or past
+ * num_blocks * block sets RKV_DEV_BAD_INDEX, and the token is left out. Two tokens with one slot
+ * leave rows of either of them there, or pieces of both. */
+size_t rkv_rope_append_workspace_bytes(void);
+rkv_status rkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* positions,
+                           const float* inv_freq, const int32_t* slots, int tokens, int hq,
+                           int n_kv, int head_dim, int rot_dim, int interleaved, float mscale,
+                           void* q_out, void* k_pool, void* v_pool, int num_blocks, int block,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of a prompt, or of a chunk of one behind cached tokens: out[t][h] = softmax(scale *
+ * q[t][h] . K^T) V of KV head h / gqa of t's unit over the keys up to t's own. The unit's rows in the
+ * cache (len[u]) include those of its T = q_start[u+1] - q_start[u] new tokens, which are its last
+ * ones: token i stands at position len[u] - T + i. (One token each is a decode step.)
+ *   q        [tokens][n_kv*gqa][128] bf16, tokens q_stride elements apart
+ *   q_start  [n+1] int32 (device), ascending, within [0, tokens]
+ *   k, v     [n][n_kv][max_len][128] bf16, or pools with a block table as for the paged calls above
+ *            (block a power of two). Rows from len[u] on may hold anything; rows before that have
+ *            finite values (an infinite or NaN value of v makes NaN of outputs that do not see it).
+ *   len      [n] int32 (device), T <= len[u] <= max_len (paged: max_blocks * block)
+ *   out      [tokens][n_kv*gqa][128] bf16, contiguous; may not be q. Rows of tokens that belong to
+ *            no unit are left as they were.
+ *   gqa      1 .. 64
+ * len out of range: RKV_DEV_LEN_OVER_CAP; q_start out of order or range, or T > len[u]:
+ * RKV_DEV_BAD_WINDOW; the unit is skipped, its rows left as they were. A table entry outside the pool
+ * among the unit's blocks: RKV_DEV_BAD_INDEX, block 0 is read. RKV_ERR_TOO_LARGE where tokens * n_kv *
+ * gqa, or the rows of k, exceed 2^31 - 513. The softmax's numerators are rounded to bf16 for the
+ * product with V; everything else is fp32. */
+size_t rkv_prompt_attention_workspace_bytes(int n, int n_kv, int gqa, int tokens);
+rkv_status rkv_prompt_attention(const void* q, int64_t q_stride, const int32_t* q_start,
+                                const void* k, const void* v, const int32_t* len, int n, int n_kv,
+                                int gqa, int head_dim, int tokens, int max_len, float scale,
+                                void* out, void* ws, size_t ws_bytes, void* stream);
+rkv_status rkv_prompt_attention_paged(const void* q, int64_t q_stride, const int32_t* q_start,
+                                      const void* k_pool, const void* v_pool,
+                                      const int32_t* block_table, const int32_t* len, int n,
+                                      int n_kv, int gqa, int head_dim, int tokens, int num_blocks,
+                                      int block, int max_blocks, float scale, void* out, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* The same for a tree of drafted tokens: the unit's T new tokens see all of the len[u] - T rows before
+ * theirs, and among theirs those that a bit mask names: token t sees row len[u] - T + j iff bit j % 32
+ * of mask[t][j / 32] is set (its ancestors and itself; any mask is taken, bits from T on are ignored).
+ *   mask     [tokens][mask_words] int32, 1 <= mask_words <= 32; T <= 32 * mask_words (else
+ *            RKV_DEV_BAD_WINDOW, unit skipped)
+ * A token that sees nothing gets zeros. The drafted rows are in the cache in the tokens' order,
+ * whatever their positions (a token's position is the number of its ancestors behind the cached ones);
+ * the rows of those that were accepted are stored again in place (rkv_rope_append), the length then
+ * covers them only. Workspace rkv_prompt_attention_workspace_bytes; the rest as above. */
+rkv_status rkv_tree_attention(const void* q, int64_t q_stride, const int32_t* q_start,
+                              const int32_t* mask, int mask_words, const void* k, const void* v,
+                              const int32_t* len, int n, int n_kv, int gqa, int head_dim,
+                              int tokens, int max_len, float scale, void* out, void* ws,
+                              size_t ws_bytes, void* stream);
+rkv_status rkv_tree_attention_paged(const void* q, int64_t q_stride, const int32_t* q_start,
+                                    const int32_t* mask, int mask_words, const void* k_pool,
+                                    const void* v_pool, const int32_t* block_table,
+                                    const int32_t* len, int n, int n_kv, int gqa, int head_dim,
+                                    int tokens, int num_blocks, int block, int max_blocks,
+                                    float scale, void* out, void* ws, size_t ws_bytes,
+                                    void* stream);
 
 #ifdef __cplusplus
 }

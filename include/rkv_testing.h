@@ -4,7 +4,7 @@
  * The kernels never spin without a bound: every wait on an mbarrier gives up after a time limit,
  * records RKV_DEV_WAIT_TIMEOUT in the workspace's status word, lets the copies it already issued
  * land, frees its tensor memory and returns, so that the CUDA context stays usable and the host
- * learns of the failure through rkv_check_status. The two wait hooks make such a wait run out on
+ * learns of the failure through rkv_check_status. The wait hooks make such a wait run out on
  * purpose, without any GPU fault, so that a test can check that path.
  */
 #ifndef RKV_TESTING_H_
@@ -48,6 +48,25 @@ rkv_status rkv_testing_prompt_wait_timeout(const void* q, const int32_t* q_len, 
                                            int head_dim, int max_q, int max_len, float scale,
                                            float* weights, int what, uint64_t wait_limit_ns,
                                            void* ws, size_t ws_bytes, void* stream);
+
+/* rkv_prompt_attention with every mbarrier wait bounded by wait_limit_ns (in [1000, 1e9], instead of
+ * 1 s) and with one load of thread block 0 never requested, by `what`:
+ *   RKV_TESTING_ATTENTION_QUERIES  its first tile of queries (of the first of a pair's tiles)
+ *   RKV_TESTING_ATTENTION_KEYS     its first tile of keys
+ *   RKV_TESTING_ATTENTION_VALUES   its first tile of values
+ * The waits on it (and those on what would follow) run out, block 0 records RKV_DEV_WAIT_TIMEOUT and
+ * returns, every other block completes normally. Arguments and errors as rkv_prompt_attention; the
+ * outputs that block 0 has a part in are not meaningful after such a call. */
+#define RKV_TESTING_ATTENTION_QUERIES 1
+#define RKV_TESTING_ATTENTION_KEYS 2
+#define RKV_TESTING_ATTENTION_VALUES 3
+rkv_status rkv_testing_attention_wait_timeout(const void* q, int64_t q_stride,
+                                              const int32_t* q_start, const void* k,
+                                              const void* v, const int32_t* len, int n, int n_kv,
+                                              int gqa, int head_dim, int tokens, int max_len,
+                                              float scale, void* out, int what,
+                                              uint64_t wait_limit_ns, void* ws, size_t ws_bytes,
+                                              void* stream);
 
 /* Shared-memory layout of every later rkv_hybrid_decode call in this process, so that a test
  * can run each on the same inputs (the results do not depend on it; one CTA per (unit, KV head)

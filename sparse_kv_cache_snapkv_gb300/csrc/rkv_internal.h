@@ -273,6 +273,70 @@ struct PromptArgs {
 size_t prompt_scratch_bytes(int n, int n_kv, int gqa, int max_q, int max_len);
 cudaError_t launch_prompt_weights(const PromptArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------- packed attention
+constexpr int kMaxAttentionGqa = 64;  // query heads of a KV group
+constexpr int kMaxTreeWords = 32;     // 32-bit words of a drafted token's mask
+
+struct AttentionArgs {
+  const bf16* q;
+  long long q_stride;  // elements between tokens
+  const int32_t* q_start;
+  const uint32_t* mask;  // nullptr: causal
+  const bf16* k;
+  const bf16* v;
+  PagedMap pm;  // table == nullptr: not paged
+  const int32_t* len;
+  int n, n_kv, gqa, tokens, cap, words;
+  float scale_log2;
+  bf16* out;
+  void* scratch;  // workspace after the status word
+  uint32_t* status;
+  uint64_t wait_limit_ns;  // 0: the default bound of every mbarrier wait (1 s)
+  int test_skip;           // testing only (rkv_testing_attention_wait_timeout)
+};
+size_t attention_scratch_bytes(int n, int gqa, int tokens);
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------- rotary positions
+struct RopeArgs {
+  const bf16* q;
+  const bf16* k;
+  const bf16* v;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  const float* inv_freq;
+  const int32_t* slots;
+  bf16* q_out;
+  bf16* k_cache;
+  bf16* v_cache;
+  int tokens, hq, n_kv, rot, interleaved, num_blocks, block;
+  float mscale;
+  uint32_t* status;
+};
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------- block tables and slots
+struct SlotArgs {
+  const int32_t* new_len;
+  const int32_t* len;
+  const int32_t* held;
+  int32_t* table;
+  int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* q_start;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* len_out;
+  int32_t* held_out;
+  int32_t* free_count_out;
+  int n, max_blocks, num_blocks, block, room;  // room: entries of slots and positions
+  void* scratch;
+  uint32_t* status;
+};
+size_t slots_scratch_bytes(int n);
+cudaError_t launch_reserve_slots(const SlotArgs& a, cudaStream_t s);
+cudaError_t launch_release_blocks(const SlotArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------------------- eviction
 struct EvictArgs {
   // the cache's arrays and the bytes of a row in each (multiples of 8; unused ones are nullptr)

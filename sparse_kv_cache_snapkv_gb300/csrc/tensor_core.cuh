@@ -164,13 +164,13 @@ inline EncodeTiledFn get_encoder() {
   return fn;
 }
 
-// rows x 128 bf16, row-major, boxes of 128 rows x 64 columns, 128-byte swizzle
-inline bool make_rows_map(CUtensorMap* map, const void* base, uint64_t rows) {
+// rows x 128 bf16, row-major, boxes of `box_rows` rows x 64 columns, 128-byte swizzle
+inline bool make_rows_map(CUtensorMap* map, const void* base, uint64_t rows, int box_rows = 128) {
   EncodeTiledFn enc = get_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
-  cuuint32_t box[2] = {64, 128};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

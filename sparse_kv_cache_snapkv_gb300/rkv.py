@@ -39,6 +39,11 @@ SYMBOLS = [
     "rkv_dense_decode_weights_workspace_bytes", "rkv_dense_decode_weights",
     "rkv_prompt_weights_workspace_bytes", "rkv_prompt_weights", "rkv_evict_workspace_bytes",
     "rkv_evict", "rkv_evict_kv4", "rkv_testing_prompt_wait_timeout",
+    "rkv_reserve_slots_workspace_bytes", "rkv_reserve_slots", "rkv_release_blocks_workspace_bytes",
+    "rkv_release_blocks", "rkv_rope_frequencies", "rkv_rope_append_workspace_bytes",
+    "rkv_rope_append", "rkv_prompt_attention_workspace_bytes", "rkv_prompt_attention",
+    "rkv_prompt_attention_paged", "rkv_tree_attention", "rkv_tree_attention_paged",
+    "rkv_testing_attention_wait_timeout",
 ]
 
 
@@ -69,6 +74,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     vp, sz, i32, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
     u32p = ctypes.POINTER(ctypes.c_uint32)
     ip = ctypes.POINTER(ctypes.c_int)
+    i64, f64 = ctypes.c_int64, ctypes.c_double
     sigs = {
         "rkv_status_string": ([i32], ctypes.c_char_p),
         "rkv_check_status": ([vp, vp, u32p], i32),
@@ -139,6 +145,28 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                        sz, vp], i32),
         "rkv_evict_kv4": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                            i32, vp, vp, sz, vp], i32),
+        "rkv_reserve_slots_workspace_bytes": ([i32], sz),
+        "rkv_reserve_slots": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp,
+                               vp, vp, sz, vp], i32),
+        "rkv_release_blocks_workspace_bytes": ([i32], sz),
+        "rkv_release_blocks": ([vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp], i32),
+        "rkv_rope_frequencies": ([i32, i32, f64, f64, i32, f64, f64, vp, ctypes.POINTER(f32)],
+                                 i32),
+        "rkv_rope_append_workspace_bytes": ([], sz),
+        "rkv_rope_append": ([vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                             f32, vp, vp, vp, i32, i32, vp, sz, vp], i32),
+        "rkv_prompt_attention_workspace_bytes": ([i32, i32, i32, i32], sz),
+        "rkv_prompt_attention": ([vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp,
+                                  vp, sz, vp], i32),
+        "rkv_prompt_attention_paged": ([vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                        i32, i32, f32, vp, vp, sz, vp], i32),
+        "rkv_tree_attention": ([vp, i64, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                f32, vp, vp, sz, vp], i32),
+        "rkv_tree_attention_paged": ([vp, i64, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32,
+                                      i32, i32, i32, i32, f32, vp, vp, sz, vp], i32),
+        "rkv_testing_attention_wait_timeout": ([vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                                i32, f32, vp, i32, ctypes.c_uint64, vp, sz, vp],
+                                               i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -806,3 +834,179 @@ def rkv_evict_kv4(k_codes, k_scales, v_codes, v_scales, length, weights, pos, se
     n, n_kv, cap, ptrs = _kv4(k_codes, k_scales, v_codes, v_scales, dev)
     return _evict("rkv_evict_kv4", ptrs, n, n_kv, cap, HEAD_DIM, length, weights, pos, seen, keep,
                   recent, length_out, weights_out, pos_out, src_rows, ws, dev, stream)
+
+
+# ------------------------------------------------------------------------------- a serving step
+def _tokens(t, name, heads, dev, tokens=None):
+    """Address and token stride (elements) of packed rows [tokens][heads][128] bf16: contiguous, or a
+    slice of rows that hold more (the strides of tokens free, a token's heads side by side)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 3 and t.get_device() == dev
+            and t.shape[1] == heads and t.shape[2] == HEAD_DIM and tokens in (None, t.shape[0])
+            and t.stride(2) == 1 and (heads == 1 or t.stride(1) == HEAD_DIM)):
+        if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 3 and t.get_device() == dev:
+            if t.shape[1] == heads and t.shape[2] == HEAD_DIM and tokens in (None, t.shape[0]):
+                raise ValueError(f"{name}: the heads of a token must lie side by side")
+        _refuse(t, name, _BF16, (t.shape[0] if tokens is None and _rank(t) else tokens, heads, HEAD_DIM), dev)
+    stride = t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
+    p = t.data_ptr()
+    if p % 16 or stride % 8 or stride < heads * HEAD_DIM:
+        raise ValueError(f"{name}: tokens must begin on 16 bytes and not overlap")
+    return p, stride
+
+
+def _rank(t):
+    return isinstance(t, torch.Tensor) and t.dim() > 0
+
+
+def rkv_reserve_slots_workspace_bytes(n: int) -> int:
+    return int(load().rkv_reserve_slots_workspace_bytes(n))
+
+
+def rkv_reserve_slots(new_len, length, held, block_table, free_blocks, free_count, block: int, q_start,
+                      slots, positions, length_out, held_out, free_count_out, ws=None, stream=None):
+    """Places for new_len[u] more tokens of every unit: blocks off the free stack into block_table,
+    q_start [n + 1], and slots and positions [max_tokens] of the packed tokens; see include/rkv.h.
+    length_out, held_out and free_count_out may be the inputs."""
+    n, max_blocks = _dims(block_table, "block_table", 2)
+    num_blocks, room = _dims(free_blocks, "free_blocks", 1)[0], _dims(slots, "slots", 1)[0]
+    dev = block_table.get_device()
+    args = (_at(new_len, "new_len", _I32, (n,), dev), _at(length, "len", _I32, (n,), dev),
+            _at(held, "held", _I32, (n,), dev),
+            _at(block_table, "block_table", _I32, (n, max_blocks), dev),
+            _at(free_blocks, "free_blocks", _I32, (num_blocks,), dev),
+            _at(free_count, "free_count", _I32, (1,), dev), n, num_blocks, block, max_blocks, room,
+            _at(q_start, "q_start", _I32, (n + 1,), dev), _at(slots, "slots", _I32, (room,), dev),
+            _at(positions, "positions", _I32, (room,), dev),
+            _at(length_out, "len_out", _I32, (n,), dev), _at(held_out, "held_out", _I32, (n,), dev),
+            _at(free_count_out, "free_count_out", _I32, (1,), dev))
+    return _call("rkv_reserve_slots", args, ws, lambda: rkv_reserve_slots_workspace_bytes(n), dev,
+                 stream)
+
+
+def rkv_release_blocks_workspace_bytes(n: int) -> int:
+    return int(load().rkv_release_blocks_workspace_bytes(n))
+
+
+def rkv_release_blocks(length, held, block_table, free_blocks, free_count, block: int, held_out,
+                       free_count_out, ws=None, stream=None):
+    """Blocks that length[u] tokens do not need go back to the free stack; see include/rkv.h."""
+    n, max_blocks = _dims(block_table, "block_table", 2)
+    num_blocks = _dims(free_blocks, "free_blocks", 1)[0]
+    dev = block_table.get_device()
+    args = (_at(length, "len", _I32, (n,), dev), _at(held, "held", _I32, (n,), dev),
+            _at(block_table, "block_table", _I32, (n, max_blocks), dev),
+            _at(free_blocks, "free_blocks", _I32, (num_blocks,), dev),
+            _at(free_count, "free_count", _I32, (1,), dev), n, num_blocks, block, max_blocks,
+            _at(held_out, "held_out", _I32, (n,), dev),
+            _at(free_count_out, "free_count_out", _I32, (1,), dev))
+    return _call("rkv_release_blocks", args, ws, lambda: rkv_release_blocks_workspace_bytes(n), dev,
+                 stream)
+
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3, "smooth": 4}
+
+
+def rkv_rope_frequencies(rot_dim: int = HEAD_DIM, base: float = 10000.0, kind: str = "plain",
+                         factor: float = 1.0, ctx: int = 0, fast: float = 32.0, slow: float = 1.0):
+    """(inv_freq fp32 [rot_dim / 2] on the host, mscale) of the rotary positions; see include/rkv.h."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}")
+    freq = torch.empty(max(int(rot_dim), 2) // 2, dtype=torch.float32)
+    mscale = ctypes.c_float(0.0)
+    _check("rkv_rope_frequencies", load().rkv_rope_frequencies(
+        ROPE_KINDS[kind], rot_dim, base, factor, ctx, fast, slow, freq.data_ptr(),
+        ctypes.byref(mscale)))
+    return freq, mscale.value
+
+
+def rkv_rope_append_workspace_bytes() -> int:
+    return int(load().rkv_rope_append_workspace_bytes())
+
+
+def rkv_rope_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache,
+                    interleaved: bool = False, mscale: float = 1.0, ws=None, stream=None):
+    """Turns packed q [tokens][Hq][128] (into q_out) and k [tokens][n_kv][128] to their positions and
+    stores k and v in row slots[t] of the caches ([num_blocks][n_kv][block][128], or
+    [n][n_kv][cap][128] with slots u * cap + row); see include/rkv.h."""
+    tokens, hq, _ = _dims(q, "q", 3)
+    num_blocks, n_kv, block, d = shape = _dims(k_cache, "k_cache", 4)
+    dev = q.get_device()
+    rot = 2 * _dims(inv_freq, "inv_freq", 1)[0]
+    args = (*_tokens(q, "q", hq, dev), *_tokens(k, "k", n_kv, dev, tokens),
+            *_tokens(v, "v", n_kv, dev, tokens),
+            _at(positions, "positions", _I32, (tokens,), dev),
+            _at(inv_freq, "inv_freq", _F32, (rot // 2,), dev),
+            _at(slots, "slots", _I32, (tokens,), dev), tokens, hq, n_kv, d, rot, int(interleaved),
+            mscale, _at(q_out, "q_out", _BF16, (tokens, hq, HEAD_DIM), dev),
+            _at(k_cache, "k_cache", _BF16, shape, dev), _at(v_cache, "v_cache", _BF16, shape, dev),
+            num_blocks, block)
+    return _call("rkv_rope_append", args, ws, rkv_rope_append_workspace_bytes, dev, stream)
+
+
+def rkv_prompt_attention_workspace_bytes(n: int, n_kv: int, gqa: int, tokens: int) -> int:
+    return int(load().rkv_prompt_attention_workspace_bytes(n, n_kv, gqa, tokens))
+
+
+def _attention(fn, q, q_start, mask, k, v, table, length, scale, out, ws, stream, hook=()):
+    tokens, hq, _ = _dims(q, "q", 3)
+    lead, n_kv, rows, d = shape = _dims(k, "k", 4)
+    dev, n = q.get_device(), _dims(length, "len", 1)[0]
+    gqa = _group(hq, n_kv)
+    tree = ()
+    if mask is not None:
+        words = _dims(mask, "mask", 2)[1]
+        tree = (_at(mask, "mask", _I32, (tokens, words), dev), words)
+    if table is None:
+        if lead != n:
+            raise ValueError(f"{n} lengths for a cache of {lead} units")
+        paged, sizes = (), (tokens, rows)
+    else:
+        max_blocks = _dims(table, "block_table", 2)[1]
+        paged = (_at(table, "block_table", _I32, (n, max_blocks), dev),)
+        sizes = (tokens, lead, rows, max_blocks)
+    args = (*_tokens(q, "q", hq, dev), _at(q_start, "q_start", _I32, (n + 1,), dev), *tree,
+            _at(k, "k", _BF16, shape, dev), _at(v, "v", _BF16, shape, dev), *paged,
+            _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d, *sizes, scale,
+            _at(out, "out", _BF16, (tokens, hq, HEAD_DIM), dev), *hook)
+    return _call(fn, args, ws, lambda: rkv_prompt_attention_workspace_bytes(n, n_kv, gqa, tokens),
+                 dev, stream)
+
+
+def rkv_prompt_attention(q, q_start, k, v, length, scale: float, out, ws=None, stream=None):
+    """Causal attention of packed new tokens (q, out [tokens][Hq][128]; unit u's are
+    q_start[u] .. q_start[u + 1] - 1) over the unit's length[u] cached rows, theirs included and
+    last; see include/rkv.h."""
+    return _attention("rkv_prompt_attention", q, q_start, None, k, v, None, length, scale, out, ws,
+                      stream)
+
+
+def rkv_prompt_attention_paged(q, q_start, k_pool, v_pool, block_table, length, scale: float, out,
+                               ws=None, stream=None):
+    """rkv_prompt_attention over pools [num_blocks][n_kv][block][128] through block_table."""
+    _dims(block_table, "block_table", 2)
+    return _attention("rkv_prompt_attention_paged", q, q_start, None, k_pool, v_pool, block_table,
+                      length, scale, out, ws, stream)
+
+
+def rkv_tree_attention(q, q_start, mask, k, v, length, scale: float, out, ws=None, stream=None):
+    """Attention of a tree of drafted tokens: each sees the rows before the drafted ones, and of
+    those the ones that its bits in mask [tokens][words] int32 name; see include/rkv.h."""
+    _dims(mask, "mask", 2)
+    return _attention("rkv_tree_attention", q, q_start, mask, k, v, None, length, scale, out, ws,
+                      stream)
+
+
+def rkv_tree_attention_paged(q, q_start, mask, k_pool, v_pool, block_table, length, scale: float,
+                             out, ws=None, stream=None):
+    """rkv_tree_attention over pools [num_blocks][n_kv][block][128] through block_table."""
+    _dims(mask, "mask", 2), _dims(block_table, "block_table", 2)
+    return _attention("rkv_tree_attention_paged", q, q_start, mask, k_pool, v_pool, block_table,
+                      length, scale, out, ws, stream)
+
+
+def rkv_testing_attention_wait_timeout(q, q_start, k, v, length, scale: float, out, what: int,
+                                       wait_limit_ns: int, ws=None, stream=None):
+    """Test hook (include/rkv_testing.h): rkv_prompt_attention with one load of block 0 never
+    requested, so that its bounded waits run out after wait_limit_ns."""
+    return _attention("rkv_testing_attention_wait_timeout", q, q_start, None, k, v, None, length,
+                      scale, out, ws, stream, (int(what), int(wait_limit_ns)))
