@@ -21,6 +21,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/rkv_testing.h"
 #include "common.cuh"
@@ -29,7 +30,7 @@
 
 namespace rkv {
 
-constexpr int kAtThreads = 384;  // warp 0 loads, 1 multiplies, 2 and 3 clean; 4..7 and 8..11: a tile's softmax
+constexpr int kAtThreads = 384;  // warp 0 loads, 1 and 2 multiply, 3 cleans; 4..7 and 8..11: a tile's softmax
 constexpr int kAtRows = 128;     // rows of a tile
 constexpr int kAtTile = 128;     // cache rows of a step
 constexpr int kAtStages = 5;     // K and V tiles in flight
@@ -37,7 +38,7 @@ constexpr int kAtTileBytes = kAtTile * kHeadDim * 2;  // 32 KB
 constexpr uint32_t kAtCols = 512;                     // S or P of both tiles, O of both
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 1024;
-constexpr float kRaise = 16.f;
+constexpr float kLargest = 1048576.f;  // 2^20
 constexpr float kNoMax = -1e30f;
 constexpr int kSplitLeast = 2;   // steps of a CTA's range
 constexpr int kSplitGain = 6;    // steps that ranges must save over whole items: what parts and their join cost
@@ -220,8 +221,9 @@ struct Piece {
 
 struct Pieces {
   int split, count, per, total;
-  int wave;                   // whole items
-  int rec, head, off, left;   // ranges
+  int entry, head, off, left;  // of the piece to come; left: steps (split) or items
+  int wave;
+  AtRec ahead;                 // its record, loaded under the piece before
   __device__ __forceinline__ void init(const AtParams& p) {
     const AtPlan pl = *p.plan;
     split = pl.split;
@@ -229,45 +231,52 @@ struct Pieces {
     per = pl.per;
     total = pl.total;
     wave = 0;
-    left = 0;
+    off = head = entry = 0;
     if (split) {
       const AtFirst f = p.first[blockIdx.x];
-      rec = f.rec;
+      entry = f.rec;
       head = f.head;
       off = f.off;
-      const long long a = (long long)blockIdx.x * per;
-      left = f.rec < 0 ? 0 : (int)min((long long)per, total - a);
+      left = f.rec < 0 ? 0 : (int)min((long long)per, total - (long long)blockIdx.x * per);
+      if (left > 0) ahead = p.rec[entry];
+    } else {
+      item(p);
+    }
+  }
+  // whole items come in waves of one per CTA, every second wave from the other end
+  __device__ __forceinline__ void item(const AtParams& p) {
+    long long i = (long long)wave * gridDim.x + ((wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (i >= (long long)count * p.n_kv) {
+      ++wave;
+      i = (long long)wave * gridDim.x + ((wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    }
+    ++wave;
+    left = i < (long long)count * p.n_kv;
+    if (left) {
+      entry = (int)((uint32_t)i / (uint32_t)p.n_kv);
+      head = (int)i - entry * p.n_kv;
+      ahead = p.sorted[entry];
     }
   }
   __device__ __forceinline__ bool next(const AtParams& p, Piece& x) {
-    int len;
+    if (left <= 0) return false;
+    x.r = ahead;
+    x.g = head;
+    x.s0 = off;
+    int len = x.r.steps;
+    x.slot = -1;
     if (split) {
-      if (left <= 0) return false;
-      x.r = p.rec[rec];
-      x.g = head;
-      x.s0 = off;
       len = min(x.r.steps - off, left);
       x.slot = off > 0 ? 2 * (int)blockIdx.x : len < x.r.steps ? 2 * (int)blockIdx.x + 1 : -1;
       left -= len;
       off = 0;
       if (++head == p.n_kv) {
         head = 0;
-        ++rec;
+        ++entry;
       }
+      if (left > 0) ahead = p.rec[entry];
     } else {
-      const long long items = (long long)count * p.n_kv;
-      long long i;
-      do {
-        i = (long long)wave * gridDim.x + ((wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if ((long long)wave * gridDim.x >= items) return false;
-        ++wave;
-      } while (i >= items);
-      const int e = (int)(i / p.n_kv);
-      x.r = p.sorted[e];
-      x.g = (int)(i - (long long)e * p.n_kv);
-      x.s0 = 0;
-      len = x.r.steps;
-      x.slot = -1;
+      item(p);
     }
     x.steps = 0;
 #pragma unroll
@@ -296,28 +305,54 @@ __device__ __forceinline__ void reg_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// D += A B with A (bf16, 128 x 16) in TMEM.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
-// V as the B operand of P V: rows are the reduction, dimensions contiguous (64 of them in 128 bytes,
-// swizzled; the other 64 are 16 KB further, eight rows 1024 bytes).
-__device__ __forceinline__ uint64_t desc_rows_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(16384 >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
+// Upper halves of the operands' descriptors; the lower ones are the address in units of 16 bytes, and
+// bits 16 on. K-major rows of 128 bytes (Q, K): eight rows are 1024 bytes apart. V is the B operand with its
+// rows as the reduction and 64 dimensions in 128 bytes: the other 64 are 16 KB further, eight rows 1024 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kDescLoK = 1u << 16, kDescLoV = (16384u >> 4) << 16;
 constexpr uint32_t kIdescS = idesc_bf16(kAtRows, kAtTile);
 constexpr uint32_t kIdescO = idesc_bf16(kAtRows, kHeadDim) | (1u << 16);  // B is not K-major
+
+// D (+)= A B, both in shared memory.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t keep) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}"
+      ::"r"(d), "r"(a | kDescLoK), "r"(b | kDescLoK), "n"(kDescHi), "n"(kIdescS), "r"(keep));
+}
+// D (+)= A B with A (bf16, 128 x 16) in TMEM and B a tile of V.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t keep) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b | kDescLoV), "n"(kDescHi), "n"(kIdescO), "r"(keep));
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// A place of the ring, and the parity of its load.
+struct Ring {
+  int place;
+  uint32_t phase;
+  __device__ __forceinline__ void step() {
+    if (++place == kAtStages) {
+      place = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -330,6 +365,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
+}
+// A whole sector at once.
+__device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -345,6 +386,76 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Which keys a row sees: all below `clear` (the same for every row of a warp); of the others those up to
+// `lim`, or in a tree those whose bit is set, T of them from `base` on (T = 0: not a row).
+struct AtSees {
+  int clear, lim, base, T;
+  const uint32_t* bits;
+};
+
+// Sets the keys that the row does not see to -infinity, in 32 columns from key k on.
+template <bool TREE>
+__device__ __forceinline__ void at_hide(uint32_t (&s)[32], int k, const AtSees& a) {
+  if (TREE) {
+    const int d = k - a.base;  // number of the first key among the new ones
+    // bits d .. d + 31 of the row, ones where d is below 0, zeros from T on
+    uint32_t sees = 0u;
+    if (a.T > 0) {
+      const int w = d >> 5, o = d & 31;
+      const uint32_t lo = w < 0 ? 0xffffffffu : w * 32 < a.T ? a.bits[w] : 0u;
+      const uint32_t hi = (w + 1) * 32 < a.T ? a.bits[w + 1] : 0u;
+      sees = o ? (lo >> o) | (hi << (32 - o)) : lo;
+      const int end = a.T - d;
+      if (end < 32) sees &= end <= 0 ? 0u : (1u << end) - 1u;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!((sees >> i) & 1u)) s[i] = 0xff800000u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (k + i > a.lim) s[i] = 0xff800000u;
+  }
+}
+
+// What most steps do not need, in functions of their own, so that the steps' code has neither its branches
+// nor its registers (with branches for the masks between the chunks: 8K prompt 440 us).
+//
+// A step with keys that some row does not see, or an item's first: sets those to -infinity where S lies, and
+// returns the maximum of m and all scores.
+template <bool TREE>
+__device__ __noinline__ float at_prepare(uint32_t sp, int k0, AtSees sees, float scale, float m) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32];
+    tmem_ld32(sp + 32 * c, s);
+    if (k0 + 32 * c + 32 > sees.clear) {
+      at_hide<TREE>(s, k0 + 32 * c, sees);
+      tmem_st32(sp + 32 * c, s);
+    }
+    float y[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      y[(i >> 1) & 3] = max3(y[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    m = fmaxf(m, fmaxf(max3(y[0], y[1], y[2]), y[3]) * scale);
+  }
+  tmem_st_wait();
+  return m;
+}
+
+// Scales O by f. (The product before this step's S is done: S was issued behind it.)
+__device__ __noinline__ void at_scale(uint32_t o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32];
+    tmem_ld32(o + 32 * c, s);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
+    tmem_st32(o + 32 * c, s);
+  }
+  tmem_st_wait();
+}
+
 struct AtBars {
   uint64_t full[kAtStages], empty[kAtStages];  // the ring of K and V tiles
   uint64_t qfull[2], qempty[2];
@@ -353,7 +464,8 @@ struct AtBars {
   uint64_t ofull[2];   // the item's last product is done
   uint64_t ofree[2];   // O has been read
   uint64_t dirty, clean;      // a V tile with rows behind the last is next; they are zeros
-  uint64_t drain;      // everything issued is done (after a wait gave up)
+  uint64_t turn[2];    // a tile's turn to issue
+  uint64_t drain[2];   // everything a warp issued is done (after a wait gave up)
   uint32_t tmem;
 };
 static_assert(sizeof(AtBars) <= 256, "");
@@ -375,7 +487,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kAtStages; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.qfull[i], 1);
@@ -384,10 +496,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bar.pfull[i], 4);
       mbar_init(&bar.ofull[i], 1);
       mbar_init(&bar.ofree[i], 4);
+      mbar_init(&bar.drain[i], 1);
+      mbar_init(&bar.turn[i], 1);
     }
-    mbar_init(&bar.dirty, 1);
-    mbar_init(&bar.clean, 2);
-    mbar_init(&bar.drain, 1);
+    mbar_init(&bar.dirty, 2);
+    mbar_init(&bar.clean, 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -490,87 +603,104 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (nq[h] > 0) mbar_wait_warp(&bar.qfull[h], (uint32_t)((nq[h] - 1) & 1), drain_limit(limit));
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      int steps = 0;  // steps begun: K tile 2 steps of the ring, V tile 2 steps + 1
-      int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, nclean = 0;
-      bool pend[2] = {false, false}, first[2] = {false, false}, last[2] = {false, false};  // P V products to come
-      int vload = 0;
-      bool vtail = false, vwaited = false, vboth = false;
-      auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (!aborted && !mbar_wait(b, parity, limit)) aborted = true;
-        return !aborted;
-      };
-      auto product = [&](int h) {  // O of tile h += P V
-        pend[h] = false;
-        if (!wait(&bar.pfull[h], (uint32_t)(np[h] & 1))) return;
-        ++np[h];
-        if (first[h] && no[h] > 0 && !wait(&bar.ofree[h], (uint32_t)((no[h] - 1) & 1))) return;
-        const int s = vload % kAtStages;
-        if (!vwaited) {
-          if (!wait(&bar.full[s], (uint32_t)((vload / kAtStages) & 1))) return;
-          if (vtail && !wait(&bar.clean, (uint32_t)(nclean++ & 1))) return;
-          vwaited = true;
-        }
-        tc_fence_after();
-        const uint32_t b = smem_addr(ring + (size_t)s * kAtTileBytes);
-        const uint32_t d = tmem + 256 + h * 128, a = tmem + h * 128;
+  } else if (warp < 3) {
+    // ------------------------------------------------------------------ products of a tile
+    // A warp for each tile of the pair: one waits while the other issues (one warp for both left the tensor
+    // cores idle between its waits: 8K prompt 425 us). The whole warp follows the steps and one lane issues, so
+    // that descriptors are uniform values, a constant away from those of a place of the ring (with one lane
+    // computing them for itself: 510 us).
+    const int h = warp - 1;
+    const uint32_t ring_lo = (smem_addr(ring) & 0x3FFFFu) >> 4;
+    const uint32_t q_lo = ((smem_addr(qs) & 0x3FFFFu) >> 4) + h * (kAtTileBytes >> 4);
+    const uint32_t st = tmem + h * 128, ot = st + 256;
+    uint32_t nq = 0, np = 0, no = 0, nclean = 0;
+    Ring kr{0, 0}, vr{0, 0}, at{0, 0};  // K tile of the step, V tile of the product to come, next load
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      if (!aborted && !mbar_wait_warp(b, parity & 1u, limit)) aborted = true;
+    };
+    // A step's scores are issued behind the product of the step before, which they follow in the tensor
+    // cores. The tiles take turns with that: products of both at once would end together, and then both
+    // softmaxes would run while the tensor cores wait (8K prompt 496 us). The turn passes on two products
+    // before the last, which hides its way to the other warp.
+    bool pend = false, first = false, last = false, tail = false;
+    uint32_t nturn = 0;
+    auto product = [&](bool pass) {  // O += P V
+      const uint32_t b = ring_lo + vr.place * (kAtTileBytes >> 4), keep = first ? 0u : 1u;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ta(d, a + 8 * kk, desc_rows_sw128(b + kk * 2048), kIdescO, kk > 0 || !first[h]);
-        if (h == 1 || !vboth) umma_commit(&bar.empty[s]);
-        if (last[h]) {
-          umma_commit(&bar.ofull[h]);
-          ++no[h];
-        }
-      };
-      auto scores = [&](int h, bool begin, bool end, bool only, int kload) {  // S of tile h = Q K^T
-        if (begin && !wait(&bar.qfull[h], (uint32_t)(nq[h]++ & 1))) return;
-        const int s = kload % kAtStages;
-        if (!wait(&bar.full[s], (uint32_t)((kload / kAtStages) & 1))) return;
-        tc_fence_after();
-        const uint32_t a = smem_addr(qs + (size_t)h * kAtTileBytes);
-        const uint32_t b = smem_addr(ring + (size_t)s * kAtTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-          umma_bf16(tmem + h * 128, desc_sw128(a + off), desc_sw128(b + off), kIdescS, kk > 0);
-        }
-        umma_commit(&bar.sfull[h]);
-        if (end) umma_commit(&bar.qempty[h]);
-        if (h == 1 || only) umma_commit(&bar.empty[s]);
-      };
-      while (!aborted && it.next(p, x)) {
-        for (int j = 0; j < x.steps && !aborted; ++j, ++steps) {
-          const bool act[2] = {j < x.cnt[0], j < x.cnt[1]};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!aborted && pend[h]) product(h);
-            if (!aborted && act[h]) scores(h, j == 0, j == x.cnt[h] - 1, !act[1], 2 * steps);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            pend[h] = act[h];
-            first[h] = j == 0;
-            last[h] = j == x.cnt[h] - 1;
-          }
-          vload = 2 * steps + 1;
-          vboth = act[1];
-          vwaited = false;
-          vtail = (x.s0 + j + 1) * kAtTile > x.r.L;
-          if (vtail) mbar_arrive(&bar.dirty);
-        }
+      for (int kk = 0; kk < 8; ++kk) {
+        umma_ts(ot, st + 8 * kk, b + kk * (2048 >> 4), kk ? 1u : keep);
+        if (kk == 5 && pass) mbar_arrive(&bar.turn[h ^ 1]);
       }
+      umma_commit(&bar.empty[vr.place]);
+      if (last) umma_commit(&bar.ofull[h]);
+    };
+    auto scores = [&](bool end) {  // S = Q K^T
+      const uint32_t b = ring_lo + kr.place * (kAtTileBytes >> 4);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (!aborted && pend[h]) product(h);
-      if (aborted) {
-        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
-        umma_commit(&bar.drain);  // let issued products end
-        mbar_wait(&bar.drain, 0u, drain_limit(limit));
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        umma_ss(st, q_lo + off, b + off, kk > 0);
+        if (kk == 5) mbar_arrive(&bar.turn[h ^ 1]);
+      }
+      umma_commit(&bar.sfull[h]);
+      umma_commit(&bar.empty[kr.place]);
+      if (end) umma_commit(&bar.qempty[h]);
+    };
+    auto ready = [&]() {  // what the product to come needs
+      wait(&bar.full[vr.place], vr.phase);
+      if (tail) wait(&bar.clean, nclean++);
+      if (first && no > 0) wait(&bar.ofree[h], no - 1);
+      wait(&bar.pfull[h], np++);
+      if (last) ++no;
+    };
+    while (!aborted && it.next(p, x)) {
+      for (int j = 0; j < x.steps && !aborted; ++j) {
+        const bool act = j < x.cnt[h], end = j == x.cnt[h] - 1;
+        kr = at;
+        at.step();
+        if (act && j == 0) wait(&bar.qfull[h], nq++);
+        wait(&bar.full[kr.place], kr.phase);
+        if (pend) ready();
+        if (h == 1 || nturn > 0) wait(&bar.turn[h], h == 1 ? nturn : nturn - 1);
+        ++nturn;
+        tc_fence_after();
+        if (!aborted && elect_one()) {
+          if (pend) product(!act);
+          if (act) {
+            scores(end);
+          } else {  // a step that the tile has no part in
+            if (!pend) mbar_arrive(&bar.turn[h ^ 1]);
+            mbar_arrive(&bar.empty[kr.place]);
+          }
+        }
+        __syncwarp();
+        pend = act;
+        first = j == 0;
+        last = end;
+        vr = at;
+        at.step();
+        tail = (x.s0 + j + 1) * kAtTile > x.r.L;
+        if (tail && lane == 0) mbar_arrive(&bar.dirty);
+        if (!act) {
+          wait(&bar.full[vr.place], vr.phase);
+          if (tail) wait(&bar.clean, nclean++);
+          if (!aborted && lane == 0) mbar_arrive(&bar.empty[vr.place]);
+          __syncwarp();
+        }
       }
     }
+    if (!aborted && pend) {
+      ready();
+      tc_fence_after();
+      if (!aborted && elect_one()) product(false);
+      __syncwarp();
+    }
+    if (aborted && lane == 0) {
+      set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+      umma_commit(&bar.drain[h]);  // let issued products end
+      mbar_wait(&bar.drain[h], 0u, drain_limit(limit));
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------------ rows behind the last
     // p is 0 there, but 0 times what the cache may hold (infinity, NaN) is not. The tile's place in the ring
@@ -586,9 +716,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           aborted = true;
           break;
         }
-        // (warps 2 and 3: 64 dimensions each)
-        uint4* v = reinterpret_cast<uint4*>(ring + (size_t)s * kAtTileBytes + (warp - 2) * 16384 + cut * 128);
-        for (int i = lane; i < (kAtTile - cut) * 8; i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        uint4* v = reinterpret_cast<uint4*>(ring + (size_t)s * kAtTileBytes + cut * 128);
+        for (int i = lane; i < (kAtTile - cut) * 8; i += 32)
+          v[i] = v[i + 16384 / 16] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.clean);
@@ -605,151 +735,113 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t sp = tmem + lanes + h * 128, od = tmem + lanes + 256 + h * 128;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     const int tok = row / p.gqa, head = row - tok * p.gqa;
-    int ns = 0, no = 0;  // waits for S and for the last product
+    uint32_t ns = 0, no = 0;  // waits for S and for the last product
     while (!aborted && it.next(p, x)) {
       const int t = x.r.t0 + h * p.tile_tokens + tok;  // this row's token
       const bool valid = tok < p.tile_tokens && t < x.r.T;
       const int base = x.r.L - x.r.T;
       const int lim = valid ? base + t : -1;  // last key of a causal row
       const bool idle = !__any_sync(0xffffffffu, valid);
+      // keys below `clear` are seen by every row of the warp that is one
+      const int clear = TREE ? base : __reduce_min_sync(0xffffffffu, valid ? lim : 0x7ffffffe) + 1;
       const uint32_t* bits = TREE ? p.mask + (size_t)(x.r.row0 + h * p.tile_tokens + tok) * p.words : nullptr;
       float m = kNoMax, l = 0.f;
-      for (int j = 0; j < x.cnt[h] && !aborted; ++j) {
-        if (!mbar_wait_warp(&bar.sfull[h], (uint32_t)(ns & 1), limit)) {
+      const AtSees sees{clear, lim, base, valid ? x.r.T : 0, bits};
+      for (int j = 0; j < x.cnt[h]; ++j) {
+        if (!mbar_wait_warp(&bar.sfull[h], ns++ & 1u, limit)) {
           aborted = true;
           break;
         }
-        ++ns;
         if (idle) {
           if (lane == 0) mbar_arrive(&bar.pfull[h]);
           continue;
         }
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_start(sp + 32 * c, s[c]);
         const int k0 = (x.s0 + j) * kAtTile;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
-        // keys that the row does not see
-        if (TREE) {
-          if (k0 + kAtTile > base) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int d = k0 + 32 * c - base;  // number of the chunk's first key among the new ones
-              uint32_t sees = 0xffffffffu;
-              if (d > -32) {
-                // bits d .. d + 31 of the row, ones where d is below 0, zeros from T on
-                sees = 0u;
-                if (valid) {
-                  const int w = d >> 5, o = d & 31;
-                  const uint32_t a = w < 0 ? 0xffffffffu : w * 32 < x.r.T ? bits[w] : 0u;
-                  const uint32_t b = (w + 1) * 32 < x.r.T ? bits[w + 1] : 0u;
-                  sees = o ? (a >> o) | (b << (32 - o)) : a;
-                  const int end = x.r.T - d;
-                  if (end < 32) sees &= end <= 0 ? 0u : (1u << end) - 1u;
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((sees >> i) & 1u)) s[c][i] = 0xff800000u;
-            }
-          }
-        } else if (__any_sync(0xffffffffu, k0 + kAtTile - 1 > lim)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (k0 + 32 * c + i > lim) s[c][i] = 0xff800000u;
+        if (j == 0 || k0 + kAtTile > clear) {
+          const float to = at_prepare<TREE>(sp, k0, sees, p.scale_log2, m);
+          if (j == 0) m = to;
         }
-        float mt[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mt[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int i = 1; i < 32; ++i) mt[c] = fmaxf(mt[c], __uint_as_float(s[c][i]));
-        }
-        const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * p.scale_log2;
-        if (j == 0) {
-          m = fmaxf(mn, kNoMax);
-        } else if (__any_sync(0xffffffffu, mn > m + kRaise)) {
-          // (the product before this step's S is done: S was issued behind it)
-          const float to = fmaxf(m, mn), f = fast_exp2(m - to);
-          m = to;
-          l *= f;
+        uint32_t out[2][32];
+        float sum;
+#pragma unroll 1
+        for (bool again = j == 0;; again = true) {
+          // numerators relative to m, which most often holds: no maximum is looked for. A chunk's load runs
+          // under the one before it.
+          const uint64_t off = pack2(-m, -m);
+          uint64_t acc[2] = {0ull, 0ull};
+          uint32_t s[2][32];
+          tmem_ld32_start(sp, s[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(od + 32 * c, o);
+            tmem_ld_wait(s[c & 1]);
+            if (c < 3) tmem_ld32_start(sp + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(od + 32 * c, o);
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(s[c & 1][2 * i]), __uint_as_float(s[c & 1][2 * i + 1])),
+                                            scale2, off));
+              const float e0 = fast_exp2(y.x), e1 = fast_exp2(y.y);
+              acc[i & 1] = add2(acc[i & 1], pack2(e0, e1));
+              out[c >> 1][16 * (c & 1) + i] = pack_bf16x2(e0, e1);
+            }
           }
+          const float2 z = unpack2(add2(acc[0], acc[1]));
+          sum = z.x + z.y;
+          if (again || !__any_sync(0xffffffffu, valid && !(sum < kLargest))) break;
+          const float to = at_prepare<TREE>(sp, k0, sees, p.scale_log2, m), f = fast_exp2(m - to);
+          at_scale(od, f);
+          l *= f;
+          m = to;
         }
-        const uint64_t off = pack2(-m, -m);
-        uint64_t acc[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t out[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int a = 2 * i + 64 * c;
-            const float2 y = unpack2(fma2(pack2(__uint_as_float(s[a >> 5][a & 31]),
-                                                __uint_as_float(s[a >> 5][(a & 31) + 1])), scale2, off));
-            const float e0 = fast_exp2(y.x), e1 = fast_exp2(y.y);
-            acc[i & 1] = add2(acc[i & 1], pack2(e0, e1));
-            out[i] = pack_bf16x2(e0, e1);
-          }
-          tmem_st32(sp + 32 * c, out);
-        }
+        tmem_st32(sp, out[0]);
+        tmem_st32(sp + 32, out[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.pfull[h]);
-        const float2 sum = unpack2(add2(acc[0], acc[1]));
-        l += sum.x + sum.y;
+        l += sum;
       }
       if (aborted) break;
       if (x.cnt[h] == 0) {  // a part that this tile has no steps in
         if (x.slot >= 0) p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(kNoMax, 0.f);
         continue;
       }
-      if (!mbar_wait_warp(&bar.ofull[h], (uint32_t)(no & 1), limit)) {
+      if (!mbar_wait_warp(&bar.ofull[h], no++ & 1u, limit)) {
         aborted = true;
         break;
       }
-      ++no;
       tc_fence_after();
       if (!idle) {
         const bool none = l == 0.f;  // the row sees nothing: zeros, whatever v holds
         const float f = l > 0.f ? 1.f / l : l;
         bf16* dst = p.out + ((size_t)(x.r.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
         float* part = p.part_o + ((size_t)max(x.slot, 0) * 256 + h * 128 + row) * kHeadDim;
+        uint32_t o[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(od + 32 * c, o);
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.ofree[h]);
-          }
-          if (valid && x.slot >= 0) {
+        for (int c = 0; c < 4; ++c) tmem_ld32_start(od + 32 * c, o[c]);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          } else if (valid) {
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(o[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ofree[h]);
+        if (valid && x.slot >= 0) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = none ? 0u : pack_bf16x2(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
-              *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 32; i += 8) st_global32(part + 32 * c + i, o[c] + i);
+        } else if (valid) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = none ? 0u : pack_bf16x2(__uint_as_float(o[c][i + 2 * k]) * f, __uint_as_float(o[c][i + 2 * k + 1]) * f);
+              st_global32(dst + 32 * c + i, w);
             }
-          }
-          __syncwarp();
         }
+        __syncwarp();
       } else if (lane == 0) {
         mbar_arrive(&bar.ofree[h]);
       }
@@ -767,9 +859,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 }
 
 // Joins the parts of the items that ranges cut: the item in which CTA x + 1's range begins, unless it was
-// cut before already (grid: ranges' borders x groups of rows; a warp per row, four columns a lane).
-constexpr int kJoinRows = 32;
-__global__ void __launch_bounds__(256) at_join_kernel(AtParams p) {
+// cut before already (grid: ranges' borders x groups of rows; a warp per row, four columns a lane). A lane
+// holds a part's weight, so that the parts' loads do not wait for one another.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(32 * kJoinRows) at_join_kernel(AtParams p) {
   pdl_wait();
   const AtPlan pl = *p.plan;
   if (!pl.split) return;
@@ -781,28 +874,43 @@ __global__ void __launch_bounds__(256) at_join_kernel(AtParams p) {
   if (c0 != c - 1) return;
   const AtRec r = p.rec[f.rec];
   const int parts = (int)((a + r.steps - 1) / pl.per) - c0 + 1;
-  for (int k = warp; k < kJoinRows; k += 8) {
-    const int row = blockIdx.y * kJoinRows + k, tok = (row & 127) / p.gqa, t = (row >> 7) * p.tile_tokens + tok;
-    if (tok >= p.tile_tokens || r.t0 + t >= r.T) continue;
-    float m = kNoMax, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < parts; ++i) {
-      const size_t at = (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row;
-      const float2 y = p.part_ml[at];
-      if (y.y == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * lane);
-      const float to = fmaxf(m, y.x), f0 = fast_exp2(m - to), f1 = fast_exp2(y.x - to);
-      m = to;
-      l = l * f0 + y.y * f1;
-      o.x = o.x * f0 + v.x * f1;
-      o.y = o.y * f0 + v.y * f1;
-      o.z = o.z * f0 + v.z * f1;
-      o.w = o.w * f0 + v.w * f1;
+  const int row = blockIdx.y * kJoinRows + warp, tok = (row & 127) / p.gqa, t = (row >> 7) * p.tile_tokens + tok;
+  if (tok >= p.tile_tokens || r.t0 + t >= r.T) return;
+  auto at = [&](int i) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row; };
+  float m = kNoMax, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int n = min(32, parts - i0);
+    const float2 y = lane < n ? p.part_ml[at(i0 + lane)] : make_float2(kNoMax, 0.f);
+    // (a part without a visible key has the sum 0, and its outputs are not looked at)
+    float to = y.y == 0.f ? kNoMax : y.x;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, k));
+    to = fmaxf(to, m);
+    const float w = y.y == 0.f ? 0.f : fast_exp2(y.x - to), f0 = fast_exp2(m - to);
+    float s = w * y.y;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    m = to;
+    l = l * f0 + s;
+    o.x *= f0;
+    o.y *= f0;
+    o.z *= f0;
+    o.w *= f0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (wi == 0.f) continue;
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at(i0 + i) * kHeadDim + 4 * lane);
+      o.x += v.x * wi;
+      o.y += v.y * wi;
+      o.z += v.z * wi;
+      o.w += v.w * wi;
     }
-    const float s = l > 0.f ? 1.f / l : l;
-    bf16* dst = p.out + ((size_t)(r.row0 + t) * p.hq + f.head * p.gqa + (row & 127) - tok * p.gqa) * kHeadDim;
-    *reinterpret_cast<uint2*>(dst + 4 * lane) = make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
   }
+  const float s = l > 0.f ? 1.f / l : l;
+  bf16* dst = p.out + ((size_t)(r.row0 + t) * p.hq + f.head * p.gqa + (row & 127) - tok * p.gqa) * kHeadDim;
+  *reinterpret_cast<uint2*>(dst + 4 * lane) = make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
 }
 
 // ------------------------------------------------------------------------------------------
@@ -912,7 +1020,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   else
     e = paged ? launch_at<true, false>(qm, km, vm, p, s) : launch_at<false, false>(qm, km, vm, p, s);
   if (e != cudaSuccess || p.ctas < 2) return e;
-  return launch_pdl_kernel(at_join_kernel, dim3(p.ctas - 1, 256 / kJoinRows), dim3(256), 0, s, p);
+  return launch_pdl_kernel(at_join_kernel, dim3(p.ctas - 1, 256 / kJoinRows),
+                           dim3(32 * kJoinRows), 0, s, p);
 }
 
 }  // namespace rkv
