@@ -30,11 +30,13 @@
 
 namespace rkv {
 
-constexpr int kAtThreads = 384;  // warp 0 loads, 1 and 2 multiply, 3 cleans; 4..7 and 8..11: a tile's softmax
+constexpr int kAtThreads = 384;  // warp 0 loads, 1 and 2 multiply, 3 finds the pieces; 4..7 and 8..11: a tile's softmax
 constexpr int kAtRows = 128;     // rows of a tile
 constexpr int kAtTile = 128;     // cache rows of a step
 constexpr int kAtStages = 5;     // K and V tiles in flight
 constexpr int kAtTileBytes = kAtTile * kHeadDim * 2;  // 32 KB
+constexpr int kAtPieces = 4;     // pieces that the finding warp may be ahead
+constexpr int kAtReaders = 11;   // warps that read them
 constexpr uint32_t kAtCols = 512;                     // S or P of both tiles, O of both
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 1024;
@@ -47,7 +49,8 @@ struct AtSmem {
   static constexpr size_t q_off = 0;
   static constexpr size_t ring_off = 2 * (size_t)kAtTileBytes;
   static constexpr size_t bar_off = ring_off + (size_t)kAtStages * kAtTileBytes;
-  static constexpr size_t total = bar_off + 256;
+  static constexpr size_t piece_off = bar_off + 512;
+  static constexpr size_t total = piece_off + kAtPieces * 48;
 };
 static_assert(AtSmem::total <= 232448, "shared memory of a CTA");
 
@@ -209,15 +212,17 @@ __global__ void __launch_bounds__(kPlanThreads) at_plan_kernel(AtParams p) {
 static_assert(kPlanBuckets == kPlanThreads, "one bucket per thread in the scan");
 
 // ------------------------------------------------------------------------------------------
-// the pieces of a CTA, the same for every warp
+// the pieces of a CTA: one warp finds them, the others read them in shared memory
 // ------------------------------------------------------------------------------------------
-struct Piece {
-  AtRec r;
-  int g, s0;    // KV head, first step
-  int cnt[2];   // steps of each tile, from s0
-  int steps;    // the larger of the two
-  int slot;     // where its part goes; -1: the item is whole
+struct __align__(16) Piece {
+  int row0, t0, T, L;  // as in its AtRec
+  int u, g, s0;        // unit, KV head, first step
+  int steps;           // the larger of cnt; 0: there is no piece any more
+  int cnt[2];          // steps of each tile, from s0
+  int slot;            // where its part goes; -1: the item is whole
+  int pad;
 };
+static_assert(sizeof(Piece) == 48, "three 16-byte words");
 
 struct Pieces {
   int split, count, per, total;
@@ -259,15 +264,21 @@ struct Pieces {
     }
   }
   __device__ __forceinline__ bool next(const AtParams& p, Piece& x) {
+    x.steps = 0;
     if (left <= 0) return false;
-    x.r = ahead;
+    const AtRec r = ahead;
+    x.row0 = r.row0;
+    x.t0 = r.t0;
+    x.T = r.T;
+    x.L = r.L;
+    x.u = r.u;
     x.g = head;
     x.s0 = off;
-    int len = x.r.steps;
+    int len = r.steps;
     x.slot = -1;
     if (split) {
-      len = min(x.r.steps - off, left);
-      x.slot = off > 0 ? 2 * (int)blockIdx.x : len < x.r.steps ? 2 * (int)blockIdx.x + 1 : -1;
+      len = min(r.steps - off, left);
+      x.slot = off > 0 ? 2 * (int)blockIdx.x : len < r.steps ? 2 * (int)blockIdx.x + 1 : -1;
       left -= len;
       off = 0;
       if (++head == p.n_kv) {
@@ -278,12 +289,11 @@ struct Pieces {
     } else {
       item(p);
     }
-    x.steps = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int t = x.r.t0 + h * p.tile_tokens;  // the tile's first token
-      const int keys = p.mask ? x.r.L : x.r.L - x.r.T + min(t + p.tile_tokens, x.r.T);
-      const int all = t < x.r.T ? (keys + kAtTile - 1) / kAtTile : 0;
+      const int t = x.t0 + h * p.tile_tokens;  // the tile's first token
+      const int keys = p.mask ? x.L : x.L - x.T + min(t + p.tile_tokens, x.T);
+      const int all = t < x.T ? (keys + kAtTile - 1) / kAtTile : 0;
       x.cnt[h] = max(0, min(x.s0 + len, all) - x.s0);
       x.steps = max(x.steps, x.cnt[h]);
     }
@@ -393,11 +403,11 @@ struct AtSees {
   const uint32_t* bits;
 };
 
-// Sets the keys that the row does not see to -infinity, in 32 columns from key k on.
+// Sets the keys that the row does not see to -infinity, in 32 columns from key k on (k + 32 > clear).
 template <bool TREE>
 __device__ __forceinline__ void at_hide(uint32_t (&s)[32], int k, const AtSees& a) {
   if (TREE) {
-    const int d = k - a.base;  // number of the first key among the new ones
+    const int d = k - a.base;  // number of the first key among the new ones, above -32 (base is `clear`)
     // bits d .. d + 31 of the row, ones where d is below 0, zeros from T on
     uint32_t sees = 0u;
     if (a.T > 0) {
@@ -425,22 +435,26 @@ __device__ __forceinline__ void at_hide(uint32_t (&s)[32], int k, const AtSees& 
 // returns the maximum of m and all scores.
 template <bool TREE>
 __device__ __noinline__ float at_prepare(uint32_t sp, int k0, AtSees sees, float scale, float m) {
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t s[32];
-    tmem_ld32(sp + 32 * c, s);
-    if (k0 + 32 * c + 32 > sees.clear) {
-      at_hide<TREE>(s, k0 + 32 * c, sees);
-      tmem_st32(sp + 32 * c, s);
-    }
-    float y[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
+  uint32_t s[4][32];
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      y[(i >> 1) & 3] = max3(y[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-    m = fmaxf(m, fmaxf(max3(y[0], y[1], y[2]), y[3]) * scale);
+  for (int c = 0; c < 4; ++c) tmem_ld32_start(sp + 32 * c, s[c]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+  if (k0 + kAtTile > sees.clear) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (k0 + 32 * c + 32 > sees.clear) {
+        at_hide<TREE>(s[c], k0 + 32 * c, sees);
+        tmem_st32(sp + 32 * c, s[c]);
+      }
   }
+  float y[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
+#pragma unroll
+  for (int i = 0; i < 32; i += 2)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = max3(y[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
   tmem_st_wait();
-  return m;
+  return fmaxf(m, fmaxf(max3(y[0], y[1], y[2]), y[3]) * scale);
 }
 
 // Scales O by f. (The product before this step's S is done: S was issued behind it.)
@@ -464,11 +478,12 @@ struct AtBars {
   uint64_t ofull[2];   // the item's last product is done
   uint64_t ofree[2];   // O has been read
   uint64_t dirty, clean;      // a V tile with rows behind the last is next; they are zeros
+  uint64_t pfilled[kAtPieces], pread[kAtPieces];  // pieces
   uint64_t turn[2];    // a tile's turn to issue
   uint64_t drain[2];   // everything a warp issued is done (after a wait gave up)
   uint32_t tmem;
 };
-static_assert(sizeof(AtBars) <= 256, "");
+static_assert(sizeof(AtBars) <= 512, "");
 
 template <bool PAGED, bool TREE>
 __global__ void __launch_bounds__(kAtThreads, 1)
@@ -499,6 +514,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bar.drain[i], 1);
       mbar_init(&bar.turn[i], 1);
     }
+    for (int i = 0; i < kAtPieces; ++i) {
+      mbar_init(&bar.pfilled[i], 1);
+      mbar_init(&bar.pread[i], kAtReaders);
+    }
     mbar_init(&bar.dirty, 2);
     mbar_init(&bar.clean, 1);
     fence_barrier_init();
@@ -516,9 +535,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   pdl_trigger();
   const WaitLimit limit = p.wait_limit;
   bool aborted = false;
-  Pieces it;
-  it.init(p);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + AtSmem::piece_off);
   Piece x{};
+  uint32_t npiece = 0;
+  auto next = [&]() {  // the next piece, for a warp other than the one that finds them
+    const uint32_t i = npiece % kAtPieces;
+    if (!mbar_wait_warp(&bar.pfilled[i], (npiece / kAtPieces) & 1u, limit)) {
+      aborted = true;
+      return false;
+    }
+    const int4* src = reinterpret_cast<const int4*>(pieces + i);
+    int4* dst = reinterpret_cast<int4*>(&x);
+    dst[0] = src[0];
+    dst[1] = src[1];
+    dst[2] = src[2];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.pread[i]);
+    ++npiece;
+    return x.steps > 0;
+  };
 
   if (warp < 4) {
   reg_release<kAtLoadRegs>();
@@ -542,30 +577,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     auto tile = [&](const CUtensorMap* map, int s, int k0, int blk) {
       uint8_t* dst = ring + (size_t)s * kAtTileBytes;
       if (PAGED) {
-        const int copies = min(kAtTile / rows, (x.r.L - k0 + rows - 1) / rows);
+        const int copies = min(kAtTile / rows, (x.L - k0 + rows - 1) / rows);
         if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(copies * rows * 256));
         __syncwarp();
         for (int c = lane; c < copies; c += 32) {
           const int t = k0 + c * rows;
-          const int b = c == lane ? blk : paged_block(p.pm, x.r.u, t, p.status);
+          const int b = c == lane ? blk : paged_block(p.pm, x.u, t, p.status);
           const int y = (b * p.n_kv + x.g) * p.pm.block + (t & (p.pm.block - 1));
           tma_load_2d(dst + c * rows * 128, map, 0, y, &bar.full[s]);
           tma_load_2d(dst + 16384 + c * rows * 128, map, 64, y, &bar.full[s]);
         }
       } else if (lane == 0) {
-        const int y = (x.r.u * p.n_kv + x.g) * p.cap + k0;
+        const int y = (x.u * p.n_kv + x.g) * p.cap + k0;
         mbar_arrive_expect_tx(&bar.full[s], kAtTileBytes);
         tma_load_2d(dst, map, 0, y, &bar.full[s]);
         tma_load_2d(dst + 16384, map, 64, y, &bar.full[s]);
       }
       __syncwarp();
     };
-    while (!aborted && it.next(p, x)) {
+    while (!aborted && next()) {
       for (int j = 0; j < x.steps && !aborted; ++j) {
         const int k0 = (x.s0 + j) * kAtTile;
         int blk = 0;
-        if (PAGED && k0 + lane * rows < x.r.L && lane * rows < kAtTile)
-          blk = paged_block(p.pm, x.r.u, k0 + lane * rows, p.status);
+        if (PAGED && k0 + lane * rows < x.L && lane * rows < kAtTile)
+          blk = paged_block(p.pm, x.u, k0 + lane * rows, p.status);
         int s = slot();
         if (s < 0) break;
         if (!(skip == RKV_TESTING_ATTENTION_KEYS && ld == 0)) tile(&kmap, s, k0, blk);
@@ -583,7 +618,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               mbar_arrive_expect_tx(&bar.qfull[h], qbytes);
               for (int c = 0; c < 2; ++c)
                 tma_load_3d(dst + c * 16384, &qmap, 64 * c, x.g * p.gqa,
-                            x.r.row0 + h * p.tile_tokens, &bar.qfull[h]);
+                            x.row0 + h * p.tile_tokens, &bar.qfull[h]);
             }
             __syncwarp();
             ++nq[h];
@@ -631,7 +666,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         umma_ts(ot, st + 8 * kk, b + kk * (2048 >> 4), kk ? 1u : keep);
         if (kk == 5 && pass) mbar_arrive(&bar.turn[h ^ 1]);
       }
-      umma_commit(&bar.empty[vr.place]);
       if (last) umma_commit(&bar.ofull[h]);
     };
     auto scores = [&](bool end) {  // S = Q K^T
@@ -643,7 +677,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (kk == 5) mbar_arrive(&bar.turn[h ^ 1]);
       }
       umma_commit(&bar.sfull[h]);
-      umma_commit(&bar.empty[kr.place]);
       if (end) umma_commit(&bar.qempty[h]);
     };
     auto ready = [&]() {  // what the product to come needs
@@ -653,7 +686,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       wait(&bar.pfull[h], np++);
       if (last) ++no;
     };
-    while (!aborted && it.next(p, x)) {
+    while (!aborted && next()) {
       for (int j = 0; j < x.steps && !aborted; ++j) {
         const bool act = j < x.cnt[h], end = j == x.cnt[h] - 1;
         kr = at;
@@ -679,7 +712,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         last = end;
         vr = at;
         at.step();
-        tail = (x.s0 + j + 1) * kAtTile > x.r.L;
+        tail = (x.s0 + j + 1) * kAtTile > x.L;
         if (tail && lane == 0) mbar_arrive(&bar.dirty);
         if (!act) {
           wait(&bar.full[vr.place], vr.phase);
@@ -702,13 +735,42 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------------ rows behind the last
-    // p is 0 there, but 0 times what the cache may hold (infinity, NaN) is not. The tile's place in the ring
-    // is its own from when its step's scores are issued (they are behind all products that used the place)
-    // until its product, so the wait for its load cannot be taken for another one's.
+    // ------------------------------------------------------------------ pieces, rows behind the last
+    Pieces it;
+    it.init(p);
+    auto find = [&](uint32_t k) {  // piece k; false: there is none
+      const uint32_t i = k % kAtPieces;
+      if (k >= kAtPieces && !mbar_wait_warp(&bar.pread[i], (k / kAtPieces - 1) & 1u, limit)) {
+        aborted = true;
+        return false;
+      }
+      Piece y{};
+      const bool any = it.next(p, y);
+      if (lane == 0) {
+        const int4* src = reinterpret_cast<const int4*>(&y);
+        int4* dst = reinterpret_cast<int4*>(pieces + i);
+        dst[0] = src[0];
+        dst[1] = src[1];
+        dst[2] = src[2];
+        mbar_arrive(&bar.pfilled[i]);
+      }
+      __syncwarp();
+      return any;
+    };
+    // p is 0 for keys behind the last, but 0 times what the cache may hold there (infinity, NaN) is not. The
+    // tile's place in the ring is its own from when its step's scores are issued (they are behind all products
+    // that used the place) until its product, so the wait for its load cannot be taken for another one's.
     int steps = 0, ntail = 0;
-    while (!aborted && it.next(p, x)) {
-      const int at = x.r.L / kAtTile - x.s0, cut = x.r.L % kAtTile;  // the step that the sequence ends in
+    uint32_t found = 0;
+    bool more = true;
+    for (uint32_t k = 0; !aborted; ++k) {
+      while (more && found <= k + 2 && !aborted) more = find(found++);
+      if (aborted) break;
+      // (its own reading of a piece: no other warp writes them)
+      x = pieces[k % kAtPieces];
+      __syncwarp();
+      if (x.steps == 0) break;
+      const int at = x.L / kAtTile - x.s0, cut = x.L % kAtTile;  // the step that the sequence ends in
       if (cut && at >= 0 && at < x.steps) {
         const int load = 2 * (steps + at) + 1, s = load % kAtStages;
         if (!mbar_wait_warp(&bar.dirty, (uint32_t)(ntail++ & 1), limit) ||
@@ -736,22 +798,33 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     const int tok = row / p.gqa, head = row - tok * p.gqa;
     uint32_t ns = 0, no = 0;  // waits for S and for the last product
-    while (!aborted && it.next(p, x)) {
-      const int t = x.r.t0 + h * p.tile_tokens + tok;  // this row's token
-      const bool valid = tok < p.tile_tokens && t < x.r.T;
-      const int base = x.r.L - x.r.T;
+    Ring at{0, 0};            // the step's K tile
+    int vplace = 0;           // the V tile of the step before
+    while (!aborted && next()) {
+      const int t = x.t0 + h * p.tile_tokens + tok;  // this row's token
+      const bool valid = tok < p.tile_tokens && t < x.T;
+      const int base = x.L - x.T;
       const int lim = valid ? base + t : -1;  // last key of a causal row
       const bool idle = !__any_sync(0xffffffffu, valid);
       // keys below `clear` are seen by every row of the warp that is one
       const int clear = TREE ? base : __reduce_min_sync(0xffffffffu, valid ? lim : 0x7ffffffe) + 1;
-      const uint32_t* bits = TREE ? p.mask + (size_t)(x.r.row0 + h * p.tile_tokens + tok) * p.words : nullptr;
+      const uint32_t* bits = TREE ? p.mask + (size_t)(x.row0 + h * p.tile_tokens + tok) * p.words : nullptr;
       float m = kNoMax, l = 0.f;
-      const AtSees sees{clear, lim, base, valid ? x.r.T : 0, bits};
+      const AtSees sees{clear, lim, base, valid ? x.T : 0, bits};
       for (int j = 0; j < x.cnt[h]; ++j) {
         if (!mbar_wait_warp(&bar.sfull[h], ns++ & 1u, limit)) {
           aborted = true;
           break;
         }
+        // This S is done, and the product before it: their tiles' places are free. (A commit for each cost the
+        // issuing warp 50 clocks.)
+        if (row == 0) {
+          mbar_arrive(&bar.empty[at.place]);
+          if (j > 0) mbar_arrive(&bar.empty[vplace]);
+        }
+        at.step();
+        vplace = at.place;
+        at.step();
         if (idle) {
           if (lane == 0) mbar_arrive(&bar.pfull[h]);
           continue;
@@ -802,6 +875,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         l += sum;
       }
       if (aborted) break;
+      for (int j = x.cnt[h]; j < x.steps; ++j) {  // steps of the other tile alone
+        at.step();
+        at.step();
+      }
       if (x.cnt[h] == 0) {  // a part that this tile has no steps in
         if (x.slot >= 0) p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(kNoMax, 0.f);
         continue;
@@ -810,11 +887,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         aborted = true;
         break;
       }
+      if (row == 0) mbar_arrive(&bar.empty[vplace]);
       tc_fence_after();
       if (!idle) {
         const bool none = l == 0.f;  // the row sees nothing: zeros, whatever v holds
         const float f = l > 0.f ? 1.f / l : l;
-        bf16* dst = p.out + ((size_t)(x.r.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
+        bf16* dst = p.out + ((size_t)(x.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
         float* part = p.part_o + ((size_t)max(x.slot, 0) * 256 + h * 128 + row) * kHeadDim;
         uint32_t o[4][32];
 #pragma unroll
