@@ -30,13 +30,14 @@
 
 namespace rkv {
 
-constexpr int kAtThreads = 384;  // warp 0 loads, 1 and 2 multiply, 3 finds the pieces; 4..7 and 8..11: a tile's softmax
+constexpr int kAtThreads = 512;  // warp 0 loads, 1 and 2 multiply, 3 finds the pieces; 4..7: outputs;
+                                // 8..11 and 12..15: a tile's softmax
 constexpr int kAtRows = 128;     // rows of a tile
 constexpr int kAtTile = 128;     // cache rows of a step
 constexpr int kAtStages = 5;     // K and V tiles in flight
 constexpr int kAtTileBytes = kAtTile * kHeadDim * 2;  // 32 KB
 constexpr int kAtPieces = 4;     // pieces that the finding warp may be ahead
-constexpr int kAtReaders = 11;   // warps that read them
+constexpr int kAtReaders = 15;   // warps that read them
 constexpr uint32_t kAtCols = 512;                     // S or P of both tiles, O of both
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 1024;
@@ -50,7 +51,8 @@ struct AtSmem {
   static constexpr size_t ring_off = 2 * (size_t)kAtTileBytes;
   static constexpr size_t bar_off = ring_off + (size_t)kAtStages * kAtTileBytes;
   static constexpr size_t piece_off = bar_off + 512;
-  static constexpr size_t total = piece_off + kAtPieces * 48;
+  static constexpr size_t sum_off = piece_off + kAtPieces * 48;  // [2 turns][2 tiles][128]
+  static constexpr size_t total = sum_off + 2 * 2 * kAtRows * 4;
 };
 static_assert(AtSmem::total <= 232448, "shared memory of a CTA");
 
@@ -303,9 +305,9 @@ struct Pieces {
 
 // A warpgroup's registers per thread: the first hands back what the others then take (setmaxnreg; the
 // shares add up to what the block was launched with, so that no take can wait for ever).
-constexpr int kAtLoadRegs = 88, kAtSoftmaxRegs = 208, kAtLaunchRegs = 168;
-static_assert(kAtLoadRegs + 2 * kAtSoftmaxRegs <= 3 * kAtLaunchRegs, "");
-static_assert(kAtThreads * kAtLaunchRegs <= 65536 && kAtThreads * (kAtLaunchRegs + 8) > 65536, "");
+constexpr int kAtLoadRegs = 64, kAtOutRegs = 80, kAtSoftmaxRegs = 184, kAtLaunchRegs = 128;
+static_assert(kAtLoadRegs + kAtOutRegs + 2 * kAtSoftmaxRegs <= 4 * kAtLaunchRegs, "");
+static_assert(kAtThreads * kAtLaunchRegs == 65536, "");
 template <int N>
 __device__ __forceinline__ void reg_release() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -477,6 +479,7 @@ struct AtBars {
   uint64_t pfull[2];   // P of a step is written
   uint64_t ofull[2];   // the item's last product is done
   uint64_t ofree[2];   // O has been read
+  uint64_t lfull[2][2];  // a tile's sums are there (by turns)
   uint64_t dirty, clean;      // a V tile with rows behind the last is next; they are zeros
   uint64_t pfilled[kAtPieces], pread[kAtPieces];  // pieces
   uint64_t turn[2];    // a tile's turn to issue
@@ -511,6 +514,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bar.pfull[i], 4);
       mbar_init(&bar.ofull[i], 1);
       mbar_init(&bar.ofree[i], 4);
+      mbar_init(&bar.lfull[i][0], 4);
+      mbar_init(&bar.lfull[i][1], 4);
       mbar_init(&bar.drain[i], 1);
       mbar_init(&bar.turn[i], 1);
     }
@@ -536,6 +541,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const WaitLimit limit = p.wait_limit;
   bool aborted = false;
   Piece* pieces = reinterpret_cast<Piece*>(smem + AtSmem::piece_off);
+  float* sums = reinterpret_cast<float*>(smem + AtSmem::sum_off);
   Piece x{};
   uint32_t npiece = 0;
   auto next = [&]() {  // the next piece, for a warp other than the one that finds them
@@ -788,16 +794,73 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       steps += x.steps;
     }
   }
+  } else if (warp < 8) {
+    reg_release<kAtOutRegs>();
+    // ------------------------------------------------------------------ outputs
+    // While the softmax warps are at the next item. A row's sum comes in one of two places, by turns.
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const int tok = row / p.gqa, head = row - tok * p.gqa;
+    uint32_t no[2] = {0, 0};
+    int steps = 0;
+    while (!aborted && next()) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (aborted || x.cnt[h] == 0) continue;
+        const int t = x.t0 + h * p.tile_tokens + tok;  // this row's token
+        const bool valid = tok < p.tile_tokens && t < x.T;
+        const uint32_t turn = no[h] & 1;
+        if (!mbar_wait_warp(&bar.ofull[h], turn, limit) ||
+            !mbar_wait_warp(&bar.lfull[h][turn], (no[h] >> 1) & 1u, limit)) {
+          aborted = true;
+          continue;
+        }
+        ++no[h];
+        if (row == 0) mbar_arrive(&bar.empty[(2 * (steps + x.cnt[h] - 1) + 1) % kAtStages]);  // the last V tile
+        tc_fence_after();
+        const float l = sums[turn * 256 + h * 128 + row];
+        const bool none = l == 0.f;  // the row sees nothing: zeros, whatever v holds
+        const float f = l > 0.f ? 1.f / l : l;
+        const uint32_t od = tmem + ((uint32_t)(quarter * 32) << 16) + 256 + h * 128;
+        bf16* dst = p.out + ((size_t)(x.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
+        float* part = p.part_o + ((size_t)max(x.slot, 0) * 256 + h * 128 + row) * kHeadDim;
+        if (__any_sync(0xffffffffu, valid)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(od + 32 * c, o);
+            if (valid && x.slot >= 0) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) st_global32(part + 32 * c + i, o + i);
+            } else if (valid) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  w[k] = none ? 0u : pack_bf16x2(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
+                st_global32(dst + 32 * c + i, w);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ofree[h]);
+      }
+      steps += x.steps;
+    }
+    if (aborted && lane == 0) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
   } else {
     reg_take<kAtSoftmaxRegs>();
     // ------------------------------------------------------------------ softmax of a tile
-    const int h = (warp >> 2) - 1, quarter = warp & 3;
+    const int h = (warp >> 2) - 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t sp = tmem + lanes + h * 128, od = tmem + lanes + 256 + h * 128;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    const int tok = row / p.gqa, head = row - tok * p.gqa;
-    uint32_t ns = 0, no = 0;  // waits for S and for the last product
+    const int tok = row / p.gqa;
+    uint32_t ns = 0, no = 0;  // waits for S; items
     Ring at{0, 0};            // the step's K tile
     int vplace = 0;           // the V tile of the step before
     while (!aborted && next()) {
@@ -879,51 +942,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at.step();
         at.step();
       }
-      if (x.cnt[h] == 0) {  // a part that this tile has no steps in
-        if (x.slot >= 0) p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(kNoMax, 0.f);
-        continue;
-      }
-      if (!mbar_wait_warp(&bar.ofull[h], no++ & 1u, limit)) {
-        aborted = true;
-        break;
-      }
-      if (row == 0) mbar_arrive(&bar.empty[vplace]);
-      tc_fence_after();
-      if (!idle) {
-        const bool none = l == 0.f;  // the row sees nothing: zeros, whatever v holds
-        const float f = l > 0.f ? 1.f / l : l;
-        bf16* dst = p.out + ((size_t)(x.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
-        float* part = p.part_o + ((size_t)max(x.slot, 0) * 256 + h * 128 + row) * kHeadDim;
-        uint32_t o[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_start(od + 32 * c, o[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(o[c]);
-        tc_fence_before();
+      if (x.slot >= 0)  // (l = 0: a part that the tile has no steps in, or rows that see nothing in)
+        p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(m, valid ? l : 0.f);
+      if (x.cnt[h] > 0) {
+        sums[(no & 1) * 256 + h * 128 + row] = l;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ofree[h]);
-        if (valid && x.slot >= 0) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) st_global32(part + 32 * c + i, o[c] + i);
-        } else if (valid) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                w[k] = none ? 0u : pack_bf16x2(__uint_as_float(o[c][i + 2 * k]) * f, __uint_as_float(o[c][i + 2 * k + 1]) * f);
-              st_global32(dst + 32 * c + i, w);
-            }
-        }
-        __syncwarp();
-      } else if (lane == 0) {
-        mbar_arrive(&bar.ofree[h]);
+        if (lane == 0) mbar_arrive(&bar.lfull[h][no & 1]);
+        ++no;
       }
-      if (x.slot >= 0) p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(m, valid ? l : 0.f);
     }
     if (aborted && lane == 0) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
   }
