@@ -118,6 +118,7 @@ rkv_status rkv_reserve_slots(const int32_t* new_len, const int32_t* len, const i
   a.num_blocks = num_blocks;
   a.block = block;
   a.room = max_tokens;
+  a.wide = aligned16(slots) && aligned16(positions);
   a.scratch = after_status(ws);
   a.status = status_ptr(ws);
   return from_cuda(launch_reserve_slots(a, as_stream(stream)));

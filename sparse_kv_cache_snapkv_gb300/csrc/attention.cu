@@ -40,11 +40,12 @@ constexpr int kAtPieces = 4;     // pieces that the finding warp may be ahead
 constexpr int kAtReaders = 15;   // warps that read them
 constexpr uint32_t kAtCols = 512;                     // S or P of both tiles, O of both
 constexpr int kPlanThreads = 1024;
+constexpr int kFewPairs = 64;    // pairs of tiles whose plan a warp makes in its registers
 constexpr int kPlanBuckets = 1024;
 constexpr float kLargest = 1048576.f;  // 2^20
 constexpr float kNoMax = -1e30f;
 constexpr int kSplitLeast = 2;   // steps of a CTA's range
-constexpr int kSplitGain = 6;    // steps that ranges must save over whole items: what parts and their join cost
+constexpr int kSplitGain = 12;    // steps that ranges must save over whole items: what parts and their join cost
 
 struct AtSmem {
   static constexpr size_t q_off = 0;
@@ -80,6 +81,7 @@ struct AtFirst {
 
 struct AtParams {
   int n, n_kv, gqa, hq, tokens, cap, words, room, ctas;
+  int few;          // 1: every CTA makes the plan of at most kFewPairs pairs itself
   int tile_tokens;  // 128 / gqa
   float scale_log2;
   const int32_t* q_start;
@@ -118,6 +120,13 @@ __device__ __forceinline__ bool at_unit(const AtParams& p, int u, int* row0, int
   }
   *T = b - a;
   return true;
+}
+
+// Whole items, unless the longest would outlast an equal share of all steps by what parts and their join cost.
+__device__ __forceinline__ AtPlan at_decide(long long total, int longest, int count, int ctas) {
+  const long long each = (total + ctas - 1) / ctas;
+  const int split = total < (1ll << 30) && longest - each >= kSplitGain && longest * 4ll > each * 5ll;
+  return AtPlan{split, count, (int)max((long long)kSplitLeast, min(each, 1ll << 30)), (int)min(total, 1ll << 30)};
 }
 
 __global__ void __launch_bounds__(kPlanThreads) at_plan_kernel(AtParams p) {
@@ -177,10 +186,10 @@ __global__ void __launch_bounds__(kPlanThreads) at_plan_kernel(AtParams p) {
   }
   const long long total = steps_before * p.n_kv;
   if (tid == 0) {
-    const long long each = (total + p.ctas - 1) / p.ctas;
-    sh_split = total < (1ll << 30) && longest - each >= kSplitGain && longest * 4ll > each * 5ll;
-    sh_per = (int)max((long long)kSplitLeast, min(each, 1ll << 30));
-    *p.plan = AtPlan{sh_split, count, sh_per, (int)min(total, 1ll << 30)};
+    const AtPlan pl = at_decide(total, longest, count, p.ctas);
+    sh_split = pl.split;
+    sh_per = pl.per;
+    *p.plan = pl;
   }
   __syncthreads();
   if (!sh_split) {  // largest first
@@ -231,8 +240,17 @@ struct Pieces {
   int entry, head, off, left;  // of the piece to come; left: steps (split) or items
   int wave;
   AtRec ahead;                 // its record, loaded under the piece before
+  AtRec mine[2];               // few pairs: lane i holds those of pairs i and 32 + i,
+  int rank[2];                 // and their places in the sorted order
   __device__ __forceinline__ void init(const AtParams& p) {
-    const AtPlan pl = *p.plan;
+    AtFirst f{-1, 0, 0, 0};
+    AtPlan pl;
+    if (p.few) {
+      pl = plan(p, f);
+    } else {
+      pl = *p.plan;
+      if (pl.split) f = p.first[blockIdx.x];
+    }
     split = pl.split;
     count = pl.count;
     per = pl.per;
@@ -240,15 +258,115 @@ struct Pieces {
     wave = 0;
     off = head = entry = 0;
     if (split) {
-      const AtFirst f = p.first[blockIdx.x];
       entry = f.rec;
       head = f.head;
       off = f.off;
       left = f.rec < 0 ? 0 : (int)min((long long)per, total - (long long)blockIdx.x * per);
-      if (left > 0) ahead = p.rec[entry];
+      if (left > 0) ahead = record(p, entry);
     } else {
       item(p);
     }
+  }
+  __device__ __forceinline__ AtRec record(const AtParams& p, int e) const {
+    if (!p.few) return split ? p.rec[e] : p.sorted[e];
+    if (!split) {
+      const uint32_t b0 = __ballot_sync(0xffffffffu, rank[0] == e), b1 = __ballot_sync(0xffffffffu, rank[1] == e);
+      e = b0 ? __ffs(b0) - 1 : 31 + __ffs(b1);
+    }
+    AtRec r;
+    const int src = e & 31;
+    const bool hi = e >= 32;
+    auto get = [&](int a, int b) {
+      a = __shfl_sync(0xffffffffu, a, src);
+      b = __shfl_sync(0xffffffffu, b, src);
+      return hi ? b : a;
+    };
+    r.row0 = get(mine[0].row0, mine[1].row0);
+    r.t0 = get(mine[0].t0, mine[1].t0);
+    r.T = get(mine[0].T, mine[1].T);
+    r.L = get(mine[0].L, mine[1].L);
+    r.u = get(mine[0].u, mine[1].u);
+    r.steps = get(mine[0].steps, mine[1].steps);
+    r.before = get(mine[0].before, mine[1].before);
+    r.pad = 0;
+    return r;
+  }
+  // What at_plan_kernel does, for few pairs and by one warp. What the join reads is left where it looks.
+  __device__ __forceinline__ AtPlan plan(const AtParams& p, AtFirst& f) {
+    const int lane = threadIdx.x & 31, pair = 2 * p.tile_tokens;
+    int row0[2], T[2], L[2], first[2], n = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int u = 32 * i + lane;
+      row0[i] = T[i] = L[i] = 0;
+      if (u < p.n) at_unit(p, u, &row0[i], &T[i], &L[i]);
+      const int tiles = (T[i] + pair - 1) / pair, incl = warp_incl_scan(tiles);
+      first[i] = u < p.n ? n + incl - tiles : 0x7fffffff;  // the unit's first pair
+      n += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    // (units that overlap could come to more pairs than there is room for)
+    if (n > p.room && lane == 0) set_status(p.status, RKV_DEV_BAD_WINDOW);
+    n = min(n, p.room);
+    int longest = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 32 * i + lane;
+      int u = 0;  // the last unit whose pairs begin at or before e
+#pragma unroll
+      for (int step = 32; step; step >>= 1) {
+        const int at = u + step, a = __shfl_sync(0xffffffffu, first[0], at & 31), b = __shfl_sync(0xffffffffu, first[1], at & 31);
+        if ((at >= 32 ? b : a) <= e) u = at;
+      }
+      auto get = [&](const int (&x)[2]) {
+        const int a = __shfl_sync(0xffffffffu, x[0], u & 31), b = __shfl_sync(0xffffffffu, x[1], u & 31);
+        return u >= 32 ? b : a;
+      };
+      AtRec& r = mine[i];
+      r.u = u;
+      r.T = get(T);
+      r.L = get(L);
+      r.t0 = (e - get(first)) * pair;
+      r.row0 = get(row0) + r.t0;
+      const int keys = p.mask ? r.L : r.L - r.T + min(r.t0 + pair, r.T);
+      r.steps = e < n ? (keys + kAtTile - 1) / kAtTile : 0;
+      const int incl = warp_incl_scan(r.steps);
+      r.before = before + incl - r.steps;
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      longest = max(longest, __reduce_max_sync(0xffffffffu, r.steps));
+      r.pad = 0;
+      if (blockIdx.x == 0 && e < n) p.rec[e] = r;
+    }
+    const AtPlan pl = at_decide((long long)before * p.n_kv, longest, n, p.ctas);
+    if (blockIdx.x == 0 && lane == 0) *p.plan = pl;
+    if (pl.split) {
+      split = 1;
+      const long long a = (long long)blockIdx.x * pl.per;
+      if (a < pl.total) {  // the last pair that begins at or before a
+        const uint32_t b0 = __ballot_sync(0xffffffffu, lane < n && (long long)mine[0].before * p.n_kv <= a);
+        const uint32_t b1 = __ballot_sync(0xffffffffu, 32 + lane < n && (long long)mine[1].before * p.n_kv <= a);
+        f.rec = b1 ? 63 - __clz(b1) : 31 - __clz(b0);
+        const AtRec r = record(p, f.rec);
+        const int x = (int)(a - (long long)r.before * p.n_kv);
+        f.head = x / r.steps;
+        f.off = x - f.head * r.steps;
+      }
+      if (lane == 0) p.first[blockIdx.x] = f;
+    } else {
+      const bool order = (long long)n * p.n_kv > gridDim.x;  // (else all are begun at once)
+      int k[2] = {lane, 32 + lane};
+      if (order) {
+        k[0] = k[1] = 0;
+        for (int e = 0; e < n; ++e) {
+          const int a = __shfl_sync(0xffffffffu, mine[0].steps, e & 31), b = __shfl_sync(0xffffffffu, mine[1].steps, e & 31);
+          const int y = e >= 32 ? b : a;
+          k[0] += y > mine[0].steps || (y == mine[0].steps && e < lane);
+          k[1] += y > mine[1].steps || (y == mine[1].steps && e < 32 + lane);
+        }
+      }
+      rank[0] = lane < n ? k[0] : -1;
+      rank[1] = 32 + lane < n ? k[1] : -1;
+    }
+    return pl;
   }
   // whole items come in waves of one per CTA, every second wave from the other end
   __device__ __forceinline__ void item(const AtParams& p) {
@@ -262,7 +380,7 @@ struct Pieces {
     if (left) {
       entry = (int)((uint32_t)i / (uint32_t)p.n_kv);
       head = (int)i - entry * p.n_kv;
-      ahead = p.sorted[entry];
+      ahead = record(p, entry);
     }
   }
   __device__ __forceinline__ bool next(const AtParams& p, Piece& x) {
@@ -287,7 +405,7 @@ struct Pieces {
         head = 0;
         ++entry;
       }
-      if (left > 0) ahead = p.rec[entry];
+      if (left > 0) ahead = record(p, entry);
     } else {
       item(p);
     }
@@ -965,56 +1083,102 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // Joins the parts of the items that ranges cut: the item in which CTA x + 1's range begins, unless it was
 // cut before already (grid: ranges' borders x groups of rows; a warp per row, four columns a lane). A lane
 // holds a part's weight, so that the parts' loads do not wait for one another.
-constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(32 * kJoinRows) at_join_kernel(AtParams p) {
+constexpr int kJoinWarps = 16;
+
+// R rows of an item by a warp, their loads under way together.
+template <int R>
+__device__ __forceinline__ void join_rows(const AtParams& p, const AtRec& r, int g, int c0, int parts, int row0) {
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int i, int k) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row0 + k; };
+  bool valid[R], any = false;
+  int tok[R];
+  float m[R], l[R];
+  float4 o[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int row = row0 + k, t = (row & 127) / p.gqa;
+    tok[k] = (row >> 7) * p.tile_tokens + t;
+    valid[k] = t < p.tile_tokens && r.t0 + tok[k] < r.T;
+    any = any || valid[k];
+    m[k] = kNoMax;
+    l[k] = 0.f;
+    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (!any) return;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int n = min(32, parts - i0);
+    float w[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float2 y = lane < n && valid[k] ? p.part_ml[at(i0 + lane, k)] : make_float2(kNoMax, 0.f);
+      // (a part without a visible key has the sum 0, and its outputs are not looked at)
+      float to = y.y == 0.f ? kNoMax : y.x;
+#pragma unroll
+      for (int b = 16; b; b >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, b));
+      to = fmaxf(to, m[k]);
+      w[k] = y.y == 0.f ? 0.f : fast_exp2(y.x - to);
+      float s = w[k] * y.y;
+#pragma unroll
+      for (int b = 16; b; b >>= 1) s += __shfl_xor_sync(0xffffffffu, s, b);
+      const float f0 = fast_exp2(m[k] - to);
+      m[k] = to;
+      l[k] = l[k] * f0 + s;
+      o[k].x *= f0;
+      o[k].y *= f0;
+      o[k].z *= f0;
+      o[k].w *= f0;
+    }
+    constexpr int kAhead = 8 / R;
+    for (int i = 0; i < n; i += kAhead) {
+      float4 v[kAhead][R];
+      float wi[kAhead][R];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          wi[q][k] = __shfl_sync(0xffffffffu, w[k], min(i + q, 31));
+          if (i + q >= n) wi[q][k] = 0.f;
+          if (wi[q][k] != 0.f)
+            v[q][k] = *reinterpret_cast<const float4*>(p.part_o + at(i0 + i + q, k) * kHeadDim + 4 * lane);
+        }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+          if (wi[q][k] != 0.f) {
+            o[k].x += v[q][k].x * wi[q][k];
+            o[k].y += v[q][k].y * wi[q][k];
+            o[k].z += v[q][k].z * wi[q][k];
+            o[k].w += v[q][k].w * wi[q][k];
+          }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (!valid[k]) continue;
+    const float s = l[k] > 0.f ? 1.f / l[k] : l[k];
+    bf16* dst = p.out + ((size_t)(r.row0 + tok[k]) * p.hq + g * p.gqa + ((row0 + k) & 127) % p.gqa) * kHeadDim;
+    *reinterpret_cast<uint2*>(dst + 4 * lane) =
+        make_uint2(pack_bf16x2(o[k].x * s, o[k].y * s), pack_bf16x2(o[k].z * s, o[k].w * s));
+  }
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) at_join_kernel(AtParams p) {
   pdl_wait();
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5;
   const AtPlan pl = *p.plan;
-  if (!pl.split) return;
-  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AtFirst f = p.first[c];
-  if (f.rec < 0 || f.off == 0) return;
+  if (!pl.split || f.rec < 0 || f.off == 0) return;
   const long long a = (long long)c * pl.per - f.off;
   const int c0 = (int)(a / pl.per);
   if (c0 != c - 1) return;
   const AtRec r = p.rec[f.rec];
   const int parts = (int)((a + r.steps - 1) / pl.per) - c0 + 1;
-  const int row = blockIdx.y * kJoinRows + warp, tok = (row & 127) / p.gqa, t = (row >> 7) * p.tile_tokens + tok;
-  if (tok >= p.tile_tokens || r.t0 + t >= r.T) return;
-  auto at = [&](int i) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row; };
-  float m = kNoMax, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const int n = min(32, parts - i0);
-    const float2 y = lane < n ? p.part_ml[at(i0 + lane)] : make_float2(kNoMax, 0.f);
-    // (a part without a visible key has the sum 0, and its outputs are not looked at)
-    float to = y.y == 0.f ? kNoMax : y.x;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, k));
-    to = fmaxf(to, m);
-    const float w = y.y == 0.f ? 0.f : fast_exp2(y.x - to), f0 = fast_exp2(m - to);
-    float s = w * y.y;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    m = to;
-    l = l * f0 + s;
-    o.x *= f0;
-    o.y *= f0;
-    o.z *= f0;
-    o.w *= f0;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (wi == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at(i0 + i) * kHeadDim + 4 * lane);
-      o.x += v.x * wi;
-      o.y += v.y * wi;
-      o.z += v.z * wi;
-      o.w += v.w * wi;
-    }
-  }
-  const float s = l > 0.f ? 1.f / l : l;
-  bf16* dst = p.out + ((size_t)(r.row0 + t) * p.hq + f.head * p.gqa + (row & 127) - tok * p.gqa) * kHeadDim;
-  *reinterpret_cast<uint2*>(dst + 4 * lane) = make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
+  // few parts: many rows in all, and their latency counts; many: few rows, each with loads enough
+  if (parts > 4)
+    join_rows<1>(p, r, f.head, c0, parts, blockIdx.y * kJoinWarps + warp);
+  else if (blockIdx.y < 4)
+    join_rows<4>(p, r, f.head, c0, parts, (blockIdx.y * kJoinWarps + warp) * 4);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1117,15 +1281,18 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.status = a.status;
   p.wait_limit = a.wait_limit_ns ? WaitLimit{a.wait_limit_ns} : kWaitLimit;
   p.test_skip = a.test_skip;
-  cudaError_t e = launch_pdl_kernel(at_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+  p.few = z.room <= kFewPairs;
+  cudaError_t e = cudaSuccess;
+  if (!p.few) e = launch_pdl_kernel(at_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
   if (e != cudaSuccess) return e;
   if (p.mask)
     e = paged ? launch_at<true, true>(qm, km, vm, p, s) : launch_at<false, true>(qm, km, vm, p, s);
   else
     e = paged ? launch_at<true, false>(qm, km, vm, p, s) : launch_at<false, false>(qm, km, vm, p, s);
-  if (e != cudaSuccess || p.ctas < 2) return e;
-  return launch_pdl_kernel(at_join_kernel, dim3(p.ctas - 1, 256 / kJoinRows),
-                           dim3(32 * kJoinRows), 0, s, p);
+  // (items of so few steps are never cut)
+  if (e != cudaSuccess || p.ctas < 2 || (a.cap + kAtTile - 1) / kAtTile < kSplitGain) return e;
+  return launch_pdl_kernel(at_join_kernel, dim3(p.ctas - 1, 256 / kJoinWarps),
+                           dim3(32 * kJoinWarps), 0, s, p);
 }
 
 }  // namespace rkv

@@ -330,6 +330,7 @@ struct SlotArgs {
   int32_t* held_out;
   int32_t* free_count_out;
   int n, max_blocks, num_blocks, block, room;  // room: entries of slots and positions
+  int wide;                                    // slots and positions begin on 16 bytes
   void* scratch;
   uint32_t* status;
 };

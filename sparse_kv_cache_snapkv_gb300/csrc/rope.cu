@@ -19,8 +19,9 @@
 namespace rkv {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 4;  // heads whose loads a thread has under way
 
-__device__ __forceinline__ void rotate(const uint4& a, const uint4& b, const float* cs, const float* sn,
+__device__ __forceinline__ void rotate(uint4 a, uint4 b, const float* cs, const float* sn,
                                        bool interleaved, uint4* oa, uint4* ob) {
   float x[16], y[16];
   unpack8(a, x);
@@ -90,25 +91,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, i
     }
     const long long blk = slot / a.block, in_blk = slot - blk * a.block;
     const int end = min(heads, (part + 1) * per);
-#pragma unroll 4
-    for (int h = part * per + (lane >> 3); h < end; h += 4) {
-      const bf16* src;
-      bf16* dst;
-      if (h < a.hq) {
-        src = a.q + token * a.q_stride + h * kHeadDim;
-        dst = a.q_out + ((size_t)token * a.hq + h) * kHeadDim;
-      } else {
-        const int g = h - a.hq < a.n_kv ? h - a.hq : h - a.hq - a.n_kv;
-        const bool key = h < a.hq + a.n_kv;
-        src = (key ? a.k + token * a.k_stride : a.v + token * a.v_stride) + g * kHeadDim;
-        dst = (key ? a.k_cache : a.v_cache) + ((size_t)(blk * a.n_kv + g) * a.block + in_blk) * kHeadDim;
+    // the loads of several heads first: a store might be to where a later load is from, for all the compiler
+    // knows (36856 tokens of 48 heads: 153 us with one head at a time)
+    for (int h0 = part * per + (lane >> 3); h0 < end; h0 += 4 * kRopeAhead) {
+      uint4 x[kRopeAhead], y[kRopeAhead];
+      bf16* dst[kRopeAhead];
+#pragma unroll
+      for (int i = 0; i < kRopeAhead; ++i) {
+        const int h = h0 + 4 * i;
+        const bf16* src;
+        if (h < a.hq) {
+          src = a.q + token * a.q_stride + h * kHeadDim;
+          dst[i] = a.q_out + ((size_t)token * a.hq + h) * kHeadDim;
+        } else {
+          const bool key = h < a.hq + a.n_kv;
+          const int g = key ? h - a.hq : h - a.hq - a.n_kv;
+          src = (key ? a.k + token * a.k_stride : a.v + token * a.v_stride) + g * kHeadDim;
+          dst[i] = (key ? a.k_cache : a.v_cache) + ((size_t)(blk * a.n_kv + g) * a.block + in_blk) * kHeadDim;
+        }
+        if (h < end) {
+          x[i] = *reinterpret_cast<const uint4*>(src + at0);
+          y[i] = *reinterpret_cast<const uint4*>(src + at1);
+        }
       }
-      const uint4 x = *reinterpret_cast<const uint4*>(src + at0);
-      const uint4 y = *reinterpret_cast<const uint4*>(src + at1);
-      uint4 ox = x, oy = y;
-      if (turned && h < a.hq + a.n_kv) rotate(x, y, cs, sn, a.interleaved, &ox, &oy);
-      *reinterpret_cast<uint4*>(dst + at0) = ox;
-      *reinterpret_cast<uint4*>(dst + at1) = oy;
+#pragma unroll
+      for (int i = 0; i < kRopeAhead; ++i) {
+        const int h = h0 + 4 * i;
+        if (h >= end) break;
+        if (turned && h < a.hq + a.n_kv) rotate(x[i], y[i], cs, sn, a.interleaved, &x[i], &y[i]);
+        *reinterpret_cast<uint4*>(dst[i] + at0) = x[i];
+        *reinterpret_cast<uint4*>(dst[i] + at1) = y[i];
+      }
     }
   }
 }

@@ -34,38 +34,58 @@ __device__ __forceinline__ int ceil_blocks(long long tokens, int block) {
   return (int)((tokens + block - 1) / block);
 }
 
-// Places of tokens t = first, first + step, ...
+// Places of Q tokens each, t = Q first, Q (first + step), ... Neighbours mostly share the unit and the block,
+// which are looked up again only where they change. (One token each where there are few: 256 requests of one
+// token 4.1 us, with four each 7.1; 1.08M tokens of 64 requests 11.3 us with one, 8.4 with four.)
+template <int Q>
 __device__ __forceinline__ void place_tokens(const SlotArgs& a, const SlotUnit* unit, int all, int count,
                                              long long first, long long step) {
-  for (long long t = first; t < a.room; t += step) {
-    int slot = -1, pos = 0;
-    if (t < all) {
-      int lo = 0, hi = a.n;  // the last unit that begins at or before t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (unit[mid].start <= t) lo = mid; else hi = mid;
+  for (long long t0 = Q * first; t0 < a.room; t0 += Q * step) {
+    int slot[Q], pos[Q];
+    SlotUnit u{};
+    int at = -1, end = -1;  // the unit, and the first token behind it
+    int held = -1, b = -1;  // the block's number in the table, and the block
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const long long t = t0 + i;
+      slot[i] = -1;
+      pos[i] = 0;
+      if (t >= all || t >= a.room) continue;
+      if (t >= end) {
+        int lo = at < 0 ? 0 : at, hi = a.n;  // the last unit that begins at or before t
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (unit[mid].start <= t) lo = mid; else hi = mid;
+        }
+        at = lo;
+        u = unit[lo];
+        end = unit[lo + 1].start;
+        held = -1;
       }
-      const SlotUnit u = unit[lo];
-      if (u.before >= 0) {
-        pos = u.len + (int)(t - u.start);
-        const int j = pos / a.block, off = pos - j * a.block;
-        int b;
-        if (j < u.held) {
-          b = a.table[(size_t)lo * a.max_blocks + j];
-        } else {
-          b = a.free_blocks[count - 1 - u.before - (j - u.held)];
-          if (off == 0) a.table[(size_t)lo * a.max_blocks + j] = b;
-        }
-        if (b >= 0 && b < a.num_blocks) {
-          slot = b * a.block + off;
-        } else {
-          set_status(a.status, RKV_DEV_BAD_INDEX);
-          pos = 0;
-        }
+      if (u.before < 0) continue;
+      const int p = u.len + (int)(t - u.start), j = p / a.block, off = p - j * a.block;
+      if (j != held) {
+        held = j;
+        b = j < u.held ? a.table[(size_t)at * a.max_blocks + j] : a.free_blocks[count - 1 - u.before - (j - u.held)];
+        if (b < 0 || b >= a.num_blocks) set_status(a.status, RKV_DEV_BAD_INDEX);
+      }
+      if (j >= u.held && off == 0) a.table[(size_t)at * a.max_blocks + j] = b;
+      if (b >= 0 && b < a.num_blocks) {
+        slot[i] = b * a.block + off;
+        pos[i] = p;
       }
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+    if (Q == 4 && t0 + Q <= a.room && a.wide) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1 % Q], slot[2 % Q], slot[3 % Q]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1 % Q], pos[2 % Q], pos[3 % Q]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < Q; ++i)
+        if (t0 + i < a.room) {
+          a.slots[t0 + i] = slot[i];
+          a.positions[t0 + i] = pos[i];
+        }
+    }
   }
 }
 
@@ -136,14 +156,14 @@ __global__ void __launch_bounds__(kSlotThreads) reserve_kernel(SlotArgs a, SlotU
   }
   if (a.room > kSlotFew) return;
   __syncthreads();
-  place_tokens(a, unit, all, count, tid, kSlotThreads);
+  place_tokens<1>(a, unit, all, count, tid, kSlotThreads);
 }
 
 __global__ void __launch_bounds__(256) place_kernel(SlotArgs a, const SlotUnit* unit) {
   pdl_wait();
   pdl_trigger();
   const SlotUnit end = unit[a.n];
-  place_tokens(a, unit, end.start, end.len, (long long)blockIdx.x * 256 + threadIdx.x,
+  place_tokens<4>(a, unit, end.start, end.len, (long long)blockIdx.x * 256 + threadIdx.x,
                (long long)gridDim.x * 256);
 }
 
@@ -209,7 +229,7 @@ cudaError_t launch_reserve_slots(const SlotArgs& a, cudaStream_t s) {
   SlotUnit* unit = static_cast<SlotUnit*>(a.scratch);
   const cudaError_t e = launch_pdl_kernel(reserve_kernel, dim3(1), dim3(kSlotThreads), 0, s, a, unit);
   if (e != cudaSuccess || a.room <= kSlotFew) return e;
-  const int most = device_sm_count() * 8, ctas = (a.room - 1) / 256 + 1;
+  const int most = device_sm_count() * 8, ctas = (a.room - 1) / 1024 + 1;
   return launch_pdl_kernel(place_kernel, dim3(ctas < most ? ctas : most), dim3(256), 0, s, a,
                            (const SlotUnit*)unit);
 }
