@@ -817,9 +817,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at.step();
         if (act && j == 0) wait(&bar.qfull[h], nq++);
         wait(&bar.full[kr.place], kr.phase);
-        if (pend) ready();
         if (h == 1 || nturn > 0) wait(&bar.turn[h], h == 1 ? nturn : nturn - 1);
         ++nturn;
+        if (pend) ready();
         tc_fence_after();
         if (!aborted && elect_one()) {
           if (pend) product(!act);
