@@ -516,10 +516,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Which keys a row sees: all below `clear` (the same for every row of a warp); of the others those up to
-// `lim`, or in a tree those whose bit is set, T of them from `base` on (T = 0: not a row).
+// Which keys a row sees: all below `clear` and none from `end` on (the same for every row of a warp); of the
+// others those up to `lim`, or in a tree those whose bit is set, T of them from `base` on (T = 0: not a row).
 struct AtSees {
-  int clear, lim, base, T;
+  int clear, end, lim, base, T;
   const uint32_t* bits;
 };
 
@@ -551,30 +551,39 @@ __device__ __forceinline__ void at_hide(uint32_t (&s)[32], int k, const AtSees& 
 // What most steps do not need, in functions of their own, so that the steps' code has neither its branches
 // nor its registers (with branches for the masks between the chunks: 8K prompt 440 us).
 //
-// A step with keys that some row does not see, or an item's first: sets those to -infinity where S lies, and
-// returns the maximum of m and all scores.
+// A step with keys that some row does not see: sets those to -infinity where S lies.
 template <bool TREE>
-__device__ __noinline__ float at_prepare(uint32_t sp, int k0, AtSees sees, float scale, float m) {
-  uint32_t s[4][32];
+__device__ __noinline__ void at_mask(uint32_t sp, int k0, AtSees sees) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int k = k0 + 32 * c;
+    if (k + 32 <= sees.clear) continue;
+    uint32_t s[32];
+    if (k < sees.end) {
+      tmem_ld32(sp + 32 * c, s);
+      at_hide<TREE>(s, k, sees);
+    } else {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32_start(sp + 32 * c, s[c]);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
-  if (k0 + kAtTile > sees.clear) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (k0 + 32 * c + 32 > sees.clear) {
-        at_hide<TREE>(s[c], k0 + 32 * c, sees);
-        tmem_st32(sp + 32 * c, s[c]);
-      }
+      for (int i = 0; i < 32; ++i) s[i] = 0xff800000u;
+    }
+    tmem_st32(sp + 32 * c, s);
   }
-  float y[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
-#pragma unroll
-  for (int i = 0; i < 32; i += 2)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = max3(y[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
   tmem_st_wait();
-  return fmaxf(m, fmaxf(max3(y[0], y[1], y[2]), y[3]) * scale);
+}
+
+// The maximum of m and the first n scores (32 or 128).
+__device__ __noinline__ float at_most(uint32_t sp, int n, float scale, float m) {
+#pragma unroll 1
+  for (int c = 0; c < n; c += 32) {
+    uint32_t s[32];
+    tmem_ld32(sp + c, s);
+    float y[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      y[(i >> 1) & 3] = max3(y[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    m = fmaxf(m, fmaxf(max3(y[0], y[1], y[2]), y[3]) * scale);
+  }
+  return m;
 }
 
 // Scales O by f. (The product before this step's S is done: S was issued behind it.)
@@ -991,7 +1000,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int clear = TREE ? base : __reduce_min_sync(0xffffffffu, valid ? lim : 0x7ffffffe) + 1;
       const uint32_t* bits = TREE ? p.mask + (size_t)(x.row0 + h * p.tile_tokens + tok) * p.words : nullptr;
       float m = kNoMax, l = 0.f;
-      const AtSees sees{clear, lim, base, valid ? x.T : 0, bits};
+      const int end = TREE ? x.L : __reduce_max_sync(0xffffffffu, lim) + 1;
+      const AtSees sees{clear, end, lim, base, valid ? x.T : 0, bits};
       for (int j = 0; j < x.cnt[h]; ++j) {
         if (!mbar_wait_warp(&bar.sfull[h], ns++ & 1u, limit)) {
           aborted = true;
@@ -1012,14 +1022,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         tc_fence_after();
         const int k0 = (x.s0 + j) * kAtTile;
-        if (j == 0 || k0 + kAtTile > clear) {
-          const float to = at_prepare<TREE>(sp, k0, sees, p.scale_log2, m);
-          if (j == 0) m = to;
-        }
+        if (k0 + kAtTile > clear) at_mask<TREE>(sp, k0, sees);
+        if (j == 0) m = at_most(sp, 32, p.scale_log2, m);  // (near enough: what passes it by far raises it)
         uint32_t out[2][32];
         float sum;
 #pragma unroll 1
-        for (bool again = j == 0;; again = true) {
+        for (bool again = false;; again = true) {
           // numerators relative to m, which most often holds: no maximum is looked for. A chunk's load runs
           // under the one before it.
           const uint64_t off = pack2(-m, -m);
@@ -1042,8 +1050,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           const float2 z = unpack2(add2(acc[0], acc[1]));
           sum = z.x + z.y;
           if (again || !__any_sync(0xffffffffu, valid && !(sum < kLargest))) break;
-          const float to = at_prepare<TREE>(sp, k0, sees, p.scale_log2, m), f = fast_exp2(m - to);
-          at_scale(od, f);
+          const float to = at_most(sp, kAtTile, p.scale_log2, m), f = fast_exp2(m - to);
+          if (j > 0) at_scale(od, f);
           l *= f;
           m = to;
         }
