@@ -124,7 +124,7 @@ __device__ __forceinline__ bool at_unit(const AtParams& p, int u, int* row0, int
 
 // Whole items, unless the longest would outlast an equal share of all steps by what parts and their join cost.
 __device__ __forceinline__ AtPlan at_decide(long long total, int longest, int count, int ctas) {
-  const long long each = (total + ctas - 1) / ctas;
+  const long long each = total < (1ll << 30) ? ((int)total + ctas - 1) / ctas : (total + ctas - 1) / ctas;
   const int split = total < (1ll << 30) && longest - each >= kSplitGain && longest * 4ll > each * 5ll;
   return AtPlan{split, count, (int)max((long long)kSplitLeast, min(each, 1ll << 30)), (int)min(total, 1ll << 30)};
 }
@@ -299,6 +299,8 @@ struct Pieces {
     for (int i = 0; i < 2; ++i) {
       const int u = 32 * i + lane;
       row0[i] = T[i] = L[i] = 0;
+      first[i] = 0x7fffffff;
+      if (32 * i >= p.n) continue;
       if (u < p.n) at_unit(p, u, &row0[i], &T[i], &L[i]);
       const int tiles = (T[i] + pair - 1) / pair, incl = warp_incl_scan(tiles);
       first[i] = u < p.n ? n + incl - tiles : 0x7fffffff;  // the unit's first pair
@@ -311,9 +313,11 @@ struct Pieces {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = 32 * i + lane;
+      mine[i] = AtRec{};
+      if (32 * i >= n) continue;
       int u = 0;  // the last unit whose pairs begin at or before e
-#pragma unroll
-      for (int step = 32; step; step >>= 1) {
+#pragma unroll 1
+      for (int step = p.n > 32 ? 32 : 16; step && p.n > 1; step >>= 1) {
         const int at = u + step, a = __shfl_sync(0xffffffffu, first[0], at & 31), b = __shfl_sync(0xffffffffu, first[1], at & 31);
         if ((at >= 32 ? b : a) <= e) u = at;
       }

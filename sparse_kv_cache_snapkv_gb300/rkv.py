@@ -837,25 +837,21 @@ def rkv_evict_kv4(k_codes, k_scales, v_codes, v_scales, length, weights, pos, se
 
 
 # ------------------------------------------------------------------------------- a serving step
-def _tokens(t, name, heads, dev, tokens=None):
+def _tokens(t, name, heads, dev, tokens):
     """Address and token stride (elements) of packed rows [tokens][heads][128] bf16: contiguous, or a
     slice of rows that hold more (the strides of tokens free, a token's heads side by side)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 3 and t.get_device() == dev
-            and t.shape[1] == heads and t.shape[2] == HEAD_DIM and tokens in (None, t.shape[0])
-            and t.stride(2) == 1 and (heads == 1 or t.stride(1) == HEAD_DIM)):
-        if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 3 and t.get_device() == dev:
-            if t.shape[1] == heads and t.shape[2] == HEAD_DIM and tokens in (None, t.shape[0]):
-                raise ValueError(f"{name}: the heads of a token must lie side by side")
-        _refuse(t, name, _BF16, (t.shape[0] if tokens is None and _rank(t) else tokens, heads, HEAD_DIM), dev)
-    stride = t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
-    p = t.data_ptr()
-    if p % 16 or stride % 8 or stride < heads * HEAD_DIM:
-        raise ValueError(f"{name}: tokens must begin on 16 bytes and not overlap")
-    return p, stride
-
-
-def _rank(t):
-    return isinstance(t, torch.Tensor) and t.dim() > 0
+    if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == (tokens, heads, HEAD_DIM)
+            and t.get_device() == dev):
+        stride, head, one = t.stride()
+        if one == 1 and (head == HEAD_DIM or heads == 1):
+            if tokens <= 1:
+                stride = heads * HEAD_DIM
+            p = t.data_ptr()
+            if p % 16 or stride % 8 or stride < heads * HEAD_DIM:
+                raise ValueError(f"{name}: tokens must begin on 16 bytes and not overlap")
+            return p, stride
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    _refuse(t, name, _BF16, (tokens, heads, HEAD_DIM), dev)
 
 
 def rkv_reserve_slots_workspace_bytes(n: int) -> int:
@@ -932,7 +928,7 @@ def rkv_rope_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache
     num_blocks, n_kv, block, d = shape = _dims(k_cache, "k_cache", 4)
     dev = q.get_device()
     rot = 2 * _dims(inv_freq, "inv_freq", 1)[0]
-    args = (*_tokens(q, "q", hq, dev), *_tokens(k, "k", n_kv, dev, tokens),
+    args = (*_tokens(q, "q", hq, dev, tokens), *_tokens(k, "k", n_kv, dev, tokens),
             *_tokens(v, "v", n_kv, dev, tokens),
             _at(positions, "positions", _I32, (tokens,), dev),
             _at(inv_freq, "inv_freq", _F32, (rot // 2,), dev),
@@ -964,7 +960,7 @@ def _attention(fn, q, q_start, mask, k, v, table, length, scale, out, ws, stream
         max_blocks = _dims(table, "block_table", 2)[1]
         paged = (_at(table, "block_table", _I32, (n, max_blocks), dev),)
         sizes = (tokens, lead, rows, max_blocks)
-    args = (*_tokens(q, "q", hq, dev), _at(q_start, "q_start", _I32, (n + 1,), dev), *tree,
+    args = (*_tokens(q, "q", hq, dev, tokens), _at(q_start, "q_start", _I32, (n + 1,), dev), *tree,
             _at(k, "k", _BF16, shape, dev), _at(v, "v", _BF16, shape, dev), *paged,
             _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d, *sizes, scale,
             _at(out, "out", _BF16, (tokens, hq, HEAD_DIM), dev), *hook)
