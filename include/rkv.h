@@ -638,10 +638,11 @@ rkv_status rkv_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   q_start  [n+1] int32 (device), ascending, within [0, tokens]
  *   k, v     [n][n_kv][max_len][128] bf16, or pools with a block table as for the paged calls above
  *            (block a power of two). Rows from len[u] on may hold anything; rows before that have
- *            finite values (an infinite or NaN value of v makes NaN of outputs that do not see it).
+ *            finite values, v below 2^80 in magnitude (sums of v come before the division by the
+ *            softmax's sum; an infinite or NaN value of v makes NaN of outputs that do not see it).
  *   len      [n] int32 (device), T <= len[u] <= max_len (paged: max_blocks * block)
- *   out      [tokens][n_kv*gqa][128] bf16, contiguous; may not be q. Rows of tokens that belong to
- *            no unit are left as they were.
+ *   out      [tokens][n_kv*gqa][128] bf16, contiguous; may not overlap q. Rows of tokens that belong
+ *            to no unit are left as they were.
  *   gqa      1 .. 64
  * len out of range: RKV_DEV_LEN_OVER_CAP; q_start out of order or range, or T > len[u]:
  * RKV_DEV_BAD_WINDOW; the unit is skipped, its rows left as they were. A table entry outside the pool

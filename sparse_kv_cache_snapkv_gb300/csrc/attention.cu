@@ -2,22 +2,30 @@
 // prompt or a chunk of one (causal), or a tree of drafted tokens (a bit mask among the newest rows).
 //
 //   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = 2^(scale log2(e) q_r . k_j - m_r),
-// over the keys j that query row r sees. m_r is a reference, not the maximum: it is the first keys'
-// maximum, and moves up only when a later one passes it by kRaise (in log2); sums and outputs are then
-// scaled once. p stays below 2^kRaise of its reference, so bf16 and fp32 hold it and its sums as well.
+// over the keys j that query row r sees. m_r is a reference, not the maximum: it is the maximum of an item's
+// first 32 keys, and moves up where the p of a step come to more than kLargest; sums and outputs are then scaled
+// once. So most steps look for no maximum, and bf16 and fp32 hold p, its sums and the outputs all the same.
 //
 // Rows are (token, query head of the KV group), heads fastest: a tile of 128 rows holds 128 / gqa tokens
 // of one (unit, KV head), and an item is two tiles that read each key and value once. The cache streams
-// by in steps of 128 rows: S = Q K^T and O += P V on tcgen05, one tile of the pair after the other, so
-// that one tile's softmax runs under the other's products. A softmax thread owns one row: no value
-// crosses lanes. P goes back to TMEM, over the S it comes from, as the bf16 operand of P V: each p is
-// rounded once, by 2^-9 of its value on average less, where a second bf16 part would cost half as many
-// tensor operations again; the outputs are bf16 numbers with a rounding of the same size.
+// by in steps of 128 rows: S = Q K^T and O += P V on tcgen05 (operands by TMA, S, P and O in TMEM), the two tiles
+// in turns, so that one's softmax runs under the other's products. A softmax thread owns one row: no value
+// crosses lanes. P goes back to TMEM, over the S it comes from, as the bf16 operand of P V: each p is rounded
+// once, by at most 2^-8 of its value, where a second bf16 part would cost half as many tensor operations again;
+// the outputs are bf16 numbers with a rounding of the same size.
 //
-// Bound: a prompt by the tensor cores (four times 128 flops a (row, key) pair), a tree by reading the
-// cache. Items of a prompt go to CTAs as they are, largest first in waves of alternating direction;
-// where the longest item would outlast an equal share of all steps, every CTA takes an equal range of
-// the steps instead, and a second kernel joins the parts of cut items in their order.
+// Sixteen warps: loads, the two tiles' products, pieces of work (one warp each of the first two and the last,
+// as warps 0 to 3), four write outputs, four each are a tile's softmax. Between them only mbarriers, all waits
+// bounded.
+//
+// Bound: a prompt by the tensor cores (8192 tokens, 32 heads of 8 KV heads: 318 us, 1.73 PFLOP/s of the
+// causal half, 90 % of a cuBLAS product's rate; the GPU is at its power limit); a tree by reading the cache (32
+// trees over up to 20480 rows: 268 us, 6.4 TB/s) or, with 256 rows an item, by both. A step of a pair takes some
+// 2600 clocks, 2048 of them products; what is left is the chain from S through the softmax to P and the wakes
+// between. Items of a prompt go to CTAs as they are, largest first in waves of alternating direction; where
+// the longest item would outlast an equal share of all steps, every CTA takes an equal range of the steps
+// instead, and a second kernel joins the parts of cut items in their order (131071 rows, 64 drafted tokens:
+// 116 us, 80 of them the floor).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -42,10 +50,12 @@ constexpr uint32_t kAtCols = 512;                     // S or P of both tiles, O
 constexpr int kPlanThreads = 1024;
 constexpr int kFewPairs = 64;    // pairs of tiles whose plan a warp makes in its registers
 constexpr int kPlanBuckets = 1024;
-constexpr float kLargest = 1048576.f;  // 2^20
+constexpr float kLargest = 1048576.f;  // 2^20: what the p of a row's step may come to before m is raised
 constexpr float kNoMax = -1e30f;
 constexpr int kSplitLeast = 2;   // steps of a CTA's range
-constexpr int kSplitGain = 12;    // steps that ranges must save over whole items: what parts and their join cost
+// Steps that ranges must save over whole items, which is what parts and their join cost (8 steps each of 8
+// items: whole 15.5 us, cut into 2 steps each 18.6; 12 steps of 16: 24.2 and 29.0; 16 of 32: 26.1 both ways).
+constexpr int kSplitGain = 12;
 
 struct AtSmem {
   static constexpr size_t q_off = 0;
@@ -98,6 +108,7 @@ struct AtParams {
   float* part_o;      // [2 ctas][256][128]
   uint32_t* status;
   WaitLimit wait_limit;
+  WaitLimit item_limit;  // of waits that may take as long as an item
   int test_skip;
 };
 
@@ -669,7 +680,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const uint32_t tmem = bar.tmem;
   pdl_wait();
   pdl_trigger();
-  const WaitLimit limit = p.wait_limit;
+  const WaitLimit limit = p.wait_limit, item_limit = p.item_limit;
   bool aborted = false;
   Piece* pieces = reinterpret_cast<Piece*>(smem + AtSmem::piece_off);
   float* sums = reinterpret_cast<float*>(smem + AtSmem::sum_off);
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint32_t npiece = 0;
   auto next = [&]() {  // the next piece, for a warp other than the one that finds them
     const uint32_t i = npiece % kAtPieces;
-    if (!mbar_wait_warp(&bar.pfilled[i], (npiece / kAtPieces) & 1u, limit)) {
+    if (!mbar_wait_warp(&bar.pfilled[i], (npiece / kAtPieces) & 1u, item_limit)) {
       aborted = true;
       return false;
     }
@@ -877,7 +888,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     it.init(p);
     auto find = [&](uint32_t k) {  // piece k; false: there is none
       const uint32_t i = k % kAtPieces;
-      if (k >= kAtPieces && !mbar_wait_warp(&bar.pread[i], (k / kAtPieces - 1) & 1u, limit)) {
+      if (k >= kAtPieces && !mbar_wait_warp(&bar.pread[i], (k / kAtPieces - 1) & 1u, item_limit)) {
         aborted = true;
         return false;
       }
@@ -910,7 +921,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int at = x.L / kAtTile - x.s0, cut = x.L % kAtTile;  // the step that the sequence ends in
       if (cut && at >= 0 && at < x.steps) {
         const int load = 2 * (steps + at) + 1, s = load % kAtStages;
-        if (!mbar_wait_warp(&bar.dirty, (uint32_t)(ntail++ & 1), limit) ||
+        if (!mbar_wait_warp(&bar.dirty, (uint32_t)(ntail++ & 1), item_limit) ||
             !mbar_wait_warp(&bar.full[s], (uint32_t)((load / kAtStages) & 1), limit)) {
           aborted = true;
           break;
@@ -940,7 +951,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int t = x.t0 + h * p.tile_tokens + tok;  // this row's token
         const bool valid = tok < p.tile_tokens && t < x.T;
         const uint32_t turn = no[h] & 1;
-        if (!mbar_wait_warp(&bar.ofull[h], turn, limit) ||
+        if (!mbar_wait_warp(&bar.ofull[h], turn, item_limit) ||
             !mbar_wait_warp(&bar.lfull[h][turn], (no[h] >> 1) & 1u, limit)) {
           aborted = true;
           continue;
@@ -1092,105 +1103,74 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
 }
 
-// Joins the parts of the items that ranges cut: the item in which CTA x + 1's range begins, unless it was
-// cut before already (grid: ranges' borders x groups of rows; a warp per row, four columns a lane). A lane
-// holds a part's weight, so that the parts' loads do not wait for one another.
-constexpr int kJoinWarps = 16;
+// Joins the parts of the items that ranges cut. Work: the borders of the ranges x groups of rows; of a cut item,
+// the first border in it does all (a warp per row, four columns a lane). A lane holds a part's weight, so that
+// the parts' loads do not wait for one another. What this waits for is a chain of three loads a row, so warps
+// count: 64 an SM (chunks of 3 prompts 189 us; 32 with four rows each 203). Blocks go over the work themselves:
+// with one for each group, a call that cuts nothing waited 9 us for them to end.
+constexpr int kJoinWarps = 16, kJoinPerSm = 4, kJoinAhead = 2;
 
-// R rows of an item by a warp, their loads under way together.
-template <int R>
-__device__ __forceinline__ void join_rows(const AtParams& p, const AtRec& r, int g, int c0, int parts, int row0) {
-  const int lane = threadIdx.x & 31;
-  auto at = [&](int i, int k) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row0 + k; };
-  bool valid[R], any = false;
-  int tok[R];
-  float m[R], l[R];
-  float4 o[R];
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    const int row = row0 + k, t = (row & 127) / p.gqa;
-    tok[k] = (row >> 7) * p.tile_tokens + t;
-    valid[k] = t < p.tile_tokens && r.t0 + tok[k] < r.T;
-    any = any || valid[k];
-    m[k] = kNoMax;
-    l[k] = 0.f;
-    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  if (!any) return;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const int n = min(32, parts - i0);
-    float w[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const float2 y = lane < n && valid[k] ? p.part_ml[at(i0 + lane, k)] : make_float2(kNoMax, 0.f);
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinPerSm) at_join_kernel(AtParams p) {
+  pdl_wait();
+  const AtPlan pl = *p.plan;
+  if (!pl.split) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, borders = p.ctas - 1;
+  for (int work = blockIdx.x; work < borders * (256 / kJoinWarps); work += gridDim.x) {
+    const int y = work / borders, c = work - y * borders + 1;
+    const AtFirst f = p.first[c];
+    if (f.rec < 0 || f.off == 0) continue;
+    const long long a = (long long)c * pl.per - f.off;
+    const int c0 = (int)(a / pl.per);
+    if (c0 != c - 1) continue;
+    const AtRec r = p.rec[f.rec];
+    const int parts = (int)((a + r.steps - 1) / pl.per) - c0 + 1;
+    const int row = y * kJoinWarps + warp, t = (row & 127) / p.gqa, tok = (row >> 7) * p.tile_tokens + t;
+    if (t >= p.tile_tokens || r.t0 + tok >= r.T) continue;
+    auto at = [&](int i) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row; };
+    float m = kNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const int n = min(32, parts - i0);
+      const float2 x = lane < n ? p.part_ml[at(i0 + lane)] : make_float2(kNoMax, 0.f);
       // (a part without a visible key has the sum 0, and its outputs are not looked at)
-      float to = y.y == 0.f ? kNoMax : y.x;
+      float to = x.y == 0.f ? kNoMax : x.x;
 #pragma unroll
       for (int b = 16; b; b >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, b));
-      to = fmaxf(to, m[k]);
-      w[k] = y.y == 0.f ? 0.f : fast_exp2(y.x - to);
-      float s = w[k] * y.y;
+      to = fmaxf(to, m);
+      const float w = x.y == 0.f ? 0.f : fast_exp2(x.x - to), f0 = fast_exp2(m - to);
+      float s = w * x.y;
 #pragma unroll
       for (int b = 16; b; b >>= 1) s += __shfl_xor_sync(0xffffffffu, s, b);
-      const float f0 = fast_exp2(m[k] - to);
-      m[k] = to;
-      l[k] = l[k] * f0 + s;
-      o[k].x *= f0;
-      o[k].y *= f0;
-      o[k].z *= f0;
-      o[k].w *= f0;
-    }
-    constexpr int kAhead = 8 / R;
-    for (int i = 0; i < n; i += kAhead) {
-      float4 v[kAhead][R];
-      float wi[kAhead][R];
+      m = to;
+      l = l * f0 + s;
+      o.x *= f0;
+      o.y *= f0;
+      o.z *= f0;
+      o.w *= f0;
+      for (int i = 0; i < n; i += kJoinAhead) {
+        float4 v[kJoinAhead];
+        float wi[kJoinAhead];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-          wi[q][k] = __shfl_sync(0xffffffffu, w[k], min(i + q, 31));
-          if (i + q >= n) wi[q][k] = 0.f;
-          if (wi[q][k] != 0.f)
-            v[q][k] = *reinterpret_cast<const float4*>(p.part_o + at(i0 + i + q, k) * kHeadDim + 4 * lane);
+        for (int q = 0; q < kJoinAhead; ++q) {
+          wi[q] = __shfl_sync(0xffffffffu, w, min(i + q, 31));
+          if (i + q >= n) wi[q] = 0.f;
+          if (wi[q] != 0.f) v[q] = *reinterpret_cast<const float4*>(p.part_o + at(i0 + i + q) * kHeadDim + 4 * lane);
         }
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-        for (int k = 0; k < R; ++k)
-          if (wi[q][k] != 0.f) {
-            o[k].x += v[q][k].x * wi[q][k];
-            o[k].y += v[q][k].y * wi[q][k];
-            o[k].z += v[q][k].z * wi[q][k];
-            o[k].w += v[q][k].w * wi[q][k];
-          }
+        for (int q = 0; q < kJoinAhead; ++q) {
+          if (wi[q] == 0.f) continue;
+          o.x += v[q].x * wi[q];
+          o.y += v[q].y * wi[q];
+          o.z += v[q].z * wi[q];
+          o.w += v[q].w * wi[q];
+        }
+      }
     }
-  }
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    if (!valid[k]) continue;
-    const float s = l[k] > 0.f ? 1.f / l[k] : l[k];
-    bf16* dst = p.out + ((size_t)(r.row0 + tok[k]) * p.hq + g * p.gqa + ((row0 + k) & 127) % p.gqa) * kHeadDim;
+    const float s = l > 0.f ? 1.f / l : l;
+    bf16* dst = p.out + ((size_t)(r.row0 + tok) * p.hq + f.head * p.gqa + (row & 127) - t * p.gqa) * kHeadDim;
     *reinterpret_cast<uint2*>(dst + 4 * lane) =
-        make_uint2(pack_bf16x2(o[k].x * s, o[k].y * s), pack_bf16x2(o[k].z * s, o[k].w * s));
+        make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
   }
-}
-
-__global__ void __launch_bounds__(32 * kJoinWarps) at_join_kernel(AtParams p) {
-  pdl_wait();
-  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5;
-  const AtPlan pl = *p.plan;
-  const AtFirst f = p.first[c];
-  if (!pl.split || f.rec < 0 || f.off == 0) return;
-  const long long a = (long long)c * pl.per - f.off;
-  const int c0 = (int)(a / pl.per);
-  if (c0 != c - 1) return;
-  const AtRec r = p.rec[f.rec];
-  const int parts = (int)((a + r.steps - 1) / pl.per) - c0 + 1;
-  // few parts: many rows in all, and their latency counts; many: few rows, each with loads enough
-  if (parts > 4)
-    join_rows<1>(p, r, f.head, c0, parts, blockIdx.y * kJoinWarps + warp);
-  else if (blockIdx.y < 4)
-    join_rows<4>(p, r, f.head, c0, parts, (blockIdx.y * kJoinWarps + warp) * 4);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1292,6 +1272,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.part_o = reinterpret_cast<float*>(w);
   p.status = a.status;
   p.wait_limit = a.wait_limit_ns ? WaitLimit{a.wait_limit_ns} : kWaitLimit;
+  // (a step takes some 2 us)
+  p.item_limit = WaitLimit{p.wait_limit.ns + 20000ull * (uint64_t)((a.cap + kAtTile - 1) / kAtTile)};
   p.test_skip = a.test_skip;
   p.few = z.room <= kFewPairs;
   cudaError_t e = cudaSuccess;
@@ -1303,8 +1285,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     e = paged ? launch_at<true, false>(qm, km, vm, p, s) : launch_at<false, false>(qm, km, vm, p, s);
   // (items of so few steps are never cut)
   if (e != cudaSuccess || p.ctas < 2 || (a.cap + kAtTile - 1) / kAtTile < kSplitGain) return e;
-  return launch_pdl_kernel(at_join_kernel, dim3(p.ctas - 1, 256 / kJoinWarps),
-                           dim3(32 * kJoinWarps), 0, s, p);
+  return launch_pdl_kernel(at_join_kernel, dim3(p.ctas * kJoinPerSm), dim3(32 * kJoinWarps), 0, s, p);
 }
 
 }  // namespace rkv
