@@ -554,7 +554,8 @@ rkv_status rkv_evict_kv4(void* k_codes, void* k_scales, void* v_codes, void* v_s
  *   new_len, len, held [n] int32: held[u] blocks of block_table [n][max_blocks] are the unit's
  *            already, ceil(len / block) at least (blocks kept after a sequence was cut are used
  *            first); entries from held[u] on are not read
- *   block    tokens of a block, >= 1; num_blocks * block and max_blocks * block at most 2^30
+ *   block    tokens of a block; n, block, num_blocks, max_blocks, max_tokens >= 1; num_blocks * block,
+ *            max_blocks * block and max_tokens at most 2^30
  *   block_table  entries held[u] .. of a unit that needs more blocks are written: they come off the
  *            top of the stack in the order of the units. free_blocks itself is only read.
  *   q_start  [n+1] int32: prefix sums of new_len (a negative one counts as 0)

@@ -22,7 +22,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeAhead = 4;  // heads whose loads a thread has under way
 // Blocks an SM, which its registers hold: each goes on to further tokens, so that a warp's fractions of a turn
 // are worked out once (1666 tokens of 40 heads: 11.3 us with four times as many blocks, 8.5 so). With registers
-// for three, loads of one head at a time and more warps: 142 us for the 36856 tokens below.
+// for three, loads of one head at a time and more warps: 142 us for the 34800 tokens below.
 constexpr int kRopePerSm = 2;
 
 __device__ __forceinline__ void rotate(uint4 a, uint4 b, const float* cs, const float* sn,
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) rope_append_kernel(R
     const long long blk = slot / a.block, in_blk = slot - blk * a.block;
     const int end = min(heads, (part + 1) * per);
     // the loads of several heads first: a store might be to where a later load is from, for all the compiler
-    // knows (36856 tokens of 48 heads: 153 us with one head at a time)
+    // knows (34800 tokens of 48 heads: 153 us with one head at a time)
     for (int h0 = part * per + (lane >> 3); h0 < end; h0 += 4 * kRopeAhead) {
       uint4 x[kRopeAhead], y[kRopeAhead];
       bf16* dst[kRopeAhead];
