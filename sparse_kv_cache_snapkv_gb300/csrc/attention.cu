@@ -29,7 +29,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
-#include <type_traits>
 
 #include "../../include/rkv_testing.h"
 #include "common.cuh"
@@ -704,238 +703,238 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   };
 
   if (warp < 4) {
-  reg_release<kAtLoadRegs>();
-  if (warp == 0) {
-    // ------------------------------------------------------------------ loads
-    const int skip = blockIdx.x == 0 ? p.test_skip : 0;
-    const uint32_t qbytes = (uint32_t)(p.gqa * p.tile_tokens * kHeadDim * 2);
-    const int rows = PAGED ? min(p.pm.block, kAtTile) : kAtTile;  // of one copy
-    int ld = 0;                  // tiles requested
-    int nq[2] = {0, 0};          // Q tiles requested
-    auto slot = [&]() {          // waits for the next place of the ring
-      const int s = ld % kAtStages;
-      if (ld >= kAtStages &&
-          !mbar_wait_warp(&bar.empty[s], (uint32_t)((ld / kAtStages - 1) & 1), limit)) {
-        aborted = true;
-        return -1;
-      }
-      return s;
-    };
-    // rows [k0, k0 + 128) of the unit; behind L nothing need be there
-    auto tile = [&](const CUtensorMap* map, int s, int k0, int blk) {
-      uint8_t* dst = ring + (size_t)s * kAtTileBytes;
-      if (PAGED) {
-        const int copies = min(kAtTile / rows, (x.L - k0 + rows - 1) / rows);
-        if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(copies * rows * 256));
-        __syncwarp();
-        for (int c = lane; c < copies; c += 32) {
-          const int t = k0 + c * rows;
-          const int b = c == lane ? blk : paged_block(p.pm, x.u, t, p.status);
-          const int y = (b * p.n_kv + x.g) * p.pm.block + (t & (p.pm.block - 1));
-          tma_load_2d(dst + c * rows * 128, map, 0, y, &bar.full[s]);
-          tma_load_2d(dst + 16384 + c * rows * 128, map, 64, y, &bar.full[s]);
-        }
-      } else if (lane == 0) {
-        const int y = (x.u * p.n_kv + x.g) * p.cap + k0;
-        mbar_arrive_expect_tx(&bar.full[s], kAtTileBytes);
-        tma_load_2d(dst, map, 0, y, &bar.full[s]);
-        tma_load_2d(dst + 16384, map, 64, y, &bar.full[s]);
-      }
-      __syncwarp();
-    };
-    while (!aborted && next()) {
-      for (int j = 0; j < x.steps && !aborted; ++j) {
-        const int k0 = (x.s0 + j) * kAtTile;
-        int blk = 0;
-        if (PAGED && k0 + lane * rows < x.L && lane * rows < kAtTile)
-          blk = paged_block(p.pm, x.u, k0 + lane * rows, p.status);
-        int s = slot();
-        if (s < 0) break;
-        if (!(skip == RKV_TESTING_ATTENTION_KEYS && ld == 0)) tile(&kmap, s, k0, blk);
-        ++ld;
-        if (j == 0) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (aborted || x.cnt[h] == 0) continue;
-            if (nq[h] > 0 && !mbar_wait_warp(&bar.qempty[h], (uint32_t)((nq[h] - 1) & 1), limit)) {
-              aborted = true;
-              continue;
-            }
-            if (lane == 0 && !(skip == RKV_TESTING_ATTENTION_QUERIES && nq[h] == 0)) {
-              uint8_t* dst = qs + (size_t)h * kAtTileBytes;
-              mbar_arrive_expect_tx(&bar.qfull[h], qbytes);
-              for (int c = 0; c < 2; ++c)
-                tma_load_3d(dst + c * 16384, &qmap, 64 * c, x.g * p.gqa,
-                            x.row0 + h * p.tile_tokens, &bar.qfull[h]);
-            }
-            __syncwarp();
-            ++nq[h];
-          }
-          if (aborted) break;
-        }
-        s = slot();
-        if (s < 0) break;
-        if (!(skip == RKV_TESTING_ATTENTION_VALUES && ld == 1)) tile(&vmap, s, k0, blk);
-        ++ld;
-      }
-    }
-    if (aborted && lane == 0) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
-    // every issued load lands before the CTA ends, whoever gave up (else they have, and this is no wait)
-    for (int j = max(0, ld - kAtStages); j < ld; ++j)
-      mbar_wait_warp(&bar.full[j % kAtStages], (uint32_t)((j / kAtStages) & 1), drain_limit(limit));
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (nq[h] > 0) mbar_wait_warp(&bar.qfull[h], (uint32_t)((nq[h] - 1) & 1), drain_limit(limit));
-  } else if (warp < 3) {
-    // ------------------------------------------------------------------ products of a tile
-    // A warp for each tile of the pair: one waits while the other issues (one warp for both left the tensor
-    // cores idle between its waits: 8K prompt 425 us). The whole warp follows the steps and one lane issues, so
-    // that descriptors are uniform values, a constant away from those of a place of the ring (with one lane
-    // computing them for itself: 510 us).
-    const int h = warp - 1;
-    const uint32_t ring_lo = (smem_addr(ring) & 0x3FFFFu) >> 4;
-    const uint32_t q_lo = ((smem_addr(qs) & 0x3FFFFu) >> 4) + h * (kAtTileBytes >> 4);
-    const uint32_t st = tmem + h * 128, ot = st + 256;
-    uint32_t nq = 0, np = 0, no = 0, nclean = 0;
-    Ring kr{0, 0}, vr{0, 0}, at{0, 0};  // K tile of the step, V tile of the product to come, next load
-    auto wait = [&](uint64_t* b, uint32_t parity) {
-      if (!aborted && !mbar_wait_warp(b, parity & 1u, limit)) aborted = true;
-    };
-    // A step's scores are issued behind the product of the step before, which they follow in the tensor
-    // cores. The tiles take turns with that: products of both at once would end together, and then both
-    // softmaxes would run while the tensor cores wait (8K prompt 496 us). The turn passes on two products
-    // before the last, which hides its way to the other warp.
-    bool pend = false, first = false, last = false, tail = false;
-    uint32_t nturn = 0;
-    auto product = [&](bool pass) {  // O += P V
-      const uint32_t b = ring_lo + vr.place * (kAtTileBytes >> 4), keep = first ? 0u : 1u;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        umma_ts(ot, st + 8 * kk, b + kk * (2048 >> 4), kk ? 1u : keep);
-        if (kk == 5 && pass) mbar_arrive(&bar.turn[h ^ 1]);
-      }
-      if (last) umma_commit(&bar.ofull[h]);
-    };
-    auto scores = [&](bool end) {  // S = Q K^T
-      const uint32_t b = ring_lo + kr.place * (kAtTileBytes >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-        umma_ss(st, q_lo + off, b + off, kk > 0);
-        if (kk == 5) mbar_arrive(&bar.turn[h ^ 1]);
-      }
-      umma_commit(&bar.sfull[h]);
-      if (end) umma_commit(&bar.qempty[h]);
-    };
-    auto ready = [&]() {  // what the product to come needs
-      wait(&bar.full[vr.place], vr.phase);
-      if (tail) wait(&bar.clean, nclean++);
-      if (first && no > 0) wait(&bar.ofree[h], no - 1);
-      wait(&bar.pfull[h], np++);
-      if (last) ++no;
-    };
-    while (!aborted && next()) {
-      for (int j = 0; j < x.steps && !aborted; ++j) {
-        const bool act = j < x.cnt[h], end = j == x.cnt[h] - 1;
-        kr = at;
-        at.step();
-        if (act && j == 0) wait(&bar.qfull[h], nq++);
-        wait(&bar.full[kr.place], kr.phase);
-        if (h == 1 || nturn > 0) wait(&bar.turn[h], h == 1 ? nturn : nturn - 1);
-        ++nturn;
-        if (pend) ready();
-        tc_fence_after();
-        if (!aborted && elect_one()) {
-          if (pend) product(!act);
-          if (act) {
-            scores(end);
-          } else {  // a step that the tile has no part in
-            if (!pend) mbar_arrive(&bar.turn[h ^ 1]);
-            mbar_arrive(&bar.empty[kr.place]);
-          }
-        }
-        __syncwarp();
-        pend = act;
-        first = j == 0;
-        last = end;
-        vr = at;
-        at.step();
-        tail = (x.s0 + j + 1) * kAtTile > x.L;
-        if (tail && lane == 0) mbar_arrive(&bar.dirty);
-        if (!act) {
-          wait(&bar.full[vr.place], vr.phase);
-          if (tail) wait(&bar.clean, nclean++);
-          if (!aborted && lane == 0) mbar_arrive(&bar.empty[vr.place]);
-          __syncwarp();
-        }
-      }
-    }
-    if (!aborted && pend) {
-      ready();
-      tc_fence_after();
-      if (!aborted && elect_one()) product(false);
-      __syncwarp();
-    }
-    if (aborted && lane == 0) {
-      set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
-      umma_commit(&bar.drain[h]);  // let issued products end
-      mbar_wait(&bar.drain[h], 0u, drain_limit(limit));
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------------ pieces, rows behind the last
-    Pieces it;
-    it.init(p);
-    auto find = [&](uint32_t k) {  // piece k; false: there is none
-      const uint32_t i = k % kAtPieces;
-      if (k >= kAtPieces && !mbar_wait_warp(&bar.pread[i], (k / kAtPieces - 1) & 1u, item_limit)) {
-        aborted = true;
-        return false;
-      }
-      Piece y{};
-      const bool any = it.next(p, y);
-      if (lane == 0) {
-        const int4* src = reinterpret_cast<const int4*>(&y);
-        int4* dst = reinterpret_cast<int4*>(pieces + i);
-        dst[0] = src[0];
-        dst[1] = src[1];
-        dst[2] = src[2];
-        mbar_arrive(&bar.pfilled[i]);
-      }
-      __syncwarp();
-      return any;
-    };
-    // p is 0 for keys behind the last, but 0 times what the cache may hold there (infinity, NaN) is not. The
-    // tile's place in the ring is its own from when its step's scores are issued (they are behind all products
-    // that used the place) until its product, so the wait for its load cannot be taken for another one's.
-    int steps = 0, ntail = 0;
-    uint32_t found = 0;
-    bool more = true;
-    for (uint32_t k = 0; !aborted; ++k) {
-      while (more && found <= k + 2 && !aborted) more = find(found++);
-      if (aborted) break;
-      // (its own reading of a piece: no other warp writes them)
-      x = pieces[k % kAtPieces];
-      __syncwarp();
-      if (x.steps == 0) break;
-      const int at = x.L / kAtTile - x.s0, cut = x.L % kAtTile;  // the step that the sequence ends in
-      if (cut && at >= 0 && at < x.steps) {
-        const int load = 2 * (steps + at) + 1, s = load % kAtStages;
-        if (!mbar_wait_warp(&bar.dirty, (uint32_t)(ntail++ & 1), item_limit) ||
-            !mbar_wait_warp(&bar.full[s], (uint32_t)((load / kAtStages) & 1), limit)) {
+    reg_release<kAtLoadRegs>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ loads
+      const int skip = blockIdx.x == 0 ? p.test_skip : 0;
+      const uint32_t qbytes = (uint32_t)(p.gqa * p.tile_tokens * kHeadDim * 2);
+      const int rows = PAGED ? min(p.pm.block, kAtTile) : kAtTile;  // of one copy
+      int ld = 0;                  // tiles requested
+      int nq[2] = {0, 0};          // Q tiles requested
+      auto slot = [&]() {          // waits for the next place of the ring
+        const int s = ld % kAtStages;
+        if (ld >= kAtStages &&
+            !mbar_wait_warp(&bar.empty[s], (uint32_t)((ld / kAtStages - 1) & 1), limit)) {
           aborted = true;
-          break;
+          return -1;
         }
-        uint4* v = reinterpret_cast<uint4*>(ring + (size_t)s * kAtTileBytes + cut * 128);
-        for (int i = lane; i < (kAtTile - cut) * 8; i += 32)
-          v[i] = v[i + 16384 / 16] = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();
+        return s;
+      };
+      // rows [k0, k0 + 128) of the unit; behind L nothing need be there
+      auto tile = [&](const CUtensorMap* map, int s, int k0, int blk) {
+        uint8_t* dst = ring + (size_t)s * kAtTileBytes;
+        if (PAGED) {
+          const int copies = min(kAtTile / rows, (x.L - k0 + rows - 1) / rows);
+          if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(copies * rows * 256));
+          __syncwarp();
+          for (int c = lane; c < copies; c += 32) {
+            const int t = k0 + c * rows;
+            const int b = c == lane ? blk : paged_block(p.pm, x.u, t, p.status);
+            const int y = (b * p.n_kv + x.g) * p.pm.block + (t & (p.pm.block - 1));
+            tma_load_2d(dst + c * rows * 128, map, 0, y, &bar.full[s]);
+            tma_load_2d(dst + 16384 + c * rows * 128, map, 64, y, &bar.full[s]);
+          }
+        } else if (lane == 0) {
+          const int y = (x.u * p.n_kv + x.g) * p.cap + k0;
+          mbar_arrive_expect_tx(&bar.full[s], kAtTileBytes);
+          tma_load_2d(dst, map, 0, y, &bar.full[s]);
+          tma_load_2d(dst + 16384, map, 64, y, &bar.full[s]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.clean);
+      };
+      while (!aborted && next()) {
+        for (int j = 0; j < x.steps && !aborted; ++j) {
+          const int k0 = (x.s0 + j) * kAtTile;
+          int blk = 0;
+          if (PAGED && k0 + lane * rows < x.L && lane * rows < kAtTile)
+            blk = paged_block(p.pm, x.u, k0 + lane * rows, p.status);
+          int s = slot();
+          if (s < 0) break;
+          if (!(skip == RKV_TESTING_ATTENTION_KEYS && ld == 0)) tile(&kmap, s, k0, blk);
+          ++ld;
+          if (j == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (aborted || x.cnt[h] == 0) continue;
+              if (nq[h] > 0 && !mbar_wait_warp(&bar.qempty[h], (uint32_t)((nq[h] - 1) & 1), limit)) {
+                aborted = true;
+                continue;
+              }
+              if (lane == 0 && !(skip == RKV_TESTING_ATTENTION_QUERIES && nq[h] == 0)) {
+                uint8_t* dst = qs + (size_t)h * kAtTileBytes;
+                mbar_arrive_expect_tx(&bar.qfull[h], qbytes);
+                for (int c = 0; c < 2; ++c)
+                  tma_load_3d(dst + c * 16384, &qmap, 64 * c, x.g * p.gqa,
+                              x.row0 + h * p.tile_tokens, &bar.qfull[h]);
+              }
+              __syncwarp();
+              ++nq[h];
+            }
+            if (aborted) break;
+          }
+          s = slot();
+          if (s < 0) break;
+          if (!(skip == RKV_TESTING_ATTENTION_VALUES && ld == 1)) tile(&vmap, s, k0, blk);
+          ++ld;
+        }
       }
-      steps += x.steps;
+      if (aborted && lane == 0) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+      // every issued load lands before the CTA ends, whoever gave up (else they have, and this is no wait)
+      for (int j = max(0, ld - kAtStages); j < ld; ++j)
+        mbar_wait_warp(&bar.full[j % kAtStages], (uint32_t)((j / kAtStages) & 1), drain_limit(limit));
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (nq[h] > 0) mbar_wait_warp(&bar.qfull[h], (uint32_t)((nq[h] - 1) & 1), drain_limit(limit));
+    } else if (warp < 3) {
+      // ------------------------------------------------------------------ products of a tile
+      // A warp for each tile of the pair: one waits while the other issues (one warp for both left the tensor
+      // cores idle between its waits: 8K prompt 425 us). The whole warp follows the steps and one lane issues, so
+      // that descriptors are uniform values, a constant away from those of a place of the ring (with one lane
+      // computing them for itself: 510 us).
+      const int h = warp - 1;
+      const uint32_t ring_lo = (smem_addr(ring) & 0x3FFFFu) >> 4;
+      const uint32_t q_lo = ((smem_addr(qs) & 0x3FFFFu) >> 4) + h * (kAtTileBytes >> 4);
+      const uint32_t st = tmem + h * 128, ot = st + 256;
+      uint32_t nq = 0, np = 0, no = 0, nclean = 0;
+      Ring kr{0, 0}, vr{0, 0}, at{0, 0};  // K tile of the step, V tile of the product to come, next load
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (!aborted && !mbar_wait_warp(b, parity & 1u, limit)) aborted = true;
+      };
+      // A step's scores are issued behind the product of the step before, which they follow in the tensor
+      // cores. The tiles take turns with that: products of both at once would end together, and then both
+      // softmaxes would run while the tensor cores wait (8K prompt 496 us). The turn passes on two products
+      // before the last, which hides its way to the other warp.
+      bool pend = false, first = false, last = false, tail = false;
+      uint32_t nturn = 0;
+      auto product = [&](bool pass) {  // O += P V
+        const uint32_t b = ring_lo + vr.place * (kAtTileBytes >> 4), keep = first ? 0u : 1u;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_ts(ot, st + 8 * kk, b + kk * (2048 >> 4), kk ? 1u : keep);
+          if (kk == 5 && pass) mbar_arrive(&bar.turn[h ^ 1]);
+        }
+        if (last) umma_commit(&bar.ofull[h]);
+      };
+      auto scores = [&](bool end) {  // S = Q K^T
+        const uint32_t b = ring_lo + kr.place * (kAtTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          umma_ss(st, q_lo + off, b + off, kk > 0);
+          if (kk == 5) mbar_arrive(&bar.turn[h ^ 1]);
+        }
+        umma_commit(&bar.sfull[h]);
+        if (end) umma_commit(&bar.qempty[h]);
+      };
+      auto ready = [&]() {  // what the product to come needs
+        wait(&bar.full[vr.place], vr.phase);
+        if (tail) wait(&bar.clean, nclean++);
+        if (first && no > 0) wait(&bar.ofree[h], no - 1);
+        wait(&bar.pfull[h], np++);
+        if (last) ++no;
+      };
+      while (!aborted && next()) {
+        for (int j = 0; j < x.steps && !aborted; ++j) {
+          const bool act = j < x.cnt[h], end = j == x.cnt[h] - 1;
+          kr = at;
+          at.step();
+          if (act && j == 0) wait(&bar.qfull[h], nq++);
+          wait(&bar.full[kr.place], kr.phase);
+          if (h == 1 || nturn > 0) wait(&bar.turn[h], h == 1 ? nturn : nturn - 1);
+          ++nturn;
+          if (pend) ready();
+          tc_fence_after();
+          if (!aborted && elect_one()) {
+            if (pend) product(!act);
+            if (act) {
+              scores(end);
+            } else {  // a step that the tile has no part in
+              if (!pend) mbar_arrive(&bar.turn[h ^ 1]);
+              mbar_arrive(&bar.empty[kr.place]);
+            }
+          }
+          __syncwarp();
+          pend = act;
+          first = j == 0;
+          last = end;
+          vr = at;
+          at.step();
+          tail = (x.s0 + j + 1) * kAtTile > x.L;
+          if (tail && lane == 0) mbar_arrive(&bar.dirty);
+          if (!act) {
+            wait(&bar.full[vr.place], vr.phase);
+            if (tail) wait(&bar.clean, nclean++);
+            if (!aborted && lane == 0) mbar_arrive(&bar.empty[vr.place]);
+            __syncwarp();
+          }
+        }
+      }
+      if (!aborted && pend) {
+        ready();
+        tc_fence_after();
+        if (!aborted && elect_one()) product(false);
+        __syncwarp();
+      }
+      if (aborted && lane == 0) {
+        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+        umma_commit(&bar.drain[h]);  // let issued products end
+        mbar_wait(&bar.drain[h], 0u, drain_limit(limit));
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ pieces, rows behind the last
+      Pieces it;
+      it.init(p);
+      auto find = [&](uint32_t k) {  // piece k; false: there is none
+        const uint32_t i = k % kAtPieces;
+        if (k >= kAtPieces && !mbar_wait_warp(&bar.pread[i], (k / kAtPieces - 1) & 1u, item_limit)) {
+          aborted = true;
+          return false;
+        }
+        Piece y{};
+        const bool any = it.next(p, y);
+        if (lane == 0) {
+          const int4* src = reinterpret_cast<const int4*>(&y);
+          int4* dst = reinterpret_cast<int4*>(pieces + i);
+          dst[0] = src[0];
+          dst[1] = src[1];
+          dst[2] = src[2];
+          mbar_arrive(&bar.pfilled[i]);
+        }
+        __syncwarp();
+        return any;
+      };
+      // p is 0 for keys behind the last, but 0 times what the cache may hold there (infinity, NaN) is not. The
+      // tile's place in the ring is its own from when its step's scores are issued (they are behind all products
+      // that used the place) until its product, so the wait for its load cannot be taken for another one's.
+      int steps = 0, ntail = 0;
+      uint32_t found = 0;
+      bool more = true;
+      for (uint32_t k = 0; !aborted; ++k) {
+        while (more && found <= k + 2 && !aborted) more = find(found++);
+        if (aborted) break;
+        // (its own reading of a piece: no other warp writes them)
+        x = pieces[k % kAtPieces];
+        __syncwarp();
+        if (x.steps == 0) break;
+        const int at = x.L / kAtTile - x.s0, cut = x.L % kAtTile;  // the step that the sequence ends in
+        if (cut && at >= 0 && at < x.steps) {
+          const int load = 2 * (steps + at) + 1, s = load % kAtStages;
+          if (!mbar_wait_warp(&bar.dirty, (uint32_t)(ntail++ & 1), item_limit) ||
+              !mbar_wait_warp(&bar.full[s], (uint32_t)((load / kAtStages) & 1), limit)) {
+            aborted = true;
+            break;
+          }
+          uint4* v = reinterpret_cast<uint4*>(ring + (size_t)s * kAtTileBytes + cut * 128);
+          for (int i = lane; i < (kAtTile - cut) * 8; i += 32)
+            v[i] = v[i + 16384 / 16] = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.clean);
+        }
+        steps += x.steps;
+      }
     }
-  }
   } else if (warp < 8) {
     reg_release<kAtOutRegs>();
     // ------------------------------------------------------------------ outputs
@@ -958,6 +957,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         ++no[h];
         if (row == 0) mbar_arrive(&bar.empty[(2 * (steps + x.cnt[h] - 1) + 1) % kAtStages]);  // the last V tile
+        __syncwarp();
         tc_fence_after();
         const float l = sums[turn * 256 + h * 128 + row];
         const bool none = l == 0.f;  // the row sees nothing: zeros, whatever v holds
@@ -1028,6 +1028,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           mbar_arrive(&bar.empty[at.place]);
           if (j > 0) mbar_arrive(&bar.empty[vplace]);
         }
+        __syncwarp();
         at.step();
         vplace = at.place;
         at.step();
