@@ -609,6 +609,18 @@ def _weights16(t, shape, dev, given=True):
     return p
 
 
+def _first(t, name, dtype, rank, dev):
+    """Shape and address of a tensor that others' shapes follow from."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor of {rank} dimensions")
+    shape = t.shape
+    if len(shape) != rank:
+        raise ValueError(f"{name} must be a tensor of {rank} dimensions")
+    if t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+        return shape, t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+
+
 def _at_or_none(t, name, dtype, shape, dev):
     return None if t is None else _at(t, name, dtype, shape, dev)
 
@@ -624,7 +636,7 @@ def _call(fn, args, ws, nbytes, dev, stream):
     current one). nbytes(): the workspace to make where none is given; it is made on that stream."""
     if dev < 0:
         raise ValueError("librkv takes device tensors only")
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or torch._C._cuda_getDevice() != dev:
         if stream is not None and stream.device.index != dev:
             raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
         with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
@@ -863,18 +875,19 @@ def rkv_reserve_slots(new_len, length, held, block_table, free_blocks, free_coun
     """Places for new_len[u] more tokens of every unit: blocks off the free stack into block_table,
     q_start [n + 1], and slots and positions [max_tokens] of the packed tokens; see include/rkv.h.
     length_out, held_out and free_count_out may be the inputs."""
-    n, max_blocks = _dims(block_table, "block_table", 2)
-    num_blocks, room = _dims(free_blocks, "free_blocks", 1)[0], _dims(slots, "slots", 1)[0]
+    _dims(block_table, "block_table", 2)
     dev = block_table.get_device()
-    args = (_at(new_len, "new_len", _I32, (n,), dev), _at(length, "len", _I32, (n,), dev),
-            _at(held, "held", _I32, (n,), dev),
-            _at(block_table, "block_table", _I32, (n, max_blocks), dev),
-            _at(free_blocks, "free_blocks", _I32, (num_blocks,), dev),
-            _at(free_count, "free_count", _I32, (1,), dev), n, num_blocks, block, max_blocks, room,
-            _at(q_start, "q_start", _I32, (n + 1,), dev), _at(slots, "slots", _I32, (room,), dev),
+    (n, max_blocks), table = _first(block_table, "block_table", _I32, 2, dev)
+    (num_blocks,), free = _first(free_blocks, "free_blocks", _I32, 1, dev)
+    (room,), places = _first(slots, "slots", _I32, 1, dev)
+    each, one = (n,), (1,)
+    args = (_at(new_len, "new_len", _I32, each, dev), _at(length, "len", _I32, each, dev),
+            _at(held, "held", _I32, each, dev), table, free,
+            _at(free_count, "free_count", _I32, one, dev), n, num_blocks, block, max_blocks, room,
+            _at(q_start, "q_start", _I32, (n + 1,), dev), places,
             _at(positions, "positions", _I32, (room,), dev),
-            _at(length_out, "len_out", _I32, (n,), dev), _at(held_out, "held_out", _I32, (n,), dev),
-            _at(free_count_out, "free_count_out", _I32, (1,), dev))
+            _at(length_out, "len_out", _I32, each, dev), _at(held_out, "held_out", _I32, each, dev),
+            _at(free_count_out, "free_count_out", _I32, one, dev))
     return _call("rkv_reserve_slots", args, ws, lambda: rkv_reserve_slots_workspace_bytes(n), dev,
                  stream)
 
@@ -925,17 +938,16 @@ def rkv_rope_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache
     stores k and v in row slots[t] of the caches ([num_blocks][n_kv][block][128], or
     [n][n_kv][cap][128] with slots u * cap + row); see include/rkv.h."""
     tokens, hq, _ = _dims(q, "q", 3)
-    num_blocks, n_kv, block, d = shape = _dims(k_cache, "k_cache", 4)
     dev = q.get_device()
-    rot = 2 * _dims(inv_freq, "inv_freq", 1)[0]
+    shape, k_rows = _first(k_cache, "k_cache", _BF16, 4, dev)
+    num_blocks, n_kv, block, d = shape
+    (pairs,), freq = _first(inv_freq, "inv_freq", _F32, 1, dev)
+    each = (tokens,)
     args = (*_tokens(q, "q", hq, dev, tokens), *_tokens(k, "k", n_kv, dev, tokens),
-            *_tokens(v, "v", n_kv, dev, tokens),
-            _at(positions, "positions", _I32, (tokens,), dev),
-            _at(inv_freq, "inv_freq", _F32, (rot // 2,), dev),
-            _at(slots, "slots", _I32, (tokens,), dev), tokens, hq, n_kv, d, rot, int(interleaved),
-            mscale, _at(q_out, "q_out", _BF16, (tokens, hq, HEAD_DIM), dev),
-            _at(k_cache, "k_cache", _BF16, shape, dev), _at(v_cache, "v_cache", _BF16, shape, dev),
-            num_blocks, block)
+            *_tokens(v, "v", n_kv, dev, tokens), _at(positions, "positions", _I32, each, dev), freq,
+            _at(slots, "slots", _I32, each, dev), tokens, hq, n_kv, d, 2 * pairs, int(interleaved),
+            mscale, _at(q_out, "q_out", _BF16, (tokens, hq, HEAD_DIM), dev), k_rows,
+            _at(v_cache, "v_cache", _BF16, shape, dev), num_blocks, block)
     return _call("rkv_rope_append", args, ws, rkv_rope_append_workspace_bytes, dev, stream)
 
 
@@ -945,24 +957,28 @@ def rkv_prompt_attention_workspace_bytes(n: int, n_kv: int, gqa: int, tokens: in
 
 def _attention(fn, q, q_start, mask, k, v, table, length, scale, out, ws, stream, hook=()):
     tokens, hq, _ = _dims(q, "q", 3)
-    lead, n_kv, rows, d = shape = _dims(k, "k", 4)
-    dev, n = q.get_device(), _dims(length, "len", 1)[0]
+    dev = q.get_device()
+    shape, k_rows = _first(k, "k", _BF16, 4, dev)
+    lead, n_kv, rows, d = shape
+    (n,), lens = _first(length, "len", _I32, 1, dev)
     gqa = _group(hq, n_kv)
     tree = ()
     if mask is not None:
-        words = _dims(mask, "mask", 2)[1]
-        tree = (_at(mask, "mask", _I32, (tokens, words), dev), words)
+        (lines, words), bits = _first(mask, "mask", _I32, 2, dev)
+        if lines != tokens:
+            raise ValueError(f"mask has {lines} rows, expected {tokens}")
+        tree = (bits, words)
     if table is None:
         if lead != n:
             raise ValueError(f"{n} lengths for a cache of {lead} units")
         paged, sizes = (), (tokens, rows)
     else:
-        max_blocks = _dims(table, "block_table", 2)[1]
-        paged = (_at(table, "block_table", _I32, (n, max_blocks), dev),)
-        sizes = (tokens, lead, rows, max_blocks)
+        (lines, max_blocks), blocks = _first(table, "block_table", _I32, 2, dev)
+        if lines != n:
+            raise ValueError(f"block_table has {lines} rows, expected {n}")
+        paged, sizes = (blocks,), (tokens, lead, rows, max_blocks)
     args = (*_tokens(q, "q", hq, dev, tokens), _at(q_start, "q_start", _I32, (n + 1,), dev), *tree,
-            _at(k, "k", _BF16, shape, dev), _at(v, "v", _BF16, shape, dev), *paged,
-            _at(length, "len", _I32, (n,), dev), n, n_kv, gqa, d, *sizes, scale,
+            k_rows, _at(v, "v", _BF16, shape, dev), *paged, lens, n, n_kv, gqa, d, *sizes, scale,
             _at(out, "out", _BF16, (tokens, hq, HEAD_DIM), dev), *hook)
     return _call(fn, args, ws, lambda: rkv_prompt_attention_workspace_bytes(n, n_kv, gqa, tokens),
                  dev, stream)
