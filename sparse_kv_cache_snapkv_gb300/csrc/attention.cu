@@ -239,11 +239,35 @@ struct __align__(16) Piece {
   int row0, t0, T, L;  // as in its AtRec
   int u, g, s0;        // unit, KV head, first step
   int steps;           // the larger of cnt; 0: there is no piece any more
-  int cnt[2];          // steps of each tile, from s0
+  int cnt0, cnt1;      // steps of each tile, from s0
   int slot;            // where its part goes; -1: the item is whole
   int pad;
+  __device__ __forceinline__ int cnt(int h) const { return h ? cnt1 : cnt0; }
 };
 static_assert(sizeof(Piece) == 48, "three 16-byte words");
+
+// Field by field, so that a piece stays in registers (read through a pointer to it, it lay in local memory).
+__device__ __forceinline__ void read_piece(Piece& x, const Piece* from) {
+  const int4* src = reinterpret_cast<const int4*>(from);
+  const int4 a = src[0], b = src[1], c = src[2];
+  x.row0 = a.x;
+  x.t0 = a.y;
+  x.T = a.z;
+  x.L = a.w;
+  x.u = b.x;
+  x.g = b.y;
+  x.s0 = b.z;
+  x.steps = b.w;
+  x.cnt0 = c.x;
+  x.cnt1 = c.y;
+  x.slot = c.z;
+}
+__device__ __forceinline__ void write_piece(Piece* to, const Piece& x) {
+  int4* dst = reinterpret_cast<int4*>(to);
+  dst[0] = make_int4(x.row0, x.t0, x.T, x.L);
+  dst[1] = make_int4(x.u, x.g, x.s0, x.steps);
+  dst[2] = make_int4(x.cnt0, x.cnt1, x.slot, 0);
+}
 
 struct Pieces {
   int split, count, per, total;
@@ -428,8 +452,9 @@ struct Pieces {
       const int t = x.t0 + h * p.tile_tokens;  // the tile's first token
       const int keys = p.mask ? x.L : x.L - x.T + min(t + p.tile_tokens, x.T);
       const int all = t < x.T ? (keys + kAtTile - 1) / kAtTile : 0;
-      x.cnt[h] = max(0, min(x.s0 + len, all) - x.s0);
-      x.steps = max(x.steps, x.cnt[h]);
+      const int cnt = max(0, min(x.s0 + len, all) - x.s0);
+      (h ? x.cnt1 : x.cnt0) = cnt;
+      x.steps = max(x.steps, cnt);
     }
     return true;
   }
@@ -691,11 +716,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       aborted = true;
       return false;
     }
-    const int4* src = reinterpret_cast<const int4*>(pieces + i);
-    int4* dst = reinterpret_cast<int4*>(&x);
-    dst[0] = src[0];
-    dst[1] = src[1];
-    dst[2] = src[2];
+    read_piece(x, pieces + i);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.pread[i]);
     ++npiece;
@@ -755,7 +776,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (j == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (aborted || x.cnt[h] == 0) continue;
+              if (aborted || x.cnt(h) == 0) continue;
               if (nq[h] > 0 && !mbar_wait_warp(&bar.qempty[h], (uint32_t)((nq[h] - 1) & 1), limit)) {
                 aborted = true;
                 continue;
@@ -835,7 +856,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       };
       while (!aborted && next()) {
         for (int j = 0; j < x.steps && !aborted; ++j) {
-          const bool act = j < x.cnt[h], end = j == x.cnt[h] - 1;
+          const bool act = j < x.cnt(h), end = j == x.cnt(h) - 1;
           kr = at;
           at.step();
           if (act && j == 0) wait(&bar.qfull[h], nq++);
@@ -894,11 +915,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         Piece y{};
         const bool any = it.next(p, y);
         if (lane == 0) {
-          const int4* src = reinterpret_cast<const int4*>(&y);
-          int4* dst = reinterpret_cast<int4*>(pieces + i);
-          dst[0] = src[0];
-          dst[1] = src[1];
-          dst[2] = src[2];
+          write_piece(pieces + i, y);
           mbar_arrive(&bar.pfilled[i]);
         }
         __syncwarp();
@@ -914,7 +931,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         while (more && found <= k + 2 && !aborted) more = find(found++);
         if (aborted) break;
         // (its own reading of a piece: no other warp writes them)
-        x = pieces[k % kAtPieces];
+        read_piece(x, pieces + k % kAtPieces);
         __syncwarp();
         if (x.steps == 0) break;
         const int at = x.L / kAtTile - x.s0, cut = x.L % kAtTile;  // the step that the sequence ends in
@@ -946,7 +963,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     while (!aborted && next()) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (aborted || x.cnt[h] == 0) continue;
+        if (aborted || x.cnt(h) == 0) continue;
         const int t = x.t0 + h * p.tile_tokens + tok;  // this row's token
         const bool valid = tok < p.tile_tokens && t < x.T;
         const uint32_t turn = no[h] & 1;
@@ -956,7 +973,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           continue;
         }
         ++no[h];
-        if (row == 0) mbar_arrive(&bar.empty[(2 * (steps + x.cnt[h] - 1) + 1) % kAtStages]);  // the last V tile
+        if (row == 0) mbar_arrive(&bar.empty[(2 * (steps + x.cnt(h) - 1) + 1) % kAtStages]);  // the last V tile
         __syncwarp();
         tc_fence_after();
         const float l = sums[turn * 256 + h * 128 + row];
@@ -1017,7 +1034,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       float m = kNoMax, l = 0.f;
       const int end = TREE ? x.L : __reduce_max_sync(0xffffffffu, lim) + 1;
       const AtSees sees{clear, end, lim, base, valid ? x.T : 0, bits};
-      for (int j = 0; j < x.cnt[h]; ++j) {
+      for (int j = 0; j < x.cnt(h); ++j) {
         if (!mbar_wait_warp(&bar.sfull[h], ns++ & 1u, limit)) {
           aborted = true;
           break;
@@ -1080,13 +1097,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         l += sum;
       }
       if (aborted) break;
-      for (int j = x.cnt[h]; j < x.steps; ++j) {  // steps of the other tile alone
+      for (int j = x.cnt(h); j < x.steps; ++j) {  // steps of the other tile alone
         at.step();
         at.step();
       }
       if (x.slot >= 0)  // (l = 0: a part that the tile has no steps in, or rows that see nothing in)
         p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(m, valid ? l : 0.f);
-      if (x.cnt[h] > 0) {
+      if (x.cnt(h) > 0) {
         sums[(no & 1) * 256 + h * 128 + row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.lfull[h][no & 1]);
