@@ -92,6 +92,7 @@ struct AtParams {
   int n, n_kv, gqa, hq, tokens, cap, words, room, ctas;
   int few;          // 1: every CTA makes the plan of at most kFewPairs pairs itself
   int tile_tokens;  // 128 / gqa
+  int part_rows;    // rows of an item that can be any: all 256, or those of the call's few tokens
   float scale_log2;
   const int32_t* q_start;
   const int32_t* len;
@@ -103,8 +104,8 @@ struct AtParams {
   AtRec* rec;         // [room], linear order
   AtRec* sorted;      // [room]
   int* unit_first;    // [n + 1]
-  float2* part_ml;    // [2 ctas][256]
-  float* part_o;      // [2 ctas][256][128]
+  float2* part_ml;    // [2 ctas][part_rows]
+  float* part_o;      // [2 ctas][part_rows][128]
   uint32_t* status;
   WaitLimit wait_limit;
   WaitLimit item_limit;  // of waits that may take as long as an item
@@ -981,7 +982,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const float f = l > 0.f ? 1.f / l : l;
         const uint32_t od = tmem + ((uint32_t)(quarter * 32) << 16) + 256 + h * 128;
         bf16* dst = p.out + ((size_t)(x.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
-        float* part = p.part_o + ((size_t)max(x.slot, 0) * 256 + h * 128 + row) * kHeadDim;
+        float* part = p.part_o + ((size_t)max(x.slot, 0) * p.part_rows + h * 128 + row) * kHeadDim;
         if (__any_sync(0xffffffffu, valid)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -1101,8 +1102,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at.step();
         at.step();
       }
-      if (x.slot >= 0)  // (l = 0: a part that the tile has no steps in, or rows that see nothing in)
-        p.part_ml[(size_t)x.slot * 256 + h * 128 + row] = make_float2(m, valid ? l : 0.f);
+      if (x.slot >= 0 && valid)  // (l = 0: a part that the tile has no steps in, or that the row sees nothing of)
+        p.part_ml[(size_t)x.slot * p.part_rows + h * 128 + row] = make_float2(m, l);
       if (x.cnt(h) > 0) {
         sums[(no & 1) * 256 + h * 128 + row] = l;
         __syncwarp();
@@ -1133,7 +1134,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinPerSm) at_join_kernel(At
   const AtPlan pl = *p.plan;
   if (!pl.split) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, borders = p.ctas - 1;
-  for (int work = blockIdx.x; work < borders * (256 / kJoinWarps); work += gridDim.x) {
+  const int groups = (p.part_rows + kJoinWarps - 1) / kJoinWarps;
+  for (int work = blockIdx.x; work < borders * groups; work += gridDim.x) {
     const int y = work / borders, c = work - y * borders + 1;
     const AtFirst f = p.first[c];
     if (f.rec < 0 || f.off == 0) continue;
@@ -1144,7 +1146,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinPerSm) at_join_kernel(At
     const int parts = (int)((a + r.steps - 1) / pl.per) - c0 + 1;
     const int row = y * kJoinWarps + warp, t = (row & 127) / p.gqa, tok = (row >> 7) * p.tile_tokens + t;
     if (t >= p.tile_tokens || r.t0 + tok >= r.T) continue;
-    auto at = [&](int i) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * 256 + row; };
+    auto at = [&](int i) { return (size_t)(i ? 2 * (c0 + i) : 2 * c0 + 1) * p.part_rows + row; };
     float m = kNoMax, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < parts; i0 += 32) {
@@ -1196,7 +1198,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinPerSm) at_join_kernel(At
 // ------------------------------------------------------------------------------------------
 struct AtSizes {
   size_t plan, first, rec, unit, ml, o;
-  int room;
+  int room, part_rows;
 };
 
 static AtSizes at_sizes(int n, int gqa, int tokens) {
@@ -1207,8 +1209,9 @@ static AtSizes at_sizes(int n, int gqa, int tokens) {
   z.first = align_up((size_t)ctas * sizeof(AtFirst), 256);
   z.rec = align_up((size_t)z.room * sizeof(AtRec), 256);
   z.unit = align_up((size_t)(n + 1) * 4, 256);
-  z.ml = (size_t)2 * ctas * 256 * sizeof(float2);
-  z.o = (size_t)2 * ctas * 256 * kHeadDim * 4;
+  z.part_rows = tokens <= kAtRows / gqa ? tokens * gqa : 2 * kAtRows;
+  z.ml = align_up((size_t)2 * ctas * z.part_rows * sizeof(float2), 256);
+  z.o = (size_t)2 * ctas * z.part_rows * kHeadDim * 4;
   return z;
 }
 
@@ -1268,6 +1271,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.room = z.room;
   p.ctas = device_sm_count();
   p.tile_tokens = tile_tokens;
+  p.part_rows = z.part_rows;
   p.scale_log2 = a.scale_log2;
   p.q_start = a.q_start;
   p.len = a.len;

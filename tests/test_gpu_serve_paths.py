@@ -257,7 +257,8 @@ def test_captured_and_replayed_with_one_workspace():
 def test_workspace_contents_do_not_matter_and_nothing_is_written_behind():
     from sparse_kv_cache_snapkv_gb300 import rkv
     for c in (Case(51, [64], [9000], words=2), Case(52, [500, 3, 70], [500, 3000, 100]),
-              Case(53, [1] * 80, [50] * 80), Case(54, [64] * 70, [700] * 70, n_kv=1)):
+              Case(53, [1] * 80, [50] * 80), Case(54, [64] * 70, [700] * 70, n_kv=1),
+              Case(55, [3], [9000]), Case(56, [32], [20000], gqa=4, words=1), Case(57, [7, 4], [9000, 3000], gqa=11)):
         need = rkv.rkv_prompt_attention_workspace_bytes(c.n, c.n_kv, c.gqa, c.tokens)
         whole = torch.randint(0, 255, (need + 4096,), dtype=torch.uint8, device="cuda")
         behind = whole[need:].clone()
