@@ -93,6 +93,7 @@ struct AtParams {
   int few;          // 1: every CTA makes the plan of at most kFewPairs pairs itself
   int tile_tokens;  // 128 / gqa
   int part_rows;    // rows of an item that can be any: all 256, or those of the call's few tokens
+  int whole;  // 1: outputs and parts begin on 32 bytes
   float scale_log2;
   const int32_t* q_start;
   const int32_t* len;
@@ -536,7 +537,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
-// A whole sector at once.
+// A whole sector at once; dst begins on 32 bytes.
 __device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -637,6 +638,33 @@ __device__ __noinline__ void at_scale(uint32_t o, float f) {
     tmem_st32(o + 32 * c, s);
   }
   tmem_st_wait();
+}
+
+// A row of O to where it goes, in stores of 16 bytes: for outputs or a workspace that begin on 16 bytes, which is all
+// that the call asks for, and not on the 32 that a store of a sector does (packed prompts 213 us by sectors, 223 in
+// halves; 64 drafted tokens over 131071 rows 118 and 121). Out of the way of the usual code: as a branch at each store
+// it cost the packed prompts 4 us.
+__device__ __noinline__ void at_write16(uint32_t od, bool valid, float* part, bf16* dst, bool none, float f) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    tmem_ld32(od + 32 * c, o);
+    if (valid && part) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    } else if (valid) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = none ? 0u : pack_bf16x2(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
+        *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncwarp();
+  }
 }
 
 struct AtBars {
@@ -983,7 +1011,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const uint32_t od = tmem + ((uint32_t)(quarter * 32) << 16) + 256 + h * 128;
         bf16* dst = p.out + ((size_t)(x.row0 + h * p.tile_tokens + tok) * p.hq + x.g * p.gqa + head) * kHeadDim;
         float* part = p.part_o + ((size_t)max(x.slot, 0) * p.part_rows + h * 128 + row) * kHeadDim;
-        if (__any_sync(0xffffffffu, valid)) {
+        if (!__any_sync(0xffffffffu, valid)) {
+        } else if (!p.whole) {
+          at_write16(od, valid, x.slot >= 0 ? part : nullptr, dst, none, f);
+        } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
@@ -1292,6 +1323,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.part_ml = reinterpret_cast<float2*>(w);
   w += z.ml;
   p.part_o = reinterpret_cast<float*>(w);
+  p.whole = (reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.part_o)) % 32 == 0;
   p.status = a.status;
   p.wait_limit = a.wait_limit_ns ? WaitLimit{a.wait_limit_ns} : kWaitLimit;
   // (a step takes some 2 us)
