@@ -925,10 +925,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (!aborted && elect_one()) product(false);
         __syncwarp();
       }
-      if (aborted && lane == 0) {
-        set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
-        umma_commit(&bar.drain[h]);  // let issued products end
-        mbar_wait(&bar.drain[h], 0u, drain_limit(limit));
+      if (aborted) {
+        if (lane == 0) set_status(p.status, RKV_DEV_WAIT_TIMEOUT);
+        // let issued products end (a commit is about those of its own lane)
+        if (elect_one()) umma_commit(&bar.drain[h]);
+        __syncwarp();
+        mbar_wait_warp(&bar.drain[h], 0u, drain_limit(limit));
       }
       __syncwarp();
     } else {
