@@ -410,11 +410,7 @@ struct Pieces {
   }
   // whole items come in waves of one per CTA, every second wave from the other end
   __device__ __forceinline__ void item(const AtParams& p) {
-    long long i = (long long)wave * gridDim.x + ((wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (i >= (long long)count * p.n_kv) {
-      ++wave;
-      i = (long long)wave * gridDim.x + ((wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    }
+    const long long i = (long long)wave * gridDim.x + ((wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     ++wave;
     left = i < (long long)count * p.n_kv;
     if (left) {
