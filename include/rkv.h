@@ -544,8 +544,8 @@ rkv_status rkv_evict_kv4(void* k_codes, void* k_scales, void* v_codes, void* v_s
  * multiple of 8, at least heads * 128), the heads of one token contiguous.
  * A slot names a row of every KV head: slot = b * block + r is row r of block b of pools
  * [num_blocks][n_kv][block][128]; a contiguous cache [n][n_kv][cap][128] is the pool of n blocks of
- * cap rows (any block size >= 1 is taken here). A negative slot is no place. No *_workspace_bytes
- * of this part falls when one of its arguments grows.
+ * cap rows (any block size >= 1 is taken here). A negative slot is no place. n is at most 2^30.
+ * No *_workspace_bytes of this part falls when one of its arguments grows (0 for what is refused).
  *
  * Block tables and slots on the device. The free blocks are a stack: free_blocks [num_blocks]
  * int32, entries 0 .. free_count[0]-1, the top last.

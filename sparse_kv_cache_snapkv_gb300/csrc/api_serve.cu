@@ -15,6 +15,7 @@ using namespace rkv;
 namespace {
 
 constexpr int kMostRows = 1 << 30;  // rows of a pool or table: slots and positions stay within 31 bits
+constexpr int kMostUnits = 1 << 30;  // of a call: steps over the units, and pairs of tiles, stay within 31 bits
 
 rkv_status ws_check(const void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return RKV_ERR_INVALID_ARG;
@@ -29,7 +30,7 @@ bool stride_ok(int64_t stride, int heads) {
 }
 
 bool slot_sizes_ok(int n, int num_blocks, int block, int max_blocks) {
-  return n > 0 && n < INT_MAX && num_blocks > 0 && block > 0 && max_blocks > 0 &&
+  return n > 0 && n <= kMostUnits && num_blocks > 0 && block > 0 && max_blocks > 0 &&
          (long long)num_blocks * block <= kMostRows && (long long)max_blocks * block <= kMostRows;
 }
 
@@ -82,7 +83,7 @@ extern "C" {
 
 // ------------------------------------------------------------------------------- places
 size_t rkv_reserve_slots_workspace_bytes(int n) {
-  return n > 0 && n < INT_MAX ? kStatusBytes + slots_scratch_bytes(n) : 0;
+  return n > 0 && n <= kMostUnits ? kStatusBytes + slots_scratch_bytes(n) : 0;
 }
 size_t rkv_release_blocks_workspace_bytes(int n) { return rkv_reserve_slots_workspace_bytes(n); }
 
@@ -228,7 +229,7 @@ rkv_status rkv_rope_append(const void* q, int64_t q_stride, const void* k, int64
 
 // ------------------------------------------------------------------------------- attention
 size_t rkv_prompt_attention_workspace_bytes(int n, int n_kv, int gqa, int tokens) {
-  if (n <= 0 || n >= INT_MAX || n_kv <= 0 || gqa <= 0 || gqa > kMaxAttentionGqa || tokens <= 0 ||
+  if (n <= 0 || n > kMostUnits || n_kv <= 0 || gqa <= 0 || gqa > kMaxAttentionGqa || tokens <= 0 ||
       (double)tokens * n_kv * gqa > INT_MAX - 512)
     return 0;
   return kStatusBytes + attention_scratch_bytes(n, gqa, tokens);
