@@ -568,7 +568,13 @@ rkv_status rkv_evict_kv4(void* k_codes, void* k_scales, void* v_codes, void* v_s
  * blocks held than its tokens need, or a block outside [0, num_blocks) among those that its new
  * tokens go to (RKV_DEV_BAD_INDEX; in the latter case those tokens alone have no place); blocks
  * needed, and more needed by it and the units before it, served or not, than are free
- * (RKV_DEV_NO_BLOCKS). free_count outside [0, num_blocks]: RKV_DEV_BAD_INDEX, none is free. */
+ * (RKV_DEV_NO_BLOCKS). free_count outside [0, num_blocks]: RKV_DEV_BAD_INDEX, none is free.
+ * q_start counts the tokens of a unit that is not served too, where they lie in the packed arrays. With their
+ * slots of -1 rkv_rope_append leaves them out (nothing is stored, q_out stays), but the attentions below know
+ * q_start and len alone: they take the last rows of the unit's old length for those of the new tokens and write
+ * outputs that mean nothing, and report nothing themselves unless the unit has fewer rows than that. So the status
+ * of this call is to be checked before a step's outputs are used (one workspace for the step's calls gathers
+ * their statuses); the units concerned are those whose new tokens' slots are all -1. */
 size_t rkv_reserve_slots_workspace_bytes(int n);
 rkv_status rkv_reserve_slots(const int32_t* new_len, const int32_t* len, const int32_t* held,
                              int32_t* block_table, const int32_t* free_blocks,
