@@ -605,13 +605,19 @@ rkv_status rkv_release_blocks(const int32_t* len, const int32_t* held, const int
  *                     factor, linear in the pair's number between the (real) numbers of these two;
  *                     mscale = 0.1 ln(factor) + 1 (factor > 1)
  *   RKV_ROPE_SMOOTH   the same with a ramp linear in the number of turns; mscale 1
- * factor >= 1; ctx > 0, fast > slow > 0 for the last two (ignored by the others). rot_dim even,
+ *   RKV_ROPE_BY_WHOLE_PARTS  RKV_ROPE_BY_PARTS with the ramp's ends rounded outward, down to a whole pair's number
+ *                     for `fast` and up for `slow`, both brought into [0, rot_dim - 1] (the ramp of equal ends is
+ *                     0.001 long). Models that were scaled by parts were made with one or the other: with 128
+ *                     dimensions, base 1e6, ctx 32768, fast 32 and slow 1 the ends are 23.6 and 39.7, or 23 and 40,
+ *                     and frequencies on the ramp are some per cent apart
+ * factor >= 1; ctx > 0, fast > slow > 0 for the last three (ignored by the others). rot_dim even,
  * 2 .. 128; base > 1. Errors: RKV_ERR_INVALID_ARG. */
 #define RKV_ROPE_PLAIN 0
 #define RKV_ROPE_LINEAR 1
 #define RKV_ROPE_BASE 2
 #define RKV_ROPE_BY_PARTS 3
 #define RKV_ROPE_SMOOTH 4
+#define RKV_ROPE_BY_WHOLE_PARTS 5
 rkv_status rkv_rope_frequencies(int kind, int rot_dim, double base, double factor, int ctx,
                                 double fast, double slow, float* inv_freq, float* mscale);
 

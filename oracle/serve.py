@@ -84,14 +84,17 @@ def frequencies(kind, rot, base, factor=1.0, ctx=0, fast=32.0, slow=1.0):
         return np.array([b ** (-2.0 * i / rot) for i in range(rot // 2)]), 1.0
     out = []
     for i, x in enumerate(f):
-        if kind == "by_parts":
+        if kind in ("by_parts", "by_whole_parts"):
             # pair numbers at which a pair turns `fast` and `slow` times within ctx
             first, last = (rot / 2 * math.log(ctx / (2 * math.pi * t)) / math.log(base) for t in (fast, slow))
+            if kind == "by_whole_parts":
+                first, last = (min(max(e, 0), rot - 1) for e in (math.floor(first), math.ceil(last)))
+                last += 0.001 * (first == last)
             share = 1 - min(max((i - first) / (last - first), 0.0), 1.0)
         else:
             share = min(max((ctx * x / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0)
         out.append(x * share + x / factor * (1 - share))
-    return np.array(out), 0.1 * math.log(factor) + 1 if kind == "by_parts" else 1.0
+    return np.array(out), 1.0 if kind == "smooth" else 0.1 * math.log(factor) + 1
 
 
 def turn(x, positions, inv_freq, interleaved, mscale=1.0):

@@ -155,8 +155,9 @@ rkv_status rkv_release_blocks(const int32_t* len, const int32_t* held, const int
 // ------------------------------------------------------------------------------- rotary positions
 rkv_status rkv_rope_frequencies(int kind, int rot_dim, double base, double factor, int ctx,
                                 double fast, double slow, float* inv_freq, float* mscale) {
-  const bool parts = kind == RKV_ROPE_BY_PARTS || kind == RKV_ROPE_SMOOTH;
-  if (kind < RKV_ROPE_PLAIN || kind > RKV_ROPE_SMOOTH || rot_dim < 2 || rot_dim > kHeadDim || rot_dim % 2 ||
+  const bool by_pairs = kind == RKV_ROPE_BY_PARTS || kind == RKV_ROPE_BY_WHOLE_PARTS;
+  const bool parts = by_pairs || kind == RKV_ROPE_SMOOTH;
+  if (kind < RKV_ROPE_PLAIN || kind > RKV_ROPE_BY_WHOLE_PARTS || rot_dim < 2 || rot_dim > kHeadDim || rot_dim % 2 ||
       !(base > 1.0) || !std::isfinite(base) || !inv_freq || !mscale)
     return RKV_ERR_INVALID_ARG;
   if (kind != RKV_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return RKV_ERR_INVALID_ARG;
@@ -167,18 +168,29 @@ rkv_status rkv_rope_frequencies(int kind, int rot_dim, double base, double facto
   if (kind == RKV_ROPE_BASE) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
   // the (real) number of the pair that turns t times within ctx
   auto pair_of = [&](double t) { return rot_dim * std::log(ctx / (t * two_pi)) / (2.0 * std::log(base)); };
+  double first = 0.0, last = 1.0;  // the ramp's ends
+  if (by_pairs) {
+    first = pair_of(fast);
+    last = pair_of(slow);
+  }
+  if (kind == RKV_ROPE_BY_WHOLE_PARTS) {
+    auto within = [&](double x) { return x < 0.0 ? 0.0 : x > rot_dim - 1.0 ? rot_dim - 1.0 : x; };
+    first = within(std::floor(first));
+    last = within(std::ceil(last));
+    if (last == first) last += 0.001;
+  }
   for (int i = 0; i < rot_dim / 2; ++i) {
     const double f = std::pow(base, -2.0 * i / rot_dim);
     double keep = 1.0;  // share of the unscaled frequency
     if (kind == RKV_ROPE_LINEAR) keep = 0.0;
-    if (kind == RKV_ROPE_BY_PARTS) keep = (pair_of(slow) - i) / (pair_of(slow) - pair_of(fast));
+    if (by_pairs) keep = (last - i) / (last - first);
     if (kind == RKV_ROPE_SMOOTH) keep = (ctx * f / two_pi - slow) / (fast - slow);
     keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
     inv_freq[i] = (float)(kind == RKV_ROPE_PLAIN || kind == RKV_ROPE_BASE
                               ? f
                               : f * keep + f / factor * (1.0 - keep));
   }
-  *mscale = kind == RKV_ROPE_BY_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  *mscale = by_pairs ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
   return RKV_OK;
 }
 

@@ -912,7 +912,7 @@ def rkv_release_blocks(length, held, block_table, free_blocks, free_count, block
                  stream)
 
 
-ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3, "smooth": 4}
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3, "smooth": 4, "by_whole_parts": 5}
 
 
 def rkv_rope_frequencies(rot_dim: int = HEAD_DIM, base: float = 10000.0, kind: str = "plain",
