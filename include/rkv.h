@@ -60,7 +60,8 @@ typedef enum {
 #define RKV_DEV_LEN_OVER_CAP   0x1u  /* a length exceeds cap / page_cap (work for it skipped) */
 #define RKV_DEV_BAD_WINDOW     0x2u  /* a sequence shorter than the window (unit skipped)     */
 #define RKV_DEV_WAIT_TIMEOUT   0x4u  /* a bounded mbarrier wait ran out (unit abandoned)      */
-#define RKV_DEV_SELECT_FAILED  0x8u  /* a top-k selection produced the wrong count            */
+#define RKV_DEV_SELECT_FAILED  0x8u  /* a top-k selection produced the wrong count (or: a CTA's
+                                        shared memory began off its alignment; it did nothing) */
 #define RKV_DEV_BAD_INDEX      0x10u /* a kept index outside the valid rows (row 0 read)      */
 #define RKV_DEV_NO_BLOCKS      0x20u /* fewer free blocks than a unit needs (unit not served) */
 
@@ -657,6 +658,8 @@ rkv_status rkv_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   out      [tokens][n_kv*gqa][128] bf16, contiguous; may not overlap q. Rows of tokens that belong
  *            to no unit are left as they were.
  *   gqa      1 .. 64
+ *   scores   scale log2(e) q . k below 2^28 in magnitude for every row that a token sees (beyond that, fp32
+ *            numbers are 16 and more apart, and numerators relative to a rounded score may overflow)
  * len out of range: RKV_DEV_LEN_OVER_CAP; q_start out of order or range, or T > len[u]:
  * RKV_DEV_BAD_WINDOW; the unit is skipped, its rows left as they were. A table entry outside the pool
  * among the unit's blocks: RKV_DEV_BAD_INDEX, block 0 is read. RKV_ERR_TOO_LARGE where tokens * n_kv *
