@@ -28,6 +28,7 @@
 // 116 us, 80 of them the floor).
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/rkv_testing.h"
@@ -1269,12 +1270,14 @@ static cudaError_t launch_at(const CUtensorMap& qm, const CUtensorMap& km, const
   const cudaError_t e = ensure_dyn_smem((const void*)at_kernel<PAGED, TREE>, AtSmem::total);
   if (e != cudaSuccess) return e;
   // the warpgroups' shares count on the registers that the block is launched with
-  static const bool regs_ok = [] {
+  static std::atomic<bool> regs_ok{false};  // (kept once it has been seen: an error of one call is not the next one's)
+  if (!regs_ok.load(std::memory_order_relaxed)) {
     cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, (const void*)at_kernel<PAGED, TREE>) == cudaSuccess &&
-           f.numRegs == kAtLaunchRegs;
-  }();
-  if (!regs_ok) return cudaErrorInvalidConfiguration;
+    const cudaError_t seen = cudaFuncGetAttributes(&f, (const void*)at_kernel<PAGED, TREE>);
+    if (seen != cudaSuccess) return seen;
+    if (f.numRegs != kAtLaunchRegs) return cudaErrorInvalidConfiguration;
+    regs_ok.store(true, std::memory_order_relaxed);
+  }
   return launch_pdl_kernel(at_kernel<PAGED, TREE>, dim3(p.ctas), dim3(kAtThreads), AtSmem::total, s, qm,
                            km, vm, p);
 }
