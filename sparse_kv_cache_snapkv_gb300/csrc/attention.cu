@@ -1066,7 +1066,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int end = TREE ? x.L : __reduce_max_sync(0xffffffffu, lim) + 1;
       const AtSees sees{clear, end, lim, base, valid ? x.T : 0, bits};
       for (int j = 0; j < x.cnt(h); ++j) {
-        if (!mbar_wait_warp(&bar.sfull[h], ns++ & 1u, limit)) {
+        // (an item that this tile has no part in is over for it at once, and it waits here while the other tile is at it)
+        if (!mbar_wait_warp(&bar.sfull[h], ns++ & 1u, j ? limit : item_limit)) {
           aborted = true;
           break;
         }
