@@ -18,14 +18,15 @@
 // as warps 0 to 3), four write outputs, four each are a tile's softmax. Between them only mbarriers, all waits
 // bounded.
 //
-// Bound: a prompt by the tensor cores (8192 tokens, 32 heads of 8 KV heads: 318 us, 1.73 PFLOP/s of the
-// causal half, 90 % of a cuBLAS product's rate; the GPU is at its power limit); a tree by reading the cache (32
-// trees over up to 20480 rows: 268 us, 6.4 TB/s) or, with 256 rows an item, by both. A step of a pair takes some
-// 2600 clocks, 2048 of them products; what is left is the chain from S through the softmax to P and the wakes
-// between. Items of a prompt go to CTAs as they are, largest first in waves of alternating direction; where
+// Bound (times here and below are the GPU's, of calls replayed in a graph; a call from Python that is waited for
+// by the next takes up to 40 us more): a prompt by the tensor cores (8192 tokens, 32 heads of 8 KV heads: 311 us,
+// 1.77 PFLOP/s of the causal half, 92 % of a cuBLAS product's rate; the GPU is at its power limit); a tree by reading
+// the cache (32 trees over up to 20480 rows: 264 us, 6.5 TB/s) or, with 256 rows an item, by both. A step of a pair
+// takes some 2600 clocks, 2048 of them products; what is left is the chain from S through the softmax to P and the
+// wakes between. Items of a prompt go to CTAs as they are, largest first in waves of alternating direction; where
 // the longest item would outlast an equal share of all steps, every CTA takes an equal range of the steps
 // instead, and a second kernel joins the parts of cut items in their order (131071 rows, 64 drafted tokens:
-// 116 us, 80 of them the floor).
+// 115 us, 80 of them the floor).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <atomic>
@@ -135,7 +136,10 @@ __device__ __forceinline__ bool at_unit(const AtParams& p, int u, int* row0, int
   return true;
 }
 
-// Whole items, unless the longest would outlast an equal share of all steps by what parts and their join cost.
+// Whole items, unless the longest would outlast an equal share of all steps by what parts and their join cost. The
+// items' waves are not looked at: a few more items of one length than CTAs stay whole too and take two waves, the
+// second nearly empty (20 requests of one token over 16384 rows, 160 items: 343 us, as long as 32 requests'; the
+// floor is 201), where the spread of a ragged batch evens its waves out.
 __device__ __forceinline__ AtPlan at_decide(long long total, int longest, int count, int ctas) {
   const long long each = total < (1ll << 30) ? ((int)total + ctas - 1) / ctas : (total + ctas - 1) / ctas;
   const int split = total < (1ll << 30) && longest - each >= kSplitGain && longest * 4ll > each * 5ll;
